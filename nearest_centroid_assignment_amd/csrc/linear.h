@@ -81,10 +81,10 @@ struct Tile {
     static_assert(kIssues >= 1 && kIssues * 64 * DW * NW == kBytes, "tile and waves");
 
     uint32_t off[kIssues];
-    const char *base;
-    uint32_t ld;      // bytes
-    uint32_t extent;  // KC: valid rows; MC: valid bytes of a row
-    int64_t depth;
+    int kc[2];        // KC: byte of k that this lane moves, by the parity of the issue
+    uint64_t at;      // this stage's first row or column (the rest is wave-uniform too)
+    int ld, left;     // bytes of a row; KC: bytes, MC: rows of k from this stage on
+    int extent;       // KC: bytes before the last valid row (< 0: no row); MC: valid bytes of a row
 
     static __device__ __forceinline__ int swizzle(int k) {  // MC, in 16-byte chunks
         if (kSize == 2) return (((k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1)) << 1;
@@ -99,63 +99,64 @@ struct Tile {
     }
 
     // p: the tile's first row (KC) or column (MC) at k = 0; valid: rows or columns.
-    __device__ __forceinline__ void init(const char *p, int64_t ld_elems, int64_t valid,
-                                         int64_t depth_, int wave, int lane) {
-        base = p;
-        ld = (uint32_t)(ld_elems * kSize);
-        depth = depth_;
-        const uint32_t n = (uint32_t)(valid < 0 ? 0 : valid > R ? R : valid);
-        extent = __builtin_amdgcn_readfirstlane(MC ? n * kSize : n);
+    __device__ __forceinline__ void init(const char *p, int64_t ld_elems, int64_t valid, int depth,
+                                         int wave, int lane) {
+        const uint64_t a = (uint64_t)p;
+        at = ((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(a >> 32)) << 32) |
+             (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
+        ld = __builtin_amdgcn_readfirstlane((int)(ld_elems * kSize));
+        const int n = (int)(valid < 0 ? 0 : valid > R ? R : valid);
+        // 16-bit rows are padded with zeros to whole 16 bytes; the range check
+        // drops a 4-byte word that the records end inside of.
+        left = __builtin_amdgcn_readfirstlane(
+            MC ? depth : kSize == 2 ? (depth + 7) / 8 * 16 : depth * kSize);
+        extent = __builtin_amdgcn_readfirstlane(MC ? n * kSize : n ? (n - 1) * ld : -(1 << 30));
 #pragma unroll
         for (int i = 0; i < kIssues; ++i) {
             const int q = lds_byte(wave, lane, i);
             if (MC) {
                 constexpr int kRowBytes = R * kSize;
                 const int k = q / kRowBytes, c = q % kRowBytes;
-                const uint32_t src = (((c >> 4) ^ swizzle(k)) << 4) | (c & 15);
-                off[i] = src < extent ? k * ld + src : kNowhere;
+                const int src = (((c >> 4) ^ swizzle(k)) << 4) | (c & 15);
+                off[i] = src < extent ? (uint32_t)(k * ld + src) : kNowhere;
             } else {
                 off[i] = (q >> 7) * ld + kc_byte(q);
             }
         }
+        kc[0] = kc_byte(lds_byte(wave, lane, 0));
+        kc[1] = kc_byte(lds_byte(wave, lane, kIssues > 1 ? 1 : 0));
     }
 
-    __device__ __forceinline__ void issue(char *lds, int stage, int wave, int lane) const {
-        const char *at;
-        int64_t records;
-        uint32_t left = kRow;  // KC: bytes of k from this stage on
+    // Moves this stage into LDS and steps to the next. Past the last stage
+    // every lane is out of range, and zeros arrive.
+    __device__ __forceinline__ void issue(lds_char *lds, int wave, int lane) {
+        int records = 0;
         if (MC) {
-            const int64_t k = depth - (int64_t)stage * kDepth;
-            const int64_t rows = k < kDepth ? k : kDepth;
-            at = base + (int64_t)stage * kDepth * ld;
-            records = (rows - 1) * ld + extent;
-            if (extent == 0) records = 0;
+            const int rows = left < kDepth ? left : kDepth;
+            if (left > 0 && extent > 0) records = (rows - 1) * ld + extent;
         } else {
-            // 16-bit rows are padded with zeros to whole 16 bytes; the range check
-            // drops a 4-byte word that the records end inside of.
-            const int64_t all = kSize == 2 ? (depth + 7) / 8 * 16 : depth * kSize;
-            const int64_t bytes = all - (int64_t)stage * kRow;
-            at = base + (int64_t)stage * kRow;
-            records = extent ? (int64_t)(extent - 1) * ld + bytes : 0;
-            left = bytes < kRow ? (uint32_t)bytes : kRow;
+            if (left > 0) records = extent + left;
+            if (records < 0) records = 0;
         }
-        const uint64_t a = (uint64_t)at;
-        const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-        const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-        const uint32_t rec = __builtin_amdgcn_readfirstlane((uint32_t)records);
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(((uint64_t)hi << 32) | lo), 0, (int)rec, 0x00020000);
+        const __amdgpu_buffer_rsrc_t rsrc =
+            __builtin_amdgcn_make_buffer_rsrc((void *)at, 0, records, 0x00020000);
 #pragma unroll
         for (int i = 0; i < kIssues; ++i) {
             uint32_t o = off[i];
-            if (!MC && left < kRow && (uint32_t)kc_byte(lds_byte(wave, lane, i)) >= left)
-                o = kNowhere;
-            lds_void *to = (lds_void *)(lds + (wave * kIssues + i) * 64 * DW);
+            if (!MC) {
+                // With 16 bytes a lane an issue covers 8 rows, so its bytes of k
+                // depend on the parity of the issue alone; with 4, on i % 4.
+                const int k = DW == 16 ? kc[i & 1] : kc_byte(lds_byte(wave, lane, i));
+                o = k < left ? o : kNowhere;
+            }
+            lds_char *to = lds + (wave * kIssues + i) * 64 * DW;
             if constexpr (DW == 16)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16, (int)o, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)to, 16, (int)o, 0, 0, 0);
             else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 4, (int)o, 0, 0, 0);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)to, 4, (int)o, 0, 0, 0);
         }
+        at += MC ? (uint64_t)ld * kDepth : (uint64_t)kRow;
+        left -= MC ? kDepth : kRow;
     }
 };
 
@@ -163,28 +164,34 @@ struct Tile {
 template <typename T, bool MC, int R, int N>
 struct Reader {
     typedef typename Frag<T>::type frag;
-    int at[N];
+    typedef __attribute__((address_space(3))) const frag lds_frag;
+    typedef __attribute__((address_space(3))) const float lds_float;
+    int at[MC ? N : 2];  // MC: by block; KC: by half of the stage
 
     __device__ __forceinline__ void init(int first, int lane) {
         const int i = lane & 15, g = lane >> 4;
+        if (!MC) {
 #pragma unroll
-        for (int t = 0; t < N; ++t) {
-            if (!MC) {
-                at[t] = (first + 16 * t + i) * kRow + ((g ^ (i >> 1)) << 4);
-            } else if (sizeof(T) == 2) {
-                const int k = 8 * g + (i >> 2);
-                const int key = ((k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1);
-                at[t] = k * (R * 2) + (((first / 16 + t) ^ key) << 5) + (i & 3) * 8;
-            } else {
-                at[t] = 4 * g * (R * 4) + (((first / 16 + t) ^ g) << 6) + i * 4;
+            for (int s = 0; s < 2; ++s) at[s] = (first + i) * kRow + (((4 * s + g) ^ (i >> 1)) << 4);
+        } else {
+#pragma unroll
+            for (int t = 0; t < N; ++t) {
+                if (sizeof(T) == 2) {
+                    const int k = 8 * g + (i >> 2);
+                    const int key = ((k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1);
+                    at[t] = k * (R * 2) + (((first / 16 + t) ^ key) << 5) + (i & 3) * 8;
+                } else {
+                    at[t] = 4 * g * (R * 4) + (((first / 16 + t) ^ g) << 6) + i * 4;
+                }
             }
         }
     }
     // Half `s` of the stage (64 of its 128 bytes of k), block t.
-    __device__ __forceinline__ frag read(const char *lds, int t, int s) const {
-        if (!MC) return *reinterpret_cast<const frag *>(lds + (at[t] ^ (s << 6)));
-        if constexpr (sizeof(T) == 2) {
-            const char *p = lds + at[t] + s * 32 * (R * 2);
+    __device__ __forceinline__ frag read(const lds_char *lds, int t, int s) const {
+        if constexpr (!MC) {
+            return *(lds_frag *)(lds + at[s] + t * 16 * kRow);
+        } else if constexpr (sizeof(T) == 2) {
+            const lds_char *p = lds + at[t] + s * 32 * (R * 2);
             union {
                 s16x4 h[2];
                 frag f;
@@ -195,8 +202,7 @@ struct Reader {
         } else {
             frag f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                f[j] = *reinterpret_cast<const float *>(lds + at[t] + (s * 16 + j) * (R * 4));
+            for (int j = 0; j < 4; ++j) f[j] = *(lds_float *)(lds + at[t] + (s * 16 + j) * (R * 4));
             return f;
         }
     }
@@ -212,47 +218,93 @@ struct Shape {
     typedef Tile<T, QMC, BM, NW, DW> TileQ;
     typedef Reader<T, PMC, BN, TN> ReadP;
     typedef Reader<T, QMC, BM, TM> ReadQ;
-    static constexpr bool p_mc = PMC;
+    static constexpr bool p_mc = PMC, q_mc = QMC;
 };
 
-// acc[tm][tn] += the tile's product over the whole depth. Two stages in LDS:
-// the next one is in flight while this one is multiplied.
 template <class S>
-__device__ __forceinline__ void product(char *smem, typename S::TileP &tp, typename S::TileQ &tq,
-                                        int64_t depth, int wave, int lane,
+struct Frags {
+    typename Frag<typename S::type>::type p[S::TN], q[S::TM];
+};
+
+template <class S>
+__device__ __forceinline__ void read_half(const typename S::ReadP &rp, const typename S::ReadQ &rq,
+                                          const lds_char *stage, int s, Frags<S> &f) {
+#pragma unroll
+    for (int t = 0; t < S::TN; ++t) f.p[t] = rp.read(stage, t, s);
+#pragma unroll
+    for (int t = 0; t < S::TM; ++t) f.q[t] = rq.read(stage + S::BN * kRow, t, s);
+}
+template <class S>
+__device__ __forceinline__ void multiply(const Frags<S> &f, f32x4 (&acc)[S::TM][S::TN]) {
+#pragma unroll
+    for (int m = 0; m < S::TM; ++m)
+#pragma unroll
+        for (int n = 0; n < S::TN; ++n)
+            acc[m][n] = Frag<typename S::type>::mma(f.p[n], f.q[m], acc[m][n]);
+}
+
+// The order of one half-stage: its LDS reads (for the half after it) and
+// `moves` global-to-LDS loads spread evenly over its matrix instructions.
+template <class S>
+__device__ __forceinline__ void spread(bool moves) {
+    constexpr int kMma = S::TM * S::TN * (sizeof(typename S::type) == 4 ? 4 : 1);
+    constexpr int kReadsP = S::TN * (S::p_mc ? (sizeof(typename S::type) == 4 ? 4 : 2) : 1);
+    constexpr int kReadsQ = S::TM * (S::q_mc ? (sizeof(typename S::type) == 4 ? 4 : 2) : 1);
+    constexpr int kReads = kReadsP + kReadsQ;
+    constexpr int kMoves = S::TileP::kIssues + S::TileQ::kIssues;
+    constexpr int kSteps = kMma / 2;  // two matrix instructions a step
+    int reads = 0, moved = 0;
+#pragma unroll
+    for (int j = 0; j < kSteps; ++j) {
+        // The reads in the first three quarters, so that they have returned by the end.
+        const int r = (j + 1) * kReads * 4 / (kSteps * 3) < kReads ? (j + 1) * kReads * 4 / (kSteps * 3) : kReads;
+        for (; reads < r; ++reads) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (moves) {
+            const int m = (j + 1) * kMoves / kSteps;
+            for (; moved < m; ++moved) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+    }
+}
+
+// acc[tm][tn] += the tile's product over the whole depth. Two stages in LDS and
+// two half-stages of fragments in registers: while one half is multiplied, the
+// next is read, and in the second half of a stage, whose buffer every wave has
+// read by then, the stage after the next moves in.
+template <class S>
+__device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
+                                        typename S::TileQ &tq, int depth, int wave, int lane,
                                         f32x4 (&acc)[S::TM][S::TN]) {
-    typedef typename S::type T;
-    typedef typename Frag<T>::type frag;
     typename S::ReadP rp;
     typename S::ReadQ rq;
     rp.init((wave % S::WN) * (S::BN / S::WN), lane);
     rq.init((wave / S::WN) * (S::BM / S::WM), lane);
-    const int stages = (int)((depth + S::TileP::kDepth - 1) / S::TileP::kDepth);
+    const int stages = __builtin_amdgcn_readfirstlane((depth + S::TileP::kDepth - 1) / S::TileP::kDepth);
     if (stages == 0) return;
-    tp.issue(smem, 0, wave, lane);
-    tq.issue(smem + S::BN * kRow, 0, wave, lane);
+    tp.issue(smem, wave, lane);
+    tq.issue(smem + S::BN * kRow, wave, lane);
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    tp.issue(smem + S::kStage, wave, lane);
+    tq.issue(smem + S::kStage + S::BN * kRow, wave, lane);
+    Frags<S> f[2];
+    read_half<S>(rp, rq, smem, 0, f[0]);
     for (int it = 0; it < stages; ++it) {
-        char *cur = smem + (it & 1) * S::kStage;
-        char *nxt = smem + ((it & 1) ^ 1) * S::kStage;
+        lds_char *cur = smem + (it & 1) * S::kStage;
+        lds_char *nxt = smem + ((it & 1) ^ 1) * S::kStage;
+        read_half<S>(rp, rq, cur, 1, f[1]);
+        multiply<S>(f[0], acc);
+        spread<S>(false);
         __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();  // this stage has landed; every wave is done with the one before
-        if (it + 1 < stages) {
-            tp.issue(nxt, it + 1, wave, lane);
-            tq.issue(nxt + S::BN * kRow, it + 1, wave, lane);
-        }
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            frag p[S::TN], q[S::TM];
-#pragma unroll
-            for (int t = 0; t < S::TN; ++t) p[t] = rp.read(cur, t, s);
-#pragma unroll
-            for (int t = 0; t < S::TM; ++t) q[t] = rq.read(cur + S::BN * kRow, t, s);
-#pragma unroll
-            for (int m = 0; m < S::TM; ++m)
-#pragma unroll
-                for (int n = 0; n < S::TN; ++n) acc[m][n] = Frag<T>::mma(p[n], q[m], acc[m][n]);
-        }
+        __syncthreads();  // the next stage has landed, and this one is in registers
+        read_half<S>(rp, rq, nxt, 0, f[0]);
+        tp.issue(cur, wave, lane);
+        tq.issue(cur + S::BN * kRow, wave, lane);
+        multiply<S>(f[1], acc);
+        spread<S>(true);
     }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();  // the stages' memory is free
 }
 
 // Block b of a grid of `total` tiles: XCD b % 8 takes a contiguous range of
@@ -307,42 +359,68 @@ __device__ __forceinline__ Group find_group(const int *offsets, int experts, int
     return r;
 }
 
-// Four values of one row; `full`: all inside it and on a vector boundary.
+// Eight values of one row, `valid` of them inside it, at any alignment.
 template <typename T>
-__device__ __forceinline__ f32x4 load4(const T *p, int valid, bool full) {
-    f32x4 r = {0, 0, 0, 0};
-    if (full) {
-        typedef T v4 __attribute__((ext_vector_type(4)));
-        const v4 x = *reinterpret_cast<const v4 *>(p);
+__device__ __forceinline__ void load8(const T *p, int valid, float (&r)[8]) {
+    if (valid >= 8) {
+        T x[8];
+        load_vec(p, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = (float)x[i];
+        for (int i = 0; i < 8; ++i) r[i] = (float)x[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < valid) r[i] = (float)p[i];
+        for (int i = 0; i < 8; ++i) r[i] = i < valid ? (float)p[i] : 0.0f;
     }
-    return r;
 }
 template <typename T>
-__device__ __forceinline__ void store4(T *p, f32x4 v, int valid, bool full) {
-    if (full) {
-        typedef T v4 __attribute__((ext_vector_type(4)));
-        v4 x;
+__device__ __forceinline__ void store8(T *p, const float (&v)[8], int valid) {
+    T x[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = (T)v[i];
-        *reinterpret_cast<v4 *>(p) = x;
+    for (int i = 0; i < 8; ++i) x[i] = (T)v[i];
+    if (valid >= 8) {
+        store_vec(p, x);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < valid) p[i] = (T)v[i];
+        for (int i = 0; i < 8; ++i)
+            if (i < valid) p[i] = x[i];
     }
 }
 
-template <typename T>
+// Hands the wave's tile to `use(row, col, values)`, eight consecutive columns at
+// a time: 16 rows go through LDS (each wave's own part of the stages' memory),
+// so that a wave's accesses to memory are whole rows of the tile, 16 bytes a
+// lane, where the matrix instruction leaves a lane four columns of one row.
+template <class S, class F>
+__device__ __forceinline__ void by_rows(lds_char *smem, int wave, int lane,
+                                        const f32x4 (&acc)[S::TM][S::TN], F use) {
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    constexpr int kCols = S::TN * 16, kLd = (kCols + 4) * 4;
+    constexpr int kLanes = kCols / 8;      // lanes to a row
+    constexpr int kRows = 64 / kLanes;     // rows at a time
+    static_assert(16 * kLd * S::NW <= 2 * S::kStage, "the stages' memory");
+    lds_char *own = smem + wave * 16 * kLd;
+    const int row = lane / kLanes, col = lane % kLanes * 8;
+#pragma unroll
+    for (int tm = 0; tm < S::TM; ++tm) {
+#pragma unroll
+        for (int tn = 0; tn < S::TN; ++tn)
+            *(lds_f32x4 *)(own + (lane & 15) * kLd + tn * 64 + (lane >> 4) * 16) = acc[tm][tn];
+        // One wave's LDS accesses are done in order; only the compiler must keep it.
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int r = 0; r < 16; r += kRows) {
+            const lds_char *p = own + (r + row) * kLd + col * 4;
+            const f32x4 a = *(lds_f32x4 *)p, b = *(lds_f32x4 *)(p + 16);
+            float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            if (kRows <= 16 || row < 16) use(tm * 16 + r + row, col, v);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+}
+
 struct RowsArgs {
     RowsProblem pr;
-    bool vec;  // rows of out, pre, residual, in_pre and bias are whole 4-value vectors
-    int gm;    // row tiles walked per column tile, so that a group's operands stay in L2
+    int gm;  // row tiles walked per column tile, so that a group's operands stay in L2
 };
 
 // Tile (mt, nt) of the walk's place id: groups of gm row tiles, row first.
@@ -352,14 +430,15 @@ __device__ __forceinline__ void walk(int64_t id, int tiles_m, int tiles_n, int g
     const int first = (int)(panel * gm);
     const int height = tiles_m - first < gm ? tiles_m - first : gm;
     const int64_t in = id - panel * per;
-    mt = first + (int)(in % height);
-    nt = (int)(in / height);
+    mt = __builtin_amdgcn_readfirstlane(first + (int)(in % height));
+    nt = __builtin_amdgcn_readfirstlane((int)(in / height));
 }
 
 template <class S>
-__global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs<typename S::type> a) {
+__global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs a) {
     typedef typename S::type T;
-    __shared__ __align__(1024) char smem[2 * S::kStage];
+    __shared__ __align__(1024) char memory[2 * S::kStage];
+    lds_char *smem = (lds_char *)memory;
     const RowsProblem &pr = a.pr;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -392,54 +471,48 @@ __global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs<typename S
         typename S::TileQ tq;
         tp.init(p, pr.ldp, S::p_mc ? pr.p_cols - n0 : (int64_t)cols - n0, pr.depth, wave, lane);
         tq.init(q, pr.ldq, gr.hi - m0, pr.depth, wave, lane);
-        product<S>(smem, tp, tq, pr.depth, wave, lane, acc);
+        product<S>(smem, tp, tq, (int)pr.depth, wave, lane, acc);
     }
-    const int wm = m0 + (wave / S::WN) * (S::BM / S::WM) + (lane & 15);
-    const int wn = n0 + (wave % S::WN) * (S::BN / S::WN) + (lane >> 4) * 4;
+    const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
+    const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     T *out = (T *)pr.out, *pre = (T *)pr.pre;
     const T *bias = (const T *)pr.bias, *res = (const T *)pr.residual, *in = (const T *)pr.in_pre;
-#pragma unroll
-    for (int tn = 0; tn < S::TN; ++tn) {
-        const int n = wn + tn * 16;
-        const int valid = cols - n;
-        if (valid <= 0) continue;
-        const bool full = a.vec && valid >= 4;
-        f32x4 b = {0, 0, 0, 0};
-        if (bias && !tail) b = load4(bias + (int64_t)gr.expert * cols + n, valid, full);
-#pragma unroll
-        for (int tm = 0; tm < S::TM; ++tm) {
-            const int64_t m = wm + tm * 16;
-            if (m >= gr.hi) continue;
-            f32x4 z = acc[tm][tn] + b;
-            if (tail) z = f32x4{0, 0, 0, 0};
-            if (pre) store4(pre + m * pr.ldpre + n, z, valid, full);
-            if (pr.act != kActNone) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) z[i] = act_value(z[i], pr.act);
-            }
-            if (!tail) {
-                if (res) z += load4(res + m * pr.ldr + n, valid, full);
-                if (in) {
-                    const f32x4 y = load4(in + m * pr.ldin + n, valid, full);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z[i] *= act_slope(y[i], pr.in_act);
-                }
-            }
-            store4(out + m * pr.ldo + n, z, valid, full);
-        }
+    float b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (bias && !tail) {
+        const int n = wn + lane % (S::TN * 2) * 8;
+        if (n < cols) load8(bias + (int64_t)gr.expert * cols + n, cols - n, b);
     }
+    by_rows<S>(smem, wave, lane, acc, [&](int row, int col, float (&z)[8]) {
+        const int64_t m = wm + row;
+        const int n = wn + col, valid = cols - n;
+        if (m >= gr.hi || valid <= 0) return;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = tail ? 0.0f : z[i] + b[i];
+        if (pre) store8(pre + m * pr.ldpre + n, z, valid);
+        if (pr.act != kActNone) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], pr.act);
+        }
+        float y[8];
+        if (res && !tail) {
+            load8(res + m * pr.ldr + n, valid, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] += y[i];
+        }
+        if (in && !tail) {
+            load8(in + m * pr.ldin + n, valid, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[i] *= act_slope(y[i], pr.in_act);
+        }
+        store8(out + m * pr.ldo + n, z, valid);
+    });
 }
 
-struct GradArgs {
-    GradProblem pr;
-    bool vec;
-};
-
 template <class S>
-__global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradArgs a) {
+__global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
     typedef typename S::type T;
-    __shared__ __align__(1024) char smem[2 * S::kStage];
-    const GradProblem &pr = a.pr;
+    __shared__ __align__(1024) char memory[2 * S::kStage];
+    lds_char *smem = (lds_char *)memory;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int mc = (int)pr.m_cols, nc = (int)pr.n_cols, rows = (int)pr.rows;
@@ -447,14 +520,14 @@ __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradArgs a) {
     const int64_t each = (int64_t)tiles_m * tiles_n;
     const int64_t id = xcd_tile(each * pr.experts);
     if (id < 0) return;
-    const int e = (int)(id / each);
+    const int e = __builtin_amdgcn_readfirstlane((int)(id / each));
     int mt, nt;
     walk(id - e * each, tiles_m, tiles_n, 4, mt, nt);
     const int m0 = mt * S::BM, n0 = nt * S::BN;
     int lo = 0, hi = rows;
     if (pr.offsets) {
-        lo = clampi(pr.offsets[e], 0, rows);
-        hi = clampi(pr.offsets[e + 1], lo, rows);
+        lo = __builtin_amdgcn_readfirstlane(clampi(pr.offsets[e], 0, rows));
+        hi = __builtin_amdgcn_readfirstlane(clampi(pr.offsets[e + 1], lo, rows));
     }
     f32x4 acc[S::TM][S::TN];
 #pragma unroll
@@ -468,25 +541,15 @@ __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradArgs a) {
     tq.init((const char *)pr.dz + ((int64_t)lo * pr.lddz + m0) * sizeof(T), pr.lddz,
             pr.dz_cols - m0, hi - lo, wave, lane);
     product<S>(smem, tp, tq, hi - lo, wave, lane, acc);
-    const int wm = m0 + (wave / S::WN) * (S::BM / S::WM) + (lane & 15);
-    const int wn = n0 + (wave % S::WN) * (S::BN / S::WN) + (lane >> 4) * 4;
+    const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
+    const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     T *out = (T *)pr.out + (int64_t)e * mc * nc;
-#pragma unroll
-    for (int tn = 0; tn < S::TN; ++tn) {
-        const int n = wn + tn * 16;
-        const int valid = nc - n;
-        if (valid <= 0) continue;
-#pragma unroll
-        for (int tm = 0; tm < S::TM; ++tm) {
-            const int64_t m = wm + tm * 16;
-            if (m < mc) store4(out + m * nc + n, acc[tm][tn], valid, a.vec && valid >= 4);
-        }
-    }
+    by_rows<S>(smem, wave, lane, acc, [&](int row, int col, float (&z)[8]) {
+        const int m = wm + row, n = wn + col;
+        if (m < mc && n < nc) store8(out + (int64_t)m * nc + n, z, nc - n);
+    });
 }
 
-inline bool on_vector(const void *p, int64_t ld, int size) {
-    return p == nullptr || ((uintptr_t)p % (4 * size) == 0 && ld % 4 == 0);
-}
 inline bool on_chunk(const void *p, int64_t ld, int64_t len, int size) {
     return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0 && len * size % 16 == 0;
 }
@@ -498,12 +561,8 @@ inline int64_t most_row_tiles(int64_t rows, int bm, const void *offsets, int exp
 
 template <class S>
 hipError_t run_rows(const RowsProblem &pr, hipStream_t s) {
-    constexpr int size = (int)sizeof(typename S::type);
-    RowsArgs<typename S::type> a;
+    RowsArgs a;
     a.pr = pr;
-    a.vec = on_vector(pr.out, pr.ldo, size) && on_vector(pr.pre, pr.ldpre, size) &&
-            on_vector(pr.residual, pr.ldr, size) && on_vector(pr.in_pre, pr.ldin, size) &&
-            on_vector(pr.bias, pr.cols, size);
     a.gm = 8;
     const int64_t tiles = most_row_tiles(pr.rows, S::BM, pr.offsets, pr.experts) * cdiv(pr.cols, S::BN);
     rows_kernel<S><<<(unsigned)(cdiv(tiles, 8) * 8), S::NW * 64, 0, s>>>(a);
@@ -512,12 +571,8 @@ hipError_t run_rows(const RowsProblem &pr, hipStream_t s) {
 
 template <class S>
 hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
-    constexpr int size = (int)sizeof(typename S::type);
-    GradArgs a;
-    a.pr = pr;
-    a.vec = on_vector(pr.out, pr.n_cols, size);
     const int64_t tiles = cdiv(pr.m_cols, S::BM) * cdiv(pr.n_cols, S::BN) * pr.experts;
-    grad_kernel<S><<<(unsigned)(cdiv(tiles, 8) * 8), S::NW * 64, 0, s>>>(a);
+    grad_kernel<S><<<(unsigned)(cdiv(tiles, 8) * 8), S::NW * 64, 0, s>>>(pr);
     return hipGetLastError();
 }
 
