@@ -18,6 +18,8 @@
  *   - workspace is a caller-owned device buffer of at least the bytes that the
  *     matching *_workspace_bytes function gives, any alignment; its contents
  *     on entry do not matter. Two calls that may run at the same time need two.
+ *     Where those bytes are 256 or fewer (slack for the alignment alone) the
+ *     workspace may be NULL. 0 bytes mean that the shape is not supported.
  *   - stream is a hipStream_t (NULL = the default stream). Every call only
  *     enqueues kernels on it: no allocation, host wait, copy or memset, so it
  *     can be captured into a HIP graph and replayed.

@@ -88,6 +88,8 @@ struct PlanScratch {
     unsigned short *rank;  // pairs
     int64_t tiles;
 };
+// Whether one block sorts the pairs (then the scratch is not used).
+bool plan_is_small(int64_t pairs, int64_t experts);
 hipError_t launch_plan(const int64_t *ids, int64_t pairs, int64_t experts, int *order, int *place,
                        int *offsets, const PlanScratch &ws, hipStream_t s);
 hipError_t launch_dispatch(const void *x, int64_t ldx, int dtype, int64_t tokens, int64_t top,

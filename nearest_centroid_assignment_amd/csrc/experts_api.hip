@@ -30,6 +30,12 @@ char *ws_base(void *workspace) {
     return (char *)(((uintptr_t)workspace + kAlign - 1) / kAlign * kAlign);
 }
 
+// Whether the workspace holds `total` bytes; one that holds slack alone (no
+// section) may be left out.
+bool ws_ok(const void *workspace, size_t bytes, size_t total) {
+    return total <= kAlign || (workspace && bytes >= total);
+}
+
 // An array of rows (ld apart) of len elements.
 struct Span {
     const void *p;
@@ -60,7 +66,8 @@ struct PlanLayout {
     size_t hist, count, rank, total;
 };
 PlanLayout plan_layout(int64_t pairs, int64_t experts) {
-    PlanLayout L;
+    PlanLayout L = {0, 0, 0, kAlign};
+    if (kx::plan_is_small(pairs, experts)) return L;
     const int64_t tiles = cdiv(pairs, km::kSortTileRows);
     size_t off = 0;
     L.hist = off;
@@ -154,11 +161,11 @@ int experts_plan(const int64_t *ids, int64_t tokens, int64_t top, int64_t expert
                  void *stream) {
     if (!tokens_shape_ok(tokens, top) || experts < 1 || experts > kMaxExperts) return KM_ERR_SHAPE;
     const int64_t pairs = tokens * top;
-    if (!offsets || !workspace || (pairs > 0 && (!ids || !order || !place))) return KM_ERR_NULL;
+    if (!offsets || (pairs > 0 && (!ids || !order || !place))) return KM_ERR_NULL;
     if (!aligned(ids, 8) || !aligned(order, 4) || !aligned(place, 4) || !aligned(offsets, 4))
         return KM_ERR_ALIGN;
     const PlanLayout L = plan_layout(pairs, experts);
-    if (workspace_bytes < L.total) return KM_ERR_WORKSPACE;
+    if (!ws_ok(workspace, workspace_bytes, L.total)) return KM_ERR_WORKSPACE;
     const Span outs[] = {{order, 1, 0, pairs, 4},
                          {place, 1, 0, pairs, 4},
                          {offsets, 1, 0, experts + 1, 4},
@@ -279,7 +286,7 @@ int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,
     if (!linear_shape_ok(rows, outs, ins, experts) || (!offsets && experts != 1) ||
         !linear_grid_ok(dtype, rows, outs, ins, experts))
         return KM_ERR_SHAPE;
-    if (!w || !workspace || (rows > 0 && (!x || !out))) return KM_ERR_NULL;
+    if (!w || (rows > 0 && (!x || !out))) return KM_ERR_NULL;
     if (!ld_ok(x, ldx, ins) || !ld_ok(out, ldo, outs) || !ld_ok(residual, ldr, outs) ||
         !ld_ok(pre, ldpre, outs))
         return KM_ERR_SHAPE;
@@ -289,7 +296,7 @@ int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,
         return KM_ERR_ALIGN;
     const bool pads = dtype != EXPERTS_F32 && !(in_place(x, ldx, ins) && in_place(w, ins, ins));
     const LinearLayout L = linear_layout(rows, outs, ins, experts, dtype, 0, pads);
-    if (workspace_bytes < L.total) return KM_ERR_WORKSPACE;
+    if (!ws_ok(workspace, workspace_bytes, L.total)) return KM_ERR_WORKSPACE;
     const Span os[] = {{out, rows, ldo, outs, b},
                        {pre, rows, ldpre, outs, b},
                        {workspace, 1, 0, (int64_t)workspace_bytes, 1}};
@@ -339,7 +346,7 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if (!linear_shape_ok(rows, outs, ins, experts) || (!offsets && experts != 1) ||
         !linear_grid_ok(dtype, rows, outs, ins, experts))
         return KM_ERR_SHAPE;
-    if (!workspace || (!dx && !dw && !dbias)) return KM_ERR_NULL;
+    if (!dx && !dw && !dbias) return KM_ERR_NULL;
     if (rows > 0 && (!dy || (act != EXPERTS_ACT_NONE && !pre) || (dx && !w) || (dw && !x)))
         return KM_ERR_NULL;
     if (!ld_ok(dy, lddy, outs) || (dw && !ld_ok(x, ldx, ins)) ||
@@ -354,7 +361,7 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
     const bool half = dtype != EXPERTS_F32;
     const bool pads = half && ((dw && !in_place(x, ldx, ins)) || (dx && !in_place(w, ins, ins)));
     const LinearLayout L = linear_layout(rows, outs, ins, experts, dtype, 1, pads);
-    if (workspace_bytes < L.total) return KM_ERR_WORKSPACE;
+    if (!ws_ok(workspace, workspace_bytes, L.total)) return KM_ERR_WORKSPACE;
     const Span os[] = {{dx, rows, lddx, ins, b},
                        {dw, 1, 0, experts * outs * ins, b},
                        {dbias, 1, 0, experts * outs, b},

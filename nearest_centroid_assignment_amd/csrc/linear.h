@@ -307,13 +307,14 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
     __syncthreads();  // the stages' memory is free
 }
 
-// Block b of a grid of `total` tiles: XCD b % 8 takes a contiguous range of
-// them, so that tiles which share operands share an L2. -1: no tile.
-__device__ __forceinline__ int64_t xcd_tile(int64_t total) {
-    const int64_t per = (total + 7) / 8;
-    const int64_t b = blockIdx.x;
-    const int64_t id = (b & 7) * per + (b >> 3);
-    return (b >> 3) < per && id < total ? id : -1;
+// Block b of a grid of `total` tiles: XCD b % 8 takes pieces of `piece`
+// consecutive tiles, so that tiles which share operands share an L2; piece 0: one
+// piece, an eighth of the tiles. -1: no tile. (total, piece < 2^31)
+__device__ __forceinline__ int xcd_tile(int total, int piece) {
+    const int b = blockIdx.x, x = b & 7, j = b >> 3;
+    const int per = (total + 7) / 8;
+    const int id = piece ? ((j / piece) * 8 + x) * piece + j % piece : j < per ? x * per + j : total;
+    return id < total ? id : -1;
 }
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) {
@@ -386,35 +387,54 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8], int valid) {
     }
 }
 
-// Hands the wave's tile to `use(row, col, values)`, eight consecutive columns at
-// a time: 16 rows go through LDS (each wave's own part of the stages' memory),
-// so that a wave's accesses to memory are whole rows of the tile, 16 bytes a
-// lane, where the matrix instruction leaves a lane four columns of one row.
-template <class S, class F>
+// Hands the wave's tile to `use(row, col, values, aux)`, eight consecutive
+// columns at a time: 16 rows at a time go through LDS (each wave's own part of the
+// stages' memory), so that a wave's accesses to memory are whole rows of the tile,
+// 16 bytes a lane, where the matrix instruction leaves a lane four columns of one
+// row. `load(row, col)` gives the aux of a place; it is asked for two groups of rows
+// ahead (the fragments' registers are free by then), or its latency would be paid
+// again for every group.
+template <class S, class Aux, class L, class F>
 __device__ __forceinline__ void by_rows(lds_char *smem, int wave, int lane,
-                                        const f32x4 (&acc)[S::TM][S::TN], F use) {
+                                        const f32x4 (&acc)[S::TM][S::TN], L load, F use) {
     typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
     constexpr int kCols = S::TN * 16, kLd = (kCols + 4) * 4;
-    constexpr int kLanes = kCols / 8;      // lanes to a row
-    constexpr int kRows = 64 / kLanes;     // rows at a time
-    static_assert(16 * kLd * S::NW <= 2 * S::kStage, "the stages' memory");
-    lds_char *own = smem + wave * 16 * kLd;
+    constexpr int kLanes = kCols / 8;   // lanes to a row
+    constexpr int kRows = 64 / kLanes;  // rows at a time
+    constexpr int kParts = 16 / kRows;
+    constexpr int kAhead = 2;           // blocks of 16 rows in LDS at a time
+    static_assert(kAhead * 16 * kLd * S::NW <= 2 * S::kStage, "the stages' memory");
+    lds_char *own = smem + wave * kAhead * 16 * kLd;
     const int row = lane / kLanes, col = lane % kLanes * 8;
+    Aux aux[S::TM][kParts];
 #pragma unroll
-    for (int tm = 0; tm < S::TM; ++tm) {
+    for (int tm = 0; tm < 2 * kAhead && tm < S::TM; ++tm)
 #pragma unroll
-        for (int tn = 0; tn < S::TN; ++tn)
-            *(lds_f32x4 *)(own + (lane & 15) * kLd + tn * 64 + (lane >> 4) * 16) = acc[tm][tn];
+        for (int r = 0; r < kParts; ++r) aux[tm][r] = load(tm * 16 + r * kRows + row, col);
+#pragma unroll
+    for (int t0 = 0; t0 < S::TM; t0 += kAhead) {
+#pragma unroll
+        for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+            for (int tn = 0; tn < S::TN; ++tn)
+                *(lds_f32x4 *)(own + (h * 16 + (lane & 15)) * kLd + tn * 64 + (lane >> 4) * 16) =
+                    acc[t0 + h][tn];
         // One wave's LDS accesses are done in order; only the compiler must keep it.
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-        for (int r = 0; r < 16; r += kRows) {
-            const lds_char *p = own + (r + row) * kLd + col * 4;
-            const f32x4 a = *(lds_f32x4 *)p, b = *(lds_f32x4 *)(p + 16);
-            float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-            if (kRows <= 16 || row < 16) use(tm * 16 + r + row, col, v);
-        }
+        for (int h = 0; h < kAhead; ++h)
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) {
+                const lds_char *p = own + (h * 16 + r * kRows + row) * kLd + col * 4;
+                const f32x4 a = *(lds_f32x4 *)p, b = *(lds_f32x4 *)(p + 16);
+                float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                use((t0 + h) * 16 + r * kRows + row, col, v, aux[t0 + h][r]);
+            }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int tm = t0 + 2 * kAhead; tm < t0 + 3 * kAhead && tm < S::TM; ++tm)
+#pragma unroll
+            for (int r = 0; r < kParts; ++r) aux[tm][r] = load(tm * 16 + r * kRows + row, col);
     }
 }
 
@@ -424,14 +444,14 @@ struct RowsArgs {
 };
 
 // Tile (mt, nt) of the walk's place id: groups of gm row tiles, row first.
-__device__ __forceinline__ void walk(int64_t id, int tiles_m, int tiles_n, int gm, int &mt, int &nt) {
-    const int64_t per = (int64_t)gm * tiles_n;
-    const int64_t panel = id / per;
-    const int first = (int)(panel * gm);
+__device__ __forceinline__ void walk(int id, int tiles_m, int tiles_n, int gm, int &mt, int &nt) {
+    const int per = gm * tiles_n;
+    const int panel = id / per;
+    const int first = panel * gm;
     const int height = tiles_m - first < gm ? tiles_m - first : gm;
-    const int64_t in = id - panel * per;
-    mt = __builtin_amdgcn_readfirstlane(first + (int)(in % height));
-    nt = __builtin_amdgcn_readfirstlane((int)(in / height));
+    const int in = id - panel * per;
+    mt = __builtin_amdgcn_readfirstlane(first + in % height);
+    nt = __builtin_amdgcn_readfirstlane(in / height);
 }
 
 template <class S>
@@ -449,7 +469,7 @@ __global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs a) {
         tiles_m = find_group(pr.offsets, pr.experts, rows, S::BM, -1).tile;
     else
         tiles_m = (rows + S::BM - 1) / S::BM;
-    const int64_t id = xcd_tile((int64_t)tiles_m * tiles_n);
+    const int id = xcd_tile(tiles_m * tiles_n, 0);
     if (id < 0) return;
     int mt, nt;
     walk(id, tiles_m, tiles_n, a.gm, mt, nt);
@@ -476,37 +496,57 @@ __global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs a) {
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     T *out = (T *)pr.out, *pre = (T *)pr.pre;
-    const T *bias = (const T *)pr.bias, *res = (const T *)pr.residual, *in = (const T *)pr.in_pre;
+    const T *bias = (const T *)pr.bias;
+    // The residual of the forward product or the input's activation of dx.
+    const T *extra = (const T *)(pr.residual ? pr.residual : pr.in_pre);
+    const int64_t ldx = pr.residual ? pr.ldr : pr.ldin;
+    const bool in = pr.in_pre != nullptr;
     float b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (bias && !tail) {
         const int n = wn + lane % (S::TN * 2) * 8;
         if (n < cols) load8(bias + (int64_t)gr.expert * cols + n, cols - n, b);
     }
-    by_rows<S>(smem, wave, lane, acc, [&](int row, int col, float (&z)[8]) {
-        const int64_t m = wm + row;
-        const int n = wn + col, valid = cols - n;
-        if (m >= gr.hi || valid <= 0) return;
+    struct Aux {
+        T v[8];
+    };
+    by_rows<S, Aux>(
+        smem, wave, lane, acc,
+        [&](int row, int col) {
+            Aux x;
+            const int64_t m = wm + row;
+            const int n = wn + col, valid = cols - n;
+            if (extra && !tail && m < gr.hi && valid >= 8) {
+                load_vec(extra + m * ldx + n, x.v);
+            } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = tail ? 0.0f : z[i] + b[i];
-        if (pre) store8(pre + m * pr.ldpre + n, z, valid);
-        if (pr.act != kActNone) {
+                for (int i = 0; i < 8; ++i)
+                    x.v[i] = extra && !tail && m < gr.hi && i < valid ? extra[m * ldx + n + i] : (T)0.0f;
+            }
+            return x;
+        },
+        [&](int row, int col, float (&z)[8], const Aux &x) {
+            const int64_t m = wm + row;
+            const int n = wn + col, valid = cols - n;
+            if (m >= gr.hi || valid <= 0) return;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], pr.act);
-        }
-        float y[8];
-        if (res && !tail) {
-            load8(res + m * pr.ldr + n, valid, y);
+            for (int i = 0; i < 8; ++i) z[i] = tail ? 0.0f : z[i] + b[i];
+            if (pre) store8(pre + m * pr.ldpre + n, z, valid);
+            if (pr.act != kActNone) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] += y[i];
-        }
-        if (in && !tail) {
-            load8(in + m * pr.ldin + n, valid, y);
+                for (int i = 0; i < 8; ++i) z[i] = act_value(z[i], pr.act);
+            }
+            if (in) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) z[i] *= act_slope(y[i], pr.in_act);
-        }
-        store8(out + m * pr.ldo + n, z, valid);
-    });
+                for (int i = 0; i < 8; ++i) z[i] *= act_slope((float)x.v[i], pr.in_act);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] += (float)x.v[i];
+            }
+            store8(out + m * pr.ldo + n, z, valid);
+        });
 }
+
+constexpr int kPiece = 16;  // tiles: 4 x 4 of the walk
 
 template <class S>
 __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
@@ -517,10 +557,12 @@ __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int mc = (int)pr.m_cols, nc = (int)pr.n_cols, rows = (int)pr.rows;
     const int tiles_m = (mc + S::BM - 1) / S::BM, tiles_n = (nc + S::BN - 1) / S::BN;
-    const int64_t each = (int64_t)tiles_m * tiles_n;
-    const int64_t id = xcd_tile(each * pr.experts);
+    const int each = tiles_m * tiles_n;
+    // Experts' tiles cost as many stages as the expert has rows: dealt out in
+    // small pieces, every XCD gets tiles of every large expert.
+    const int id = xcd_tile(each * pr.experts, pr.offsets ? kPiece : 0);
     if (id < 0) return;
-    const int e = __builtin_amdgcn_readfirstlane((int)(id / each));
+    const int e = __builtin_amdgcn_readfirstlane(id / each);
     int mt, nt;
     walk(id - e * each, tiles_m, tiles_n, 4, mt, nt);
     const int m0 = mt * S::BM, n0 = nt * S::BN;
@@ -544,10 +586,13 @@ __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     T *out = (T *)pr.out + (int64_t)e * mc * nc;
-    by_rows<S>(smem, wave, lane, acc, [&](int row, int col, float (&z)[8]) {
-        const int m = wm + row, n = wn + col;
-        if (m < mc && n < nc) store8(out + (int64_t)m * nc + n, z, nc - n);
-    });
+    struct Aux {};
+    by_rows<S, Aux>(
+        smem, wave, lane, acc, [](int, int) { return Aux{}; },
+        [&](int row, int col, float (&z)[8], const Aux &) {
+            const int m = wm + row, n = wn + col;
+            if (m < mc && n < nc) store8(out + (int64_t)m * nc + n, z, nc - n);
+        });
 }
 
 inline bool on_chunk(const void *p, int64_t ld, int64_t len, int size) {
@@ -572,7 +617,8 @@ hipError_t run_rows(const RowsProblem &pr, hipStream_t s) {
 template <class S>
 hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
     const int64_t tiles = cdiv(pr.m_cols, S::BM) * cdiv(pr.n_cols, S::BN) * pr.experts;
-    grad_kernel<S><<<(unsigned)(cdiv(tiles, 8) * 8), S::NW * 64, 0, s>>>(pr);
+    const int64_t unit = pr.offsets ? 8 * kPiece : 8;
+    grad_kernel<S><<<(unsigned)(cdiv(tiles, unit) * unit), S::NW * 64, 0, s>>>(pr);
     return hipGetLastError();
 }
 

@@ -66,33 +66,43 @@ __global__ __launch_bounds__(256) void slope_kernel(const T *__restrict__ dy, in
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] = 0.0f;
     const bool full = c + V <= outs;
-#pragma unroll 2
-    for (int64_t r = r0 + wave; r < r1; r += 4) {
-        T y[V], z[V];
-        if (full) {
-            load_vec(dy + r * lddy + c, y);
-            if (pre) load_vec(pre + r * ldpre + c, z);
-        } else {
+    // kRows rows of a wave at a time, all their loads in flight together.
+    constexpr int kRows = 4;
+    for (int64_t rr = r0 + wave; rr < r1; rr += 4 * kRows) {
+        T y[kRows][V], z[kRows][V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                y[j] = c + j < outs ? dy[r * lddy + c + j] : (T)0.0f;
-                z[j] = pre && c + j < outs ? pre[r * ldpre + c + j] : (T)0.0f;
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = rr + 4 * u < r1 ? rr + 4 * u : rr;  // no condition on the loads
+            if (full) {
+                load_vec(dy + r * lddy + c, y[u]);
+                if (pre) load_vec(pre + r * ldpre + c, z[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    y[u][j] = c + j < outs ? dy[r * lddy + c + j] : (T)0.0f;
+                    z[u][j] = pre && c + j < outs ? pre[r * ldpre + c + j] : (T)0.0f;
+                }
             }
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float v = (float)y[j];
-            if (pre) v *= act_slope((float)z[j], act);
-            sum[j] += v;
-            y[j] = (T)v;
-        }
-        if (dz) {
-            if (c + V <= lddz) {
-                store_vec(dz + r * lddz + c, y);
-            } else {
+        for (int u = 0; u < kRows; ++u) {
+            const int64_t r = rr + 4 * u;
+            if (r >= r1) break;
 #pragma unroll
-                for (int j = 0; j < V; ++j)
-                    if (c + j < lddz) dz[r * lddz + c + j] = y[j];
+            for (int j = 0; j < V; ++j) {
+                float v = (float)y[u][j];
+                if (pre) v *= act_slope((float)z[u][j], act);
+                sum[j] += v;
+                y[u][j] = (T)v;
+            }
+            if (dz) {
+                if (c + V <= lddz) {
+                    store_vec(dz + r * lddz + c, y[u]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j)
+                        if (c + j < lddz) dz[r * lddz + c + j] = y[u][j];
+                }
             }
         }
     }
@@ -148,11 +158,11 @@ bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, int expe
     (void)dtype;
     (void)depth;
     const int64_t tiles = (rows / 64 + experts + 1) * cdiv(cols, 64);
-    return tiles <= kMaxGridThreads / 512;
+    return tiles <= kMaxGridThreads / 1024;
 }
 bool grad_grid_ok(int dtype, int64_t m_cols, int64_t n_cols, int experts) {
     (void)dtype;
-    return cdiv(m_cols, 64) * cdiv(n_cols, 64) * experts <= kMaxGridThreads / 512;
+    return cdiv(m_cols, 64) * cdiv(n_cols, 64) * experts <= kMaxGridThreads / 1024;
 }
 
 hipError_t launch_rows(int dtype, const RowsProblem &pr, hipStream_t s) {
@@ -173,11 +183,11 @@ hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t c
     return hipGetLastError();
 }
 
-// Parts of an expert's rows: about 1024 blocks in all, 32 rows a part at least.
+// Parts of an expert's rows: about 4096 blocks in all, 64 rows a part at least.
 int64_t slope_splits(int64_t rows, int64_t outs, int64_t experts) {
     const int64_t blocks = cdiv(outs, 256) * experts;
-    int64_t n = 1024 / blocks;
-    const int64_t most = rows / experts / 32;
+    int64_t n = 4096 / blocks;
+    const int64_t most = rows / experts / 64;
     n = n > most ? most : n;
     return n < 1 ? 1 : n > 128 ? 128 : n;
 }

@@ -376,9 +376,13 @@ struct Rows {
 
 }  // namespace
 
+bool plan_is_small(int64_t pairs, int64_t experts) {
+    return pairs <= kSmallPairs && experts <= kSmallExperts;
+}
+
 hipError_t launch_plan(const int64_t *ids, int64_t pairs, int64_t experts, int *order, int *place,
                        int *offsets, const PlanScratch &ws, hipStream_t s) {
-    if (pairs <= kSmallPairs && experts <= kSmallExperts) {
+    if (plan_is_small(pairs, experts)) {
         plan_small_kernel<<<1, 1024, 0, s>>>(ids, (int)pairs, (int)experts, order, place, offsets);
         return hipGetLastError();
     }

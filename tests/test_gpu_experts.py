@@ -538,7 +538,8 @@ def test_refusals():
     with pytest.raises(binding.KMeansError):
         experts.plan(ids, 0)
     with pytest.raises(binding.KMeansError):
-        experts.plan(ids, 3, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        experts.plan(torch.zeros(5000, 2, dtype=torch.int64, device="cuda"), 3,
+                     workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         experts.plan(ids.cpu(), 3)
     with pytest.raises(TypeError):
@@ -564,9 +565,11 @@ def test_refusals():
     with pytest.raises(ValueError):
         experts.linear_backward(randn(1, 10, 24), x, w, act="silu")
     q = randn(4, 24, 24)
-    for kw in (dict(out=q), dict(residual=q, out=q), dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))):
+    for kw in (dict(out=q), dict(residual=q, out=q)):
         with pytest.raises(binding.KMeansError):
             experts.linear(q, randn(5, 24, 24), **kw)
+    with pytest.raises(binding.KMeansError):
+        experts.linear_backward(q, q, q, act="relu", pre=q, workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
     params, grads = [randn(1, 300)], [randn(2, 300)]
     state = experts.adamw_state(params)
     for bad in (dict(lr=-1.0), dict(lr=float("nan")), dict(lr=1.0, betas=(1.0, 0.9)), dict(lr=1.0, step=0)):
