@@ -112,9 +112,9 @@ int experts_combine_backward(const void *dy, int64_t lddy, const void *ys, int64
  * 0 <= rows < 2^31; 1 <= outs, ins <= 2^20; 1 <= experts <= 65536; ld <= 2^20.
  * float32 uses the float32 matrix instructions, the 16-bit types theirs; both
  * accumulate in float32.
- * Workspace: nothing but slack, unless 16-bit rows do not lie on 16-byte
- * boundaries (ins not a multiple of 8, or, with `unaligned` non-zero, any
- * pointer or ld): then x and w are first copied to padded rows there. The
+ * Workspace: partial sums where the depth is split; and where 16-bit rows of x
+ * or w do not lie on 4-byte boundaries (ins odd, or, with `unaligned` non-zero, an
+ * odd ld or a pointer off 4 bytes) room for their copies on padded rows. The
  * size query's op: 0 for experts_linear, 1 for experts_linear_backward.
  */
 size_t experts_linear_workspace_bytes(int64_t rows, int64_t outs, int64_t ins, int64_t experts,

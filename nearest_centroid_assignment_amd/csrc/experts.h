@@ -121,6 +121,8 @@ struct RowsProblem {
     void *out, *pre;
     int64_t ldo, ldpre;
     int act, in_act;
+    int tile, splits;            // rows_plan's
+    float *partial;              // splits x rows x cols when splits > 1
 };
 // out[e] (m_cols x n_cols, dense) = dz[rows of e]^T x[rows of e].
 struct GradProblem {
@@ -131,11 +133,31 @@ struct GradProblem {
     const int *offsets;
     int experts;
     void *out;
+    int tile, splits;              // grad_plan's
+    float *partial;                // splits x experts x m_cols x n_cols when splits > 1
 };
+// How a product is cut: tiles of tile x tile (32: 32 x 64; 129: 128 x 128 with three
+// stages in flight; with `thin`, blocks of `tile` rows by 16 columns), its depth in
+// `splits` parts whose sums are joined by a second kernel.
+struct Cut {
+    int tile, splits;
+    bool thin;
+};
+Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped, int64_t experts,
+              bool p_rows);
+Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts);
+
+// Row tiles of all groups at most: every group that has a row may end in a
+// partial tile, and the rows past the last expert's are one more group.
+inline int64_t most_row_tiles(int64_t rows, int64_t bm, bool grouped, int64_t experts) {
+    if (!grouped) return cdiv(rows, bm);
+    return rows / bm + (experts + 1 < rows ? experts + 1 : rows);
+}
+
 // dtype: 0 float, 1 bf16, 2 f16. False when the launch grid would not fit.
 bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, int experts);
 bool grad_grid_ok(int dtype, int64_t m_cols, int64_t n_cols, int experts);
-hipError_t launch_rows(int dtype, const RowsProblem &pr, hipStream_t s);
+hipError_t launch_rows(int dtype, const RowsProblem &pr, bool thin, hipStream_t s);
 hipError_t launch_grad(int dtype, const GradProblem &pr, hipStream_t s);
 
 // dst rows of ldd elements (a multiple of 8) = src rows with zeros from cols on.

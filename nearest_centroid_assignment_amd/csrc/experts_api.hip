@@ -106,16 +106,16 @@ bool ld_ok(const void *p, int64_t ld, int64_t len) {
 }
 // Whether the 16-bit products can read rows of `len` in place.
 bool in_place(const void *p, int64_t ld, int64_t len) {
-    return aligned(p, 16) && ld % 8 == 0 && len % 8 == 0;
+    return aligned(p, 4) && ld % 2 == 0 && len % 2 == 0;
 }
 
 // Sections of the workspace. Every one that a call of this shape may need;
-// those for rows that do not lie on 16-byte boundaries only with `pads`.
+// those for rows that do not lie on 4-byte boundaries only with `pads`.
 struct LinearLayout {
     size_t x = 0, w = 0, dz = 0, partial = 0, total = 0;
 };
-LinearLayout linear_layout(int64_t rows, int64_t outs, int64_t ins, int64_t experts, int dtype,
-                           int op, bool pads) {
+LinearLayout linear_layout(int64_t rows, int64_t outs, int64_t ins, int64_t experts, bool grouped,
+                           int dtype, int op, bool pads) {
     LinearLayout L;
     size_t off = 0;
     if (pads) {
@@ -124,12 +124,23 @@ LinearLayout linear_layout(int64_t rows, int64_t outs, int64_t ins, int64_t expe
         L.w = off;
         off += round_up((size_t)experts * outs * pad8(ins) * 2);
     }
-    if (op == 1) {
+    // Partial sums of one kernel after another: the largest.
+    size_t partial = 0;
+    auto most = [&](int64_t parts, int64_t n) {
+        const size_t bytes = parts > 1 ? (size_t)parts * (size_t)n * 4 : 0;
+        partial = bytes > partial ? bytes : partial;
+    };
+    if (op == 0) {
+        most(kx::rows_plan(dtype, rows, outs, ins, grouped, experts, false).splits, rows * outs);
+    } else {
         L.dz = off;
         off += round_up((size_t)rows * pad8(outs) * size_of(dtype));
-        L.partial = off;
-        off += round_up((size_t)kx::slope_splits(rows, outs, experts) * experts * outs * 4);
+        most(kx::slope_splits(rows, outs, experts), experts * outs);
+        most(kx::rows_plan(dtype, rows, ins, outs, grouped, experts, true).splits, rows * ins);
+        most(kx::grad_plan(dtype, rows, outs, ins, experts).splits, experts * outs * ins);
     }
+    L.partial = off;
+    off += round_up(partial);
     L.total = off + kAlign;
     return L;
 }
@@ -273,8 +284,11 @@ size_t experts_linear_workspace_bytes(int64_t rows, int64_t outs, int64_t ins, i
     if (!linear_shape_ok(rows, outs, ins, experts) || !dtype_ok(dtype) || op < 0 || op > 1 ||
         !linear_grid_ok(dtype, rows, outs, ins, experts))
         return 0;
-    const bool pads = dtype != EXPERTS_F32 && (unaligned || ins % 8 != 0);
-    return linear_layout(rows, outs, ins, experts, dtype, op, pads).total;
+    // Without offsets a single expert may be cut differently; both fit.
+    const bool pads = dtype != EXPERTS_F32 && (unaligned || ins % 2 != 0);
+    const size_t grouped = linear_layout(rows, outs, ins, experts, true, dtype, op, pads).total;
+    const size_t dense = linear_layout(rows, outs, ins, experts, false, dtype, op, pads).total;
+    return experts == 1 && dense > grouped ? dense : grouped;
 }
 
 int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,
@@ -294,8 +308,11 @@ int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,
     if (!aligned(x, b) || !aligned(w, b) || !aligned(bias, b) || !aligned(residual, b) ||
         !aligned(out, b) || !aligned(pre, b) || !aligned(offsets, 4))
         return KM_ERR_ALIGN;
-    const bool pads = dtype != EXPERTS_F32 && !(in_place(x, ldx, ins) && in_place(w, ins, ins));
-    const LinearLayout L = linear_layout(rows, outs, ins, experts, dtype, 0, pads);
+    const kx::Cut cut = kx::rows_plan(dtype, rows, outs, ins, offsets != nullptr, experts, false);
+    const bool pads = dtype != EXPERTS_F32 && !cut.thin &&
+                      !(in_place(x, ldx, ins) && in_place(w, ins, ins));
+    const LinearLayout L =
+        linear_layout(rows, outs, ins, experts, offsets != nullptr, dtype, 0, pads);
     if (!ws_ok(workspace, workspace_bytes, L.total)) return KM_ERR_WORKSPACE;
     const Span os[] = {{out, rows, ldo, outs, b},
                        {pre, rows, ldpre, outs, b},
@@ -309,11 +326,17 @@ int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,
     if (rows == 0) return KM_OK;
     const hipStream_t s = (hipStream_t)stream;
     char *base = ws_base(workspace);
-    const Operand xq = operand(x, ldx, rows, ins, dtype, base + L.x, s);
-    if (xq.e != hipSuccess) return KM_ERR_HIP;
-    const Operand wp = operand(w, ins, experts * outs, ins, dtype, base + L.w, s);
-    if (wp.e != hipSuccess) return KM_ERR_HIP;
+    Operand xq = {x, ldx, ins, hipSuccess}, wp = {w, ins, ins, hipSuccess};
+    if (pads) {
+        xq = operand(x, ldx, rows, ins, dtype, base + L.x, s);
+        if (xq.e != hipSuccess) return KM_ERR_HIP;
+        wp = operand(w, ins, experts * outs, ins, dtype, base + L.w, s);
+        if (wp.e != hipSuccess) return KM_ERR_HIP;
+    }
     kx::RowsProblem pr = {};
+    pr.tile = cut.tile;
+    pr.splits = cut.splits;
+    pr.partial = (float *)(base + L.partial);
     pr.q = xq.p;
     pr.ldq = xq.ld;
     pr.p = wp.p;
@@ -333,7 +356,7 @@ int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,
     pr.pre = pre;
     pr.ldpre = ldpre;
     pr.act = act;
-    return status(kx::launch_rows(dtype, pr, s));
+    return status(kx::launch_rows(dtype, pr, cut.thin, s));
 }
 
 int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t ldx,
@@ -360,7 +383,8 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
         return KM_ERR_ALIGN;
     const bool half = dtype != EXPERTS_F32;
     const bool pads = half && ((dw && !in_place(x, ldx, ins)) || (dx && !in_place(w, ins, ins)));
-    const LinearLayout L = linear_layout(rows, outs, ins, experts, dtype, 1, pads);
+    const bool grouped = offsets != nullptr;
+    const LinearLayout L = linear_layout(rows, outs, ins, experts, grouped, dtype, 1, pads);
     if (!ws_ok(workspace, workspace_bytes, L.total)) return KM_ERR_WORKSPACE;
     const Span os[] = {{dx, rows, lddx, ins, b},
                        {dw, 1, 0, experts * outs * ins, b},
@@ -375,7 +399,7 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if (int rc = check_alias(os, 4, is, 6)) return rc;
     const hipStream_t s = (hipStream_t)stream;
     char *base = ws_base(workspace);
-    // dz: dy itself, or its product with act', or dy on 16-byte boundaries.
+    // dz: dy itself, or its product with act', or dy on 4-byte boundaries.
     const bool products = dx || dw;
     const bool copy = products && (act != EXPERTS_ACT_NONE || (half && !in_place(dy, lddy, outs)));
     const void *dz = dy;
@@ -393,7 +417,11 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if (dx && rows > 0) {
         const Operand wp = operand(w, ins, experts * outs, ins, dtype, base + L.w, s);
         if (wp.e != hipSuccess) return KM_ERR_HIP;
+        const kx::Cut cut = kx::rows_plan(dtype, rows, ins, outs, grouped, experts, true);
         kx::RowsProblem pr = {};
+        pr.tile = cut.tile;
+        pr.splits = cut.splits;
+        pr.partial = (float *)(base + L.partial);
         pr.q = dz;
         pr.ldq = lddz;
         pr.p = wp.p;
@@ -411,12 +439,16 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
         pr.in_act = in_act;
         pr.out = dx;
         pr.ldo = lddx;
-        if (kx::launch_rows(dtype, pr, s) != hipSuccess) return KM_ERR_HIP;
+        if (kx::launch_rows(dtype, pr, cut.thin, s) != hipSuccess) return KM_ERR_HIP;
     }
     if (dw) {
         const Operand xp = operand(x, ldx, rows, ins, dtype, base + L.x, s);
         if (xp.e != hipSuccess) return KM_ERR_HIP;
+        const kx::Cut cut = kx::grad_plan(dtype, rows, outs, ins, experts);
         kx::GradProblem pr = {};
+        pr.tile = cut.tile;
+        pr.splits = cut.splits;
+        pr.partial = (float *)(base + L.partial);
         pr.x = xp.p;
         pr.ldx = xp.ld;
         pr.x_cols = xp.cols;

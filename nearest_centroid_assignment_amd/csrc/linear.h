@@ -24,6 +24,7 @@
 //       (ds_read_b64_tr_b16: 16 lanes take 4 rows of 16 values and return each
 //       lane 4 values of one column) touches rows 8 a + b, b < 4, together.
 //       float: granules of 64 bytes at g ^ (k / 4 % 4), read 4 bytes a lane.
+//       (Rows of fewer granules use the low bits of the key.)
 #pragma once
 
 #include "experts.h"
@@ -46,56 +47,60 @@ struct Frag;  // 16 bytes of k per lane
 template <>
 struct Frag<bf16> {
     typedef bf16x8 type;
-    static __device__ __forceinline__ f32x4 mma(bf16x8 p, bf16x8 q, f32x4 c) {
+    static constexpr int kSteps = 1;  // matrix instructions for a fragment
+    static __device__ __forceinline__ f32x4 mma(bf16x8 p, bf16x8 q, f32x4 c, int) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q, c, 0, 0, 0);
     }
 };
 template <>
 struct Frag<f16> {
     typedef f16x8 type;
-    static __device__ __forceinline__ f32x4 mma(f16x8 p, f16x8 q, f32x4 c) {
+    static constexpr int kSteps = 1;
+    static __device__ __forceinline__ f32x4 mma(f16x8 p, f16x8 q, f32x4 c, int) {
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(p, q, c, 0, 0, 0);
     }
 };
 template <>
 struct Frag<float> {
     typedef f32x4 type;
+    static constexpr int kSteps = 4;
     // Lane group g holds k = 4 g .. 4 g + 3 of both operands; instruction j
     // takes element j of each lane, so its four k are j, 4 + j, 8 + j, 12 + j.
-    static __device__ __forceinline__ f32x4 mma(f32x4 p, f32x4 q, f32x4 c) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[j], q[j], c, 0, 0, 0);
-        return c;
+    static __device__ __forceinline__ f32x4 mma(f32x4 p, f32x4 q, f32x4 c, int j) {
+        return __builtin_amdgcn_mfma_f32_16x16x4f32(p[j], q[j], c, 0, 0, 0);
     }
 };
 
 // One operand's stage: R output rows (or columns) x 128 bytes of k, moved by
-// NW waves with DW bytes (16 or 4) a lane and instruction.
-template <typename T, bool MC, int R, int NW, int DW>
+// NW waves with 16 bytes a lane and instruction. Rows may start on any 4 bytes:
+// the buffer's range check works in 4-byte words, so a chunk that leaves the
+// operand is cut there. A chunk that leaves its row reads the next row's start,
+// which in an MC operand only reaches columns that are not stored; a KC row that
+// ends inside a chunk has its last stage moved in 4-byte pieces (`ragged`).
+template <typename T, bool MC, int R, int NW>
 struct Tile {
     static constexpr int kSize = (int)sizeof(T);
     static constexpr int kBytes = R * kRow;
     static constexpr int kDepth = kRow / kSize;  // k per stage
-    static constexpr int kIssues = kBytes / (64 * DW * NW);
-    static_assert(kIssues >= 1 && kIssues * 64 * DW * NW == kBytes, "tile and waves");
+    static constexpr int kIssues = kBytes / (1024 * NW);
+    static_assert(kIssues >= 1 && kIssues * 1024 * NW == kBytes, "tile and waves");
 
     uint32_t off[kIssues];
-    int kc[2];        // KC: byte of k that this lane moves, by the parity of the issue
+    int kc[2];        // KC: byte of k that this lane moves, by the parity of the issue (8 rows each)
     uint64_t at;      // this stage's first row or column (the rest is wave-uniform too)
     int ld, left;     // bytes of a row; KC: bytes, MC: rows of k from this stage on
     int extent;       // KC: bytes before the last valid row (< 0: no row); MC: valid bytes of a row
 
     static __device__ __forceinline__ int swizzle(int k) {  // MC, in 16-byte chunks
         if (kSize == 2) return (((k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1)) << 1;
-        return ((k >> 2) & 3) << 2;
+        return ((k >> 2) & 3 & (R / 16 - 1)) << 2;
     }
     // Byte q of the stage in LDS: its byte of the row in memory (KC).
     static __device__ __forceinline__ int kc_byte(int q) {
         return ((((q & (kRow - 1)) >> 4) ^ ((q >> 8) & 7)) << 4) | (q & 15);
     }
     static __device__ __forceinline__ int lds_byte(int wave, int lane, int i) {
-        return ((wave * kIssues + i) * 64 + lane) * DW;
+        return ((wave * kIssues + i) * 64 + lane) * 16;
     }
 
     // p: the tile's first row (KC) or column (MC) at k = 0; valid: rows or columns.
@@ -106,10 +111,8 @@ struct Tile {
              (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)a);
         ld = __builtin_amdgcn_readfirstlane((int)(ld_elems * kSize));
         const int n = (int)(valid < 0 ? 0 : valid > R ? R : valid);
-        // 16-bit rows are padded with zeros to whole 16 bytes; the range check
-        // drops a 4-byte word that the records end inside of.
-        left = __builtin_amdgcn_readfirstlane(
-            MC ? depth : kSize == 2 ? (depth + 7) / 8 * 16 : depth * kSize);
+        // (A row of an odd number of 16-bit values comes padded with a zero.)
+        left = __builtin_amdgcn_readfirstlane(MC ? depth : (depth * kSize + 3) & ~3);
         extent = __builtin_amdgcn_readfirstlane(MC ? n * kSize : n ? (n - 1) * ld : -(1 << 30));
 #pragma unroll
         for (int i = 0; i < kIssues; ++i) {
@@ -127,9 +130,13 @@ struct Tile {
         kc[1] = kc_byte(lds_byte(wave, lane, kIssues > 1 ? 1 : 0));
     }
 
+    // Whether the last stage has to be moved in 4-byte pieces.
+    __device__ __forceinline__ bool ragged() const { return !MC && (left & 15) != 0; }
+
     // Moves this stage into LDS and steps to the next. Past the last stage
-    // every lane is out of range, and zeros arrive.
-    __device__ __forceinline__ void issue(lds_char *lds, int wave, int lane) {
+    // every lane is out of range, and zeros arrive. `last`: this may be the
+    // ragged stage.
+    __device__ __forceinline__ void issue(lds_char *lds, int wave, int lane, bool last) {
         int records = 0;
         if (MC) {
             const int rows = left < kDepth ? left : kDepth;
@@ -140,20 +147,23 @@ struct Tile {
         }
         const __amdgpu_buffer_rsrc_t rsrc =
             __builtin_amdgcn_make_buffer_rsrc((void *)at, 0, records, 0x00020000);
-#pragma unroll
-        for (int i = 0; i < kIssues; ++i) {
-            uint32_t o = off[i];
-            if (!MC) {
-                // With 16 bytes a lane an issue covers 8 rows, so its bytes of k
-                // depend on the parity of the issue alone; with 4, on i % 4.
-                const int k = DW == 16 ? kc[i & 1] : kc_byte(lds_byte(wave, lane, i));
-                o = k < left ? o : kNowhere;
+        lds_char *to = lds + wave * kIssues * 1024;
+        if (!MC && last && left < kRow && (left & 15)) {
+#pragma unroll 1
+            for (int i = 0; i < kIssues * 4; ++i) {
+                const int q = (wave * kIssues * 4 + i) * 256 + lane * 4, k = kc_byte(q);
+                const uint32_t o = k < left ? (uint32_t)((q >> 7) * ld + k) : kNowhere;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + i * 256), 4, (int)o,
+                                                         0, 0, 0);
             }
-            lds_char *to = lds + (wave * kIssues + i) * 64 * DW;
-            if constexpr (DW == 16)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)to, 16, (int)o, 0, 0, 0);
-            else
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)to, 4, (int)o, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kIssues; ++i) {
+                uint32_t o = off[i];
+                if (!MC) o = kc[i & 1] < left ? o : kNowhere;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + i * 1024), 16, (int)o,
+                                                         0, 0, 0);
+            }
         }
         at += MC ? (uint64_t)ld * kDepth : (uint64_t)kRow;
         left -= MC ? kDepth : kRow;
@@ -181,7 +191,7 @@ struct Reader {
                     const int key = ((k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1);
                     at[t] = k * (R * 2) + (((first / 16 + t) ^ key) << 5) + (i & 3) * 8;
                 } else {
-                    at[t] = 4 * g * (R * 4) + (((first / 16 + t) ^ g) << 6) + i * 4;
+                    at[t] = 4 * g * (R * 4) + (((first / 16 + t) ^ (g & (R / 16 - 1))) << 6) + i * 4;
                 }
             }
         }
@@ -208,14 +218,14 @@ struct Reader {
     }
 };
 
-template <typename T, bool PMC, bool QMC, int BM_, int BN_, int WM_, int WN_, int DW_>
+template <typename T, bool PMC, bool QMC, int BM_, int BN_, int WM_, int WN_, int NS_>
 struct Shape {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, DW = DW_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
     static constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     static constexpr int kStage = (BM + BN) * kRow;
     typedef T type;
-    typedef Tile<T, PMC, BN, NW, DW> TileP;
-    typedef Tile<T, QMC, BM, NW, DW> TileQ;
+    typedef Tile<T, PMC, BN, NW> TileP;
+    typedef Tile<T, QMC, BM, NW> TileQ;
     typedef Reader<T, PMC, BN, TN> ReadP;
     typedef Reader<T, QMC, BM, TM> ReadQ;
     static constexpr bool p_mc = PMC, q_mc = QMC;
@@ -236,18 +246,22 @@ __device__ __forceinline__ void read_half(const typename S::ReadP &rp, const typ
 }
 template <class S>
 __device__ __forceinline__ void multiply(const Frags<S> &f, f32x4 (&acc)[S::TM][S::TN]) {
+    // One accumulator's instructions lie a whole block apart: back to back each
+    // would wait for the one before it.
 #pragma unroll
-    for (int m = 0; m < S::TM; ++m)
+    for (int j = 0; j < Frag<typename S::type>::kSteps; ++j)
 #pragma unroll
-        for (int n = 0; n < S::TN; ++n)
-            acc[m][n] = Frag<typename S::type>::mma(f.p[n], f.q[m], acc[m][n]);
+        for (int m = 0; m < S::TM; ++m)
+#pragma unroll
+            for (int n = 0; n < S::TN; ++n)
+                acc[m][n] = Frag<typename S::type>::mma(f.p[n], f.q[m], acc[m][n], j);
 }
 
 // The order of one half-stage: its LDS reads (for the half after it) and
 // `moves` global-to-LDS loads spread evenly over its matrix instructions.
 template <class S>
 __device__ __forceinline__ void spread(bool moves) {
-    constexpr int kMma = S::TM * S::TN * (sizeof(typename S::type) == 4 ? 4 : 1);
+    constexpr int kMma = S::TM * S::TN * Frag<typename S::type>::kSteps;
     constexpr int kReadsP = S::TN * (S::p_mc ? (sizeof(typename S::type) == 4 ? 4 : 2) : 1);
     constexpr int kReadsQ = S::TM * (S::q_mc ? (sizeof(typename S::type) == 4 ? 4 : 2) : 1);
     constexpr int kReads = kReadsP + kReadsQ;
@@ -267,10 +281,17 @@ __device__ __forceinline__ void spread(bool moves) {
     }
 }
 
-// acc[tm][tn] += the tile's product over the whole depth. Two stages in LDS and
-// two half-stages of fragments in registers: while one half is multiplied, the
-// next is read, and in the second half of a stage, whose buffer every wave has
-// read by then, the stage after the next moves in.
+// Waits until at most `loads` loads of the wave are in flight, and for its LDS reads.
+template <int loads>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(loads < 64, "the counter's width");
+    __builtin_amdgcn_s_waitcnt((loads & 15) | (7 << 4) | ((loads >> 4) << 14));
+}
+
+// acc[tm][tn] += the tile's product over the whole depth. NS stages in LDS and two
+// half-stages of fragments in registers: while one half is multiplied, the next
+// is read, and in the second half of a stage, whose buffer every wave has read
+// by then, the stage NS later moves in.
 template <class S>
 __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
                                         typename S::TileQ &tq, int depth, int wave, int lane,
@@ -281,28 +302,45 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
     rq.init((wave / S::WN) * (S::BM / S::WM), lane);
     const int stages = __builtin_amdgcn_readfirstlane((depth + S::TileP::kDepth - 1) / S::TileP::kDepth);
     if (stages == 0) return;
-    tp.issue(smem, wave, lane);
-    tq.issue(smem + S::BN * kRow, wave, lane);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    tp.issue(smem + S::kStage, wave, lane);
-    tq.issue(smem + S::kStage + S::BN * kRow, wave, lane);
+    constexpr int kMoves = S::TileP::kIssues + S::TileQ::kIssues;
+    const bool ragged = tp.ragged() || tq.ragged();
+#pragma unroll
+    for (int i = 0; i < S::NS; ++i) {
+        tp.issue(smem + i * S::kStage, wave, lane, true);
+        tq.issue(smem + i * S::kStage + S::BN * kRow, wave, lane, true);
+    }
+    wait_loads<(S::NS - 1) * kMoves>();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     Frags<S> f[2];
     read_half<S>(rp, rq, smem, 0, f[0]);
-    for (int it = 0; it < stages; ++it) {
-        lds_char *cur = smem + (it & 1) * S::kStage;
-        lds_char *nxt = smem + ((it & 1) ^ 1) * S::kStage;
+    lds_char *cur = smem;
+    auto stage = [&](bool last) {
+        lds_char *nxt = cur + S::kStage == smem + S::NS * S::kStage ? smem : cur + S::kStage;
         read_half<S>(rp, rq, cur, 1, f[1]);
         multiply<S>(f[0], acc);
         spread<S>(false);
-        __builtin_amdgcn_s_waitcnt(0);
-        __syncthreads();  // the next stage has landed, and this one is in registers
+        // (A ragged stage has more loads than kMoves: then this waits for more.)
+        wait_loads<(S::NS - 2) * kMoves>();
+        // The next stage has landed, and this one is in registers. (Loads of later
+        // stages stay in flight across the barrier; __syncthreads would wait.)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         read_half<S>(rp, rq, nxt, 0, f[0]);
-        tp.issue(cur, wave, lane);
-        tq.issue(cur + S::BN * kRow, wave, lane);
+        tp.issue(cur, wave, lane, last);
+        tq.issue(cur + S::BN * kRow, wave, lane, last);
         multiply<S>(f[1], acc);
-        spread<S>(true);
-    }
+        if (!last) spread<S>(true);
+        cur = nxt;
+    };
+    // Stage it + NS moves in during stage it: the ragged one, if any, is the last.
+    const int plain = ragged ? stages - S::NS - 1 : stages;
+    int it = 0;
+    for (; it < plain; ++it) stage(false);
+#pragma unroll 1
+    for (; it < stages; ++it) stage(true);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();  // the stages' memory is free
 }
@@ -402,8 +440,9 @@ __device__ __forceinline__ void by_rows(lds_char *smem, int wave, int lane,
     constexpr int kLanes = kCols / 8;   // lanes to a row
     constexpr int kRows = 64 / kLanes;  // rows at a time
     constexpr int kParts = 16 / kRows;
-    constexpr int kAhead = 2;           // blocks of 16 rows in LDS at a time
-    static_assert(kAhead * 16 * kLd * S::NW <= 2 * S::kStage, "the stages' memory");
+    constexpr int kAhead = S::TM < 2 ? 1 : 2;  // blocks of 16 rows in LDS at a time
+    static_assert(kParts >= 1 && S::TM % kAhead == 0, "two column blocks a wave at least");
+    static_assert(kAhead * 16 * kLd * S::NW <= S::NS * S::kStage, "the stages' memory");
     lds_char *own = smem + wave * kAhead * 16 * kLd;
     const int row = lane / kLanes, col = lane % kLanes * 8;
     Aux aux[S::TM][kParts];
@@ -443,6 +482,13 @@ struct RowsArgs {
     int gm;  // row tiles walked per column tile, so that a group's operands stay in L2
 };
 
+// Part `part` of `parts` of a depth of `stages` stages: whole stages.
+__device__ __forceinline__ void part_of(int stages, int parts, int part, int &first, int &count) {
+    const int per = (stages + parts - 1) / parts;
+    first = part * per < stages ? part * per : stages;
+    count = stages - first < per ? stages - first : per;
+}
+
 // Tile (mt, nt) of the walk's place id: groups of gm row tiles, row first.
 __device__ __forceinline__ void walk(int id, int tiles_m, int tiles_n, int gm, int &mt, int &nt) {
     const int per = gm * tiles_n;
@@ -455,9 +501,9 @@ __device__ __forceinline__ void walk(int id, int tiles_m, int tiles_n, int gm, i
 }
 
 template <class S>
-__global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs a) {
+__global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
     typedef typename S::type T;
-    __shared__ __align__(1024) char memory[2 * S::kStage];
+    __shared__ __align__(1024) char memory[S::NS * S::kStage];
     lds_char *smem = (lds_char *)memory;
     const RowsProblem &pr = a.pr;
     const int lane = threadIdx.x & 63;
@@ -469,8 +515,11 @@ __global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs a) {
         tiles_m = find_group(pr.offsets, pr.experts, rows, S::BM, -1).tile;
     else
         tiles_m = (rows + S::BM - 1) / S::BM;
-    const int id = xcd_tile(tiles_m * tiles_n, 0);
+    const int tiles = tiles_m * tiles_n;
+    int id = xcd_tile(tiles * pr.splits, 0);
     if (id < 0) return;
+    const int part = __builtin_amdgcn_readfirstlane(id / tiles);
+    id -= part * tiles;
     int mt, nt;
     walk(id, tiles_m, tiles_n, a.gm, mt, nt);
     Group gr = {0, 0, rows, mt};
@@ -484,17 +533,35 @@ __global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs a) {
 #pragma unroll
         for (int n = 0; n < S::TN; ++n) acc[m][n] = f32x4{0, 0, 0, 0};
     if (!tail) {
-        const char *q = (const char *)pr.q + (int64_t)m0 * pr.ldq * sizeof(T);
+        constexpr int kDepth = S::TileP::kDepth;
+        const int depth = (int)pr.depth;
+        int first, count;
+        part_of((depth + kDepth - 1) / kDepth, pr.splits, part, first, count);
+        const int k0 = __builtin_amdgcn_readfirstlane(first * kDepth);
+        const int len = depth - k0 < count * kDepth ? depth - k0 : count * kDepth;
+        const char *q = (const char *)pr.q + ((int64_t)m0 * pr.ldq + k0) * sizeof(T);
         const char *p = (const char *)pr.p + (int64_t)gr.expert * pr.p_expert * sizeof(T);
-        p += (S::p_mc ? (int64_t)n0 : (int64_t)n0 * pr.ldp) * sizeof(T);
+        p += (S::p_mc ? k0 * pr.ldp + n0 : n0 * pr.ldp + k0) * sizeof(T);
         typename S::TileP tp;
         typename S::TileQ tq;
-        tp.init(p, pr.ldp, S::p_mc ? pr.p_cols - n0 : (int64_t)cols - n0, pr.depth, wave, lane);
-        tq.init(q, pr.ldq, gr.hi - m0, pr.depth, wave, lane);
-        product<S>(smem, tp, tq, (int)pr.depth, wave, lane, acc);
+        tp.init(p, pr.ldp, S::p_mc ? pr.p_cols - n0 : (int64_t)cols - n0, len, wave, lane);
+        tq.init(q, pr.ldq, gr.hi - m0, len, wave, lane);
+        product<S>(smem, tp, tq, len, wave, lane, acc);
     }
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
+    struct None {};
+    if (pr.splits > 1) {
+        float *partial = pr.partial + (int64_t)part * pr.rows * cols;
+        by_rows<S, None>(
+            smem, wave, lane, acc, [](int, int) { return None{}; },
+            [&](int row, int col, float (&z)[8], const None &) {
+                const int64_t m = wm + row;
+                const int n = wn + col;
+                if (m < gr.hi && n < cols && !tail) store8(partial + m * cols + n, z, cols - n);
+            });
+        return;
+    }
     T *out = (T *)pr.out, *pre = (T *)pr.pre;
     const T *bias = (const T *)pr.bias;
     // The residual of the forward product or the input's activation of dx.
@@ -549,9 +616,9 @@ __global__ __launch_bounds__(S::NW * 64, 1) void rows_kernel(RowsArgs a) {
 constexpr int kPiece = 16;  // tiles: 4 x 4 of the walk
 
 template <class S>
-__global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
+__global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
     typedef typename S::type T;
-    __shared__ __align__(1024) char memory[2 * S::kStage];
+    __shared__ __align__(1024) char memory[S::NS * S::kStage];
     lds_char *smem = (lds_char *)memory;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -560,8 +627,11 @@ __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
     const int each = tiles_m * tiles_n;
     // Experts' tiles cost as many stages as the expert has rows: dealt out in
     // small pieces, every XCD gets tiles of every large expert.
-    const int id = xcd_tile(each * pr.experts, pr.offsets ? kPiece : 0);
+    const int tiles = each * pr.experts;
+    int id = xcd_tile(tiles * pr.splits, pr.offsets ? kPiece : 0);
     if (id < 0) return;
+    const int part = __builtin_amdgcn_readfirstlane(id / tiles);
+    id -= part * tiles;
     const int e = __builtin_amdgcn_readfirstlane(id / each);
     int mt, nt;
     walk(id - e * each, tiles_m, tiles_n, 4, mt, nt);
@@ -570,6 +640,13 @@ __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
     if (pr.offsets) {
         lo = __builtin_amdgcn_readfirstlane(clampi(pr.offsets[e], 0, rows));
         hi = __builtin_amdgcn_readfirstlane(clampi(pr.offsets[e + 1], lo, rows));
+    }
+    {
+        constexpr int kDepth = S::TileP::kDepth;
+        int first, count;
+        part_of((hi - lo + kDepth - 1) / kDepth, pr.splits, part, first, count);
+        lo = __builtin_amdgcn_readfirstlane(lo + first * kDepth);
+        hi = __builtin_amdgcn_readfirstlane(hi - lo < count * kDepth ? hi : lo + count * kDepth);
     }
     f32x4 acc[S::TM][S::TN];
 #pragma unroll
@@ -586,22 +663,18 @@ __global__ __launch_bounds__(S::NW * 64, 1) void grad_kernel(GradProblem pr) {
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     T *out = (T *)pr.out + (int64_t)e * mc * nc;
-    struct Aux {};
-    by_rows<S, Aux>(
-        smem, wave, lane, acc, [](int, int) { return Aux{}; },
-        [&](int row, int col, float (&z)[8], const Aux &) {
+    float *partial = pr.partial + ((int64_t)part * pr.experts + e) * mc * nc;
+    struct None {};
+    by_rows<S, None>(
+        smem, wave, lane, acc, [](int, int) { return None{}; },
+        [&](int row, int col, float (&z)[8], const None &) {
             const int m = wm + row, n = wn + col;
-            if (m < mc && n < nc) store8(out + (int64_t)m * nc + n, z, nc - n);
+            if (m >= mc || n >= nc) return;
+            if (pr.splits > 1)
+                store8(partial + (int64_t)m * nc + n, z, nc - n);
+            else
+                store8(out + (int64_t)m * nc + n, z, nc - n);
         });
-}
-
-inline bool on_chunk(const void *p, int64_t ld, int64_t len, int size) {
-    return (uintptr_t)p % 16 == 0 && ld * size % 16 == 0 && len * size % 16 == 0;
-}
-
-// Row tiles of all experts at most: each may end in a partial tile.
-inline int64_t most_row_tiles(int64_t rows, int bm, const void *offsets, int experts) {
-    return offsets ? rows / bm + experts + 1 : cdiv(rows, bm);
 }
 
 template <class S>
@@ -609,50 +682,165 @@ hipError_t run_rows(const RowsProblem &pr, hipStream_t s) {
     RowsArgs a;
     a.pr = pr;
     a.gm = 8;
-    const int64_t tiles = most_row_tiles(pr.rows, S::BM, pr.offsets, pr.experts) * cdiv(pr.cols, S::BN);
+    const int64_t tiles = most_row_tiles(pr.rows, S::BM, pr.offsets != nullptr, pr.experts) *
+                          cdiv(pr.cols, S::BN) * pr.splits;
     rows_kernel<S><<<(unsigned)(cdiv(tiles, 8) * 8), S::NW * 64, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <class S>
 hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
-    const int64_t tiles = cdiv(pr.m_cols, S::BM) * cdiv(pr.n_cols, S::BN) * pr.experts;
+    const int64_t tiles = cdiv(pr.m_cols, S::BM) * cdiv(pr.n_cols, S::BN) * pr.experts * pr.splits;
     const int64_t unit = pr.offsets ? 8 * kPiece : 8;
     grad_kernel<S><<<(unsigned)(cdiv(tiles, unit) * unit), S::NW * 64, 0, s>>>(pr);
     return hipGetLastError();
 }
 
-// Tiles that one launch computes with tiles of bm x bn.
-inline int64_t rows_tiles(const RowsProblem &pr, int bm, int bn) {
-    return (cdiv(pr.rows, bm) + (pr.offsets ? pr.experts / 2 : 0)) * cdiv(pr.cols, bn);
-}
-
-template <typename T, bool PMC, int DW>
+template <typename T, bool PMC>
 hipError_t pick_rows(const RowsProblem &pr, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (rows_tiles(pr, 256, 256) >= 192)
-            return run_rows<Shape<T, PMC, false, 256, 256, 2, 4, DW>>(pr, s);
+        if (pr.tile == 256) return run_rows<Shape<T, PMC, false, 256, 256, 2, 4, 2>>(pr, s);
+        if (pr.tile == 129) return run_rows<Shape<T, PMC, false, 128, 128, 2, 4, 3>>(pr, s);
+    } else {
+        if (pr.tile == 32) return run_rows<Shape<T, PMC, false, 32, 64, 2, 2, 2>>(pr, s);
     }
-    if (rows_tiles(pr, 128, 128) >= 192)
-        return run_rows<Shape<T, PMC, false, 128, 128, 2, 2, DW>>(pr, s);
-    return run_rows<Shape<T, PMC, false, 64, 64, 2, 2, DW>>(pr, s);
+    if (pr.tile == 128) return run_rows<Shape<T, PMC, false, 128, 128, 2, 4, 2>>(pr, s);
+    return run_rows<Shape<T, PMC, false, 64, 64, 2, 2, 2>>(pr, s);
 }
 
-template <typename T, int DW>
+template <typename T>
 hipError_t pick_grad(const GradProblem &pr, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (cdiv(pr.m_cols, 256) * cdiv(pr.n_cols, 256) * pr.experts >= 192)
-            return run_grad<Shape<T, true, true, 256, 256, 2, 4, DW>>(pr, s);
+        if (pr.tile == 256) return run_grad<Shape<T, true, true, 256, 256, 2, 4, 2>>(pr, s);
+        if (pr.tile == 129) return run_grad<Shape<T, true, true, 128, 128, 2, 4, 3>>(pr, s);
+    } else {
+        if (pr.tile == 32) return run_grad<Shape<T, true, true, 32, 64, 2, 2, 2>>(pr, s);
     }
-    if (cdiv(pr.m_cols, 128) * cdiv(pr.n_cols, 128) * pr.experts >= 192)
-        return run_grad<Shape<T, true, true, 128, 128, 2, 2, DW>>(pr, s);
-    return run_grad<Shape<T, true, true, 64, 64, 2, 2, DW>>(pr, s);
+    if (pr.tile == 128) return run_grad<Shape<T, true, true, 128, 128, 2, 4, 2>>(pr, s);
+    return run_grad<Shape<T, true, true, 64, 64, 2, 2, 2>>(pr, s);
+}
+
+// Products with few rows an expert (BM = 16 MT of them to a block): bound by
+// reading w once, so nothing is shared through LDS. A block has 16 columns; its
+// eight waves take an eighth of the depth each, every lane loading its fragments
+// straight from memory, 16 bytes at any alignment, a batch of them in flight, and
+// the eight partial tiles meet in LDS. Rows and columns past the end are read at
+// the last valid one and not stored.
+template <typename T, int MT>
+__global__ __launch_bounds__(512) void thin_kernel(RowsProblem pr) {
+    typedef typename Frag<T>::type frag;
+    constexpr int kWaves = 8, kLane = 16 / (int)sizeof(T), kStep = 4 * kLane;
+    constexpr int kBatch = MT == 1 ? 8 : 6;
+    __shared__ float part[kWaves][MT][64][4];
+    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int rows = (int)pr.rows, cols = (int)pr.cols, depth = (int)pr.depth;
+    const int tiles_n = (cols + 15) / 16;
+    const int mt = __builtin_amdgcn_readfirstlane(blockIdx.x / tiles_n);
+    const int n0 = (blockIdx.x - mt * tiles_n) * 16;
+    Group gr = {0, 0, rows, mt};
+    if (pr.offsets) gr = find_group(pr.offsets, pr.experts, rows, 16 * MT, mt);
+    if (gr.expert < 0) return;
+    const int m0 = gr.lo + gr.tile * 16 * MT;
+    const bool tail = gr.expert == pr.experts;
+    f32x4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = f32x4{0, 0, 0, 0};
+    if (!tail) {
+        const int steps = (depth + kStep - 1) / kStep;
+        int first, count;
+        part_of(steps, kWaves, wave, first, count);
+        const int n = n0 + i < cols ? n0 + i : cols - 1;
+        const T *p = (const T *)pr.p + gr.expert * pr.p_expert + n * pr.ldp + g * kLane;
+        const T *q[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const int m = m0 + 16 * t + i < gr.hi ? m0 + 16 * t + i : gr.hi - 1;
+            q[t] = (const T *)pr.q + (int64_t)m * pr.ldq + g * kLane;
+        }
+        int s = first;
+        const int whole = depth / kStep < first + count ? depth / kStep : first + count;
+        union Chunk {
+            T v[kLane];
+            frag f;
+        };
+        for (; s + kBatch <= whole; s += kBatch) {
+            Chunk a[kBatch], b[kBatch][MT];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                load_vec(p + (s + u) * kStep, a[u].v);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) load_vec(q[t] + (s + u) * kStep, b[u][t].v);
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+#pragma unroll
+                    for (int j = 0; j < Frag<T>::kSteps; ++j)
+                        acc[t] = Frag<T>::mma(a[u].f, b[u][t].f, acc[t], j);
+        }
+        for (; s < first + count; ++s) {
+            // One step at a time, the last of them possibly past the depth's end.
+            const int left = depth - s * kStep - g * kLane;
+            Chunk a, b;
+            auto some = [&](const T *x, Chunk &c) {
+                if (left >= kLane) {
+                    load_vec(x + s * kStep, c.v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kLane; ++j) c.v[j] = j < left ? x[s * kStep + j] : (T)0.0f;
+                }
+            };
+            some(p, a);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                some(q[t], b);
+#pragma unroll
+                for (int j = 0; j < Frag<T>::kSteps; ++j) acc[t] = Frag<T>::mma(a.f, b.f, acc[t], j);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) part[wave][t][lane][r] = acc[t][r];
+    __syncthreads();
+    // Lane l of the tile holds columns 4 (l / 16) .. + 3 of row l % 16.
+    for (int j = threadIdx.x; j < MT * 256; j += 512) {
+        const int t = j >> 8, row = (j >> 4) & 15, col = j & 15;
+        const int64_t m = m0 + 16 * t + row;
+        const int n = n0 + col;
+        if (m >= gr.hi || n >= cols) continue;
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) z += part[w][t][(col >> 2) * 16 + row][col & 3];
+        if (tail) z = 0.0f;
+        if (pr.bias && !tail) z += (float)((const T *)pr.bias)[(int64_t)gr.expert * cols + n];
+        if (pr.pre) ((T *)pr.pre)[m * pr.ldpre + n] = (T)z;
+        z = act_value(z, pr.act);
+        if (pr.residual && !tail) z += (float)((const T *)pr.residual)[m * pr.ldr + n];
+        ((T *)pr.out)[m * pr.ldo + n] = (T)z;
+    }
+}
+
+template <typename T, int MT>
+hipError_t run_thin(const RowsProblem &pr, hipStream_t s) {
+    const int64_t tiles = most_row_tiles(pr.rows, 16 * MT, pr.offsets != nullptr, pr.experts);
+    thin_kernel<T, MT><<<(unsigned)(tiles * cdiv(pr.cols, 16)), 512, 0, s>>>(pr);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t pick_thin(const RowsProblem &pr, hipStream_t s) {
+    return pr.tile == 16 ? run_thin<T, 1>(pr, s) : run_thin<T, 2>(pr, s);
 }
 
 }  // namespace
 
 template <typename T>
 hipError_t launch_rows_t(const RowsProblem &pr, hipStream_t s);
+template <typename T>
+hipError_t launch_thin_t(const RowsProblem &pr, hipStream_t s);
 template <typename T>
 hipError_t launch_grad_t(const GradProblem &pr, hipStream_t s);
 

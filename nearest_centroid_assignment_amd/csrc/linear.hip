@@ -8,6 +8,8 @@ namespace kx {
 template <typename T>
 hipError_t launch_rows_t(const RowsProblem &pr, hipStream_t s);
 template <typename T>
+hipError_t launch_thin_t(const RowsProblem &pr, hipStream_t s);
+template <typename T>
 hipError_t launch_grad_t(const GradProblem &pr, hipStream_t s);
 
 namespace {
@@ -33,6 +35,103 @@ __global__ __launch_bounds__(256) void pad_rows_kernel(const uint16_t *__restric
         for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? p[j] : (uint16_t)0;
     }
     store_vec(dst + r * ldd + c, v);
+}
+
+// The join of a product whose depth was split: eight columns of a row a thread,
+// the parts added in order, then the epilogue.
+template <typename T>
+__global__ __launch_bounds__(256) void join_rows_kernel(RowsProblem pr) {
+    const int64_t chunks = (pr.cols + 7) / 8;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = id / chunks;
+    const int n = (int)(id - m * chunks) * 8;
+    if (m >= pr.rows) return;
+    const int valid = (int)pr.cols - n < 8 ? (int)pr.cols - n : 8;
+    int expert = 0;
+    if (pr.offsets) {  // the first expert whose rows end past m
+        int lo = 0, hi = pr.experts;
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (pr.offsets[mid + 1] > m)
+                hi = mid;
+            else
+                lo = mid + 1;
+        }
+        expert = lo;
+    }
+    const bool tail = expert == pr.experts && pr.offsets;
+    const int64_t part = pr.rows * pr.cols;
+    const float *p = pr.partial + m * pr.cols + n;
+    float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (!tail) {
+#pragma unroll 4
+        for (int s = 0; s < pr.splits; ++s) {
+            if (valid == 8) {
+                float x[8];
+                load_vec(p + s * part, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[i] += x[i];
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < valid) z[i] += p[s * part + i];
+            }
+        }
+    }
+    const T *bias = (const T *)pr.bias, *res = (const T *)pr.residual, *in = (const T *)pr.in_pre;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i >= valid) break;
+        if (bias && !tail) z[i] += (float)bias[(int64_t)expert * pr.cols + n + i];
+        if (pr.pre) ((T *)pr.pre)[m * pr.ldpre + n + i] = (T)z[i];
+        z[i] = act_value(z[i], pr.act);
+        if (res && !tail) z[i] += (float)res[m * pr.ldr + n + i];
+        if (in && !tail) z[i] *= act_slope((float)in[m * pr.ldin + n + i], pr.in_act);
+        ((T *)pr.out)[m * pr.ldo + n + i] = (T)z[i];
+    }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void join_grad_kernel(const float *__restrict__ partial,
+                                                        int splits, int64_t n, T *__restrict__ out) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+    if (i >= n) return;
+    if (i + 4 <= n) {
+        float z[4] = {0, 0, 0, 0};
+#pragma unroll 4
+        for (int s = 0; s < splits; ++s) {
+            float x[4];
+            load_vec(partial + s * n + i, x);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) z[j] += x[j];
+        }
+        T r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = (T)z[j];
+        store_vec(out + i, r);
+    } else {
+        for (int64_t j = i; j < n; ++j) {
+            float z = 0.0f;
+            for (int s = 0; s < splits; ++s) z += partial[s * n + j];
+            out[j] = (T)z;
+        }
+    }
+}
+
+template <typename T>
+hipError_t rows_t(const RowsProblem &pr, bool thin, hipStream_t s) {
+    const hipError_t e = thin ? launch_thin_t<T>(pr, s) : launch_rows_t<T>(pr, s);
+    if (e != hipSuccess || pr.splits == 1) return e;
+    join_rows_kernel<T><<<(unsigned)cdiv(pr.rows * cdiv(pr.cols, 8), 256), 256, 0, s>>>(pr);
+    return hipGetLastError();
+}
+template <typename T>
+hipError_t grad_t(const GradProblem &pr, hipStream_t s) {
+    const hipError_t e = launch_grad_t<T>(pr, s);
+    if (e != hipSuccess || pr.splits == 1) return e;
+    const int64_t n = pr.m_cols * pr.n_cols * pr.experts;
+    join_grad_kernel<T><<<(unsigned)cdiv(n, 1024), 256, 0, s>>>(pr.partial, pr.splits, n, (T *)pr.out);
+    return hipGetLastError();
 }
 
 // One block: 64 * V columns (a lane has V of them) of the rows of part s of
@@ -153,26 +252,95 @@ hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
 
 }  // namespace
 
-// The smallest tile is 64 x 64 with 256 threads; larger ones need fewer.
+// The most blocks that any cut launches: 16 x 16 with 512 threads, or 32 x 64 with
+// 256 (a depth is split only where there are at most 1024 blocks).
 bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, int experts) {
     (void)dtype;
     (void)depth;
-    const int64_t tiles = (rows / 64 + experts + 1) * cdiv(cols, 64);
-    return tiles <= kMaxGridThreads / 1024;
+    const int64_t thin = (rows / 16 + experts + 1) * cdiv(cols, 16);
+    return thin <= kMaxGridThreads / 512;
 }
 bool grad_grid_ok(int dtype, int64_t m_cols, int64_t n_cols, int experts) {
     (void)dtype;
-    return cdiv(m_cols, 64) * cdiv(n_cols, 64) * experts <= kMaxGridThreads / 1024;
+    return cdiv(m_cols, 32) * cdiv(n_cols, 64) * experts <= kMaxGridThreads / 512;
 }
 
-hipError_t launch_rows(int dtype, const RowsProblem &pr, hipStream_t s) {
+namespace {
+
+// What a cut costs, in microseconds, from measured runs: a tile's stage costs
+// `each` on a compute unit that is kept busy by its tiles, and `wait` on top per
+// stage for latency that nothing hides; a round of tiles costs `edge` for its first
+// loads and its epilogue; joining split depths writes and reads the sums.
+//   (bf16, before -> chosen: 2048 x 2048 x 2048 30 us in 256 tiles of 128 -> 25 with three stages
+//   in flight; 512 x 1024 with depth 4096 37 us in 128 tiles of 64 -> 20 in four parts;
+//   188 x 4096 with depth 776 8 us in 64s against 15 in two parts or in 128s.)
+struct TileCost {
+    int tile, rows, cols;
+    double each, wait, edge;
+};
+constexpr TileCost kHalf[] = {{256, 256, 256, 1.65, 0.10, 8.0},
+                              {128, 128, 128, 0.50, 0.20, 2.5},
+                              {64, 64, 64, 0.13, 0.40, 1.0}};
+constexpr TileCost kFloat[] = {{128, 128, 128, 1.75, 0.10, 5.0},
+                               {64, 64, 64, 0.44, 0.15, 2.0},
+                               {32, 32, 64, 0.23, 0.20, 1.5}};
+
+// tiles_of(rows, cols): the number of tiles of that size; sums: values to join.
+template <class F>
+Cut best_cut(int dtype, int64_t stages, int64_t sums, F tiles_of) {
+    Cut best = {64, 1, false};
+    double least = 1e300;
+    for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
+        const int64_t tiles = tiles_of(c.rows, c.cols);
+        for (int parts = 1; parts <= 16; parts *= 2) {
+            if (parts > 1 && (c.tile != 64 || stages / parts < 4 || tiles * parts > 1024)) break;
+            const double rounds = (double)cdiv(tiles * parts, 256);
+            double t = (double)cdiv(stages, parts) * (rounds * c.each + c.wait) + rounds * c.edge;
+            if (parts > 1) t += 4.0 + (double)parts * (double)sums * 8.0 / 3e6;
+            if (t < least) {
+                least = t;
+                best = {c.tile, parts, false};
+            }
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped, int64_t experts,
+              bool p_rows) {
+    // Rows that a group has on average (every expert that has one), and the
+    // row tiles to expect: half a tile lost per expert.
+    int64_t groups = grouped ? (experts < rows ? experts : rows) : 1;
+    if (groups < 1) groups = 1;
+    const int64_t each = rows / groups;
+    auto tiles = [&](int64_t m, int64_t n) {
+        return (cdiv(rows, m) + (grouped ? groups / 2 : 0)) * cdiv(cols, n);
+    };
+    // Few rows and too few tiles to stream w with: 16 x 4096 with depth 4096 10 us
+    // against 15 in eight parts of 64s; but 16 x 4096 of 16 experts 45 against 43.
+    if (!p_rows && each <= 32 && groups * cdiv(cols, 64) < 256) return {each <= 16 ? 16 : 32, 1, true};
+    Cut c = best_cut(dtype, cdiv(depth, dtype == 0 ? 32 : 64), rows * cols, tiles);
+    if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
+    return c;
+}
+
+Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts) {
+    auto tiles = [&](int64_t m, int64_t n) { return cdiv(m_cols, m) * cdiv(n_cols, n) * experts; };
+    Cut c = best_cut(dtype, cdiv(rows / experts, dtype == 0 ? 32 : 64), m_cols * n_cols * experts, tiles);
+    if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
+    return c;
+}
+
+hipError_t launch_rows(int dtype, const RowsProblem &pr, bool thin, hipStream_t s) {
     if (pr.rows == 0) return hipSuccess;
-    if (dtype == 0) return launch_rows_t<float>(pr, s);
-    return dtype == 1 ? launch_rows_t<bf16>(pr, s) : launch_rows_t<f16>(pr, s);
+    if (dtype == 0) return rows_t<float>(pr, thin, s);
+    return dtype == 1 ? rows_t<bf16>(pr, thin, s) : rows_t<f16>(pr, thin, s);
 }
 hipError_t launch_grad(int dtype, const GradProblem &pr, hipStream_t s) {
-    if (dtype == 0) return launch_grad_t<float>(pr, s);
-    return dtype == 1 ? launch_grad_t<bf16>(pr, s) : launch_grad_t<f16>(pr, s);
+    if (dtype == 0) return grad_t<float>(pr, s);
+    return dtype == 1 ? grad_t<bf16>(pr, s) : grad_t<f16>(pr, s);
 }
 
 hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst,

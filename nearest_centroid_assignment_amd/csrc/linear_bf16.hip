@@ -1,16 +1,20 @@
-// linear_bf16.hip - the tiled products of linear.h for bf16 operands, which the
-// caller has laid on 16-byte boundaries.
+// linear_bf16.hip - the products of linear.h for bf16 operands, whose rows the caller has laid on
+// 4-byte boundaries (thin products take any).
 #include "linear.h"
 
 namespace kx {
 
 template <>
 hipError_t launch_rows_t<bf16>(const RowsProblem &pr, hipStream_t s) {
-    return pr.p_rows ? pick_rows<bf16, true, 16>(pr, s) : pick_rows<bf16, false, 16>(pr, s);
+    return pr.p_rows ? pick_rows<bf16, true>(pr, s) : pick_rows<bf16, false>(pr, s);
+}
+template <>
+hipError_t launch_thin_t<bf16>(const RowsProblem &pr, hipStream_t s) {
+    return pick_thin<bf16>(pr, s);
 }
 template <>
 hipError_t launch_grad_t<bf16>(const GradProblem &pr, hipStream_t s) {
-    return pick_grad<bf16, 16>(pr, s);
+    return pick_grad<bf16>(pr, s);
 }
 
 }  // namespace kx

@@ -340,8 +340,8 @@ def _weights(w, dtype, offsets, dev):
 
 
 def _misplaced(px, ldx, pw, ins):
-    """Whether x or w misses the 16-byte boundaries that 16-bit rows are read on."""
-    return ((px or 0) | (pw or 0)) % 16 != 0 or (ldx | ins) % 8 != 0
+    """Whether x or w misses the 4-byte boundaries that 16-bit rows are read on."""
+    return ((px or 0) | (pw or 0)) % 4 != 0 or (ldx | ins) % 2 != 0
 
 
 @_on_device

@@ -298,6 +298,27 @@ def test_linear_large_tiles(dtype, rows, outs, ins, counts):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,outs,ins,counts", [
+    (200, 72, 1100, None), (100, 1096, 72, None), (140, 90, 1602, None), (600, 302, 1026, None), (258, 642, 2046, None), (1300, 40, 56, None), (90, 700, 2050, None),
+    (0, 72, 1096, [100, 0, 700, 33]), (0, 1048, 136, [65, 0, 130]), (0, 33, 40, [1500, 3, 900])])
+def test_linear_split_depth(dtype, rows, outs, ins, counts):
+    """Few tiles with a long depth, in each direction: the depth is split."""
+    gu.announce(f"linear split {dtype} {rows} x {outs} x {ins} {counts}")
+    check_linear(dtype, rows, outs, ins, "silu", counts=counts, tail=0 if counts is None else 13,
+                 in_act="silu")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,outs,ins,counts", [
+    (1, 33, 4099, None), (16, 520, 2048, None), (30, 17, 1500, None), (64, 40, 4104, None), (33, 72, 31, None),
+    (0, 136, 1032, [1, 0, 16, 17, 3]), (0, 24, 2056, [30, 0, 50, 2]), (0, 50, 777, [64, 70, 3, 0])])
+def test_linear_few_rows(dtype, rows, outs, ins, counts):
+    """Few rows an expert: the depth is split over a block's waves."""
+    gu.announce(f"linear few rows {dtype} {rows} x {outs} x {ins} {counts}")
+    check_linear(dtype, rows, outs, ins, "gelu_tanh", counts=counts, tail=0 if counts is None else 5)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_linear_options(dtype):
     """Row strides on and off 16 bytes, no bias, and gradients one at a time."""
     rows, outs, ins = 70, 88, 104
