@@ -47,6 +47,30 @@ __device__ __forceinline__ void store_vec(T *p, const T (&in)[V]) {
     *reinterpret_cast<typename Unaligned<T, V>::type *>(p) = x;
 }
 
+// V values of one row, `valid` of them inside it, at any alignment.
+template <typename T, int V>
+__device__ __forceinline__ void load_row(const T *p, int valid, T (&x)[V]) {
+    if (valid >= V) {
+        load_vec(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = i < valid ? p[i] : (T)0.0f;
+    }
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_row(T *p, const float (&v)[V], int valid) {
+    T x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = (T)v[i];
+    if (valid >= V) {
+        store_vec(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (i < valid) p[i] = x[i];
+    }
+}
+
 // ------------------------------------------------------------ activations
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
 
@@ -57,28 +81,56 @@ __device__ __forceinline__ float sigmoid(float x) {
 constexpr float kGelu1 = 1.59576912160573f;   // 2 sqrt(2/pi)
 constexpr float kGelu3 = 0.0713548162726f;    // 0.044715 * 2 sqrt(2/pi)
 
-__device__ __forceinline__ float act_value(float z, int act) {
-    switch (act) {
-        case kActRelu: return z < 0.0f ? 0.0f : z;  // keeps NaN
-        case kActGelu: return z * sigmoid(z * (kGelu1 + kGelu3 * z * z));
-        case kActSilu: return z * sigmoid(z);
-        default: return z;
-    }
+template <int ACT>
+__device__ __forceinline__ float act_of(float z) {
+    if (ACT == kActRelu) return z < 0.0f ? 0.0f : z;  // keeps NaN
+    if (ACT == kActGelu) return z * sigmoid(z * (kGelu1 + kGelu3 * z * z));
+    if (ACT == kActSilu) return z * sigmoid(z);
+    return z;
 }
 // act'(z). With s = sigmoid(u(z)): (z s)' = s + z s (1 - s) u'.
-__device__ __forceinline__ float act_slope(float z, int act) {
-    switch (act) {
-        case kActRelu: return z > 0.0f ? 1.0f : 0.0f;
-        case kActGelu: {
-            const float s = sigmoid(z * (kGelu1 + kGelu3 * z * z));
-            return s + z * s * (1.0f - s) * (kGelu1 + 3.0f * kGelu3 * z * z);
-        }
-        case kActSilu: {
-            const float s = sigmoid(z);
-            return s + z * s * (1.0f - s);
-        }
-        default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float slope_of(float z) {
+    if (ACT == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
+    if (ACT == kActGelu) {
+        const float s = sigmoid(z * (kGelu1 + kGelu3 * z * z));
+        return s + z * s * (1.0f - s) * (kGelu1 + 3.0f * kGelu3 * z * z);
     }
+    if (ACT == kActSilu) {
+        const float s = sigmoid(z);
+        return s + z * s * (1.0f - s);
+    }
+    return 1.0f;
+}
+template <int ACT>
+struct ActTag {
+    static constexpr int value = ACT;
+};
+// f(tag of act): the choice is made once, around the loops that use it. (Made for
+// each value inside them, it left the products' epilogue with 2500 branches.)
+template <class F>
+__host__ __device__ __forceinline__ void with_act(int act, F f) {
+    switch (act) {
+        case kActRelu: f(ActTag<kActRelu>{}); break;
+        case kActGelu: f(ActTag<kActGelu>{}); break;
+        case kActSilu: f(ActTag<kActSilu>{}); break;
+        default: f(ActTag<kActNone>{}); break;
+    }
+}
+template <int V>
+__device__ __forceinline__ void apply_act(float (&z)[V], int act) {
+    with_act(act, [&](auto tag) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = act_of<decltype(tag)::value>(z[i]);
+    });
+}
+// z *= act'(x)
+template <typename T, int V>
+__device__ __forceinline__ void apply_slope(float (&z)[V], const T (&x)[V], int act) {
+    with_act(act, [&](auto tag) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] *= slope_of<decltype(tag)::value>((float)x[i]);
+    });
 }
 
 // ----------------------------------------------------------------- tokens

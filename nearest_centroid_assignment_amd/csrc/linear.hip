@@ -79,16 +79,24 @@ __global__ __launch_bounds__(256) void join_rows_kernel(RowsProblem pr) {
         }
     }
     const T *bias = (const T *)pr.bias, *res = (const T *)pr.residual, *in = (const T *)pr.in_pre;
+    T x[8];
+    if (bias && !tail) {
+        load_row(bias + (int64_t)expert * pr.cols + n, valid, x);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (i >= valid) break;
-        if (bias && !tail) z[i] += (float)bias[(int64_t)expert * pr.cols + n + i];
-        if (pr.pre) ((T *)pr.pre)[m * pr.ldpre + n + i] = (T)z[i];
-        z[i] = act_value(z[i], pr.act);
-        if (res && !tail) z[i] += (float)res[m * pr.ldr + n + i];
-        if (in && !tail) z[i] *= act_slope((float)in[m * pr.ldin + n + i], pr.in_act);
-        ((T *)pr.out)[m * pr.ldo + n + i] = (T)z[i];
+        for (int i = 0; i < 8; ++i) z[i] += (float)x[i];
     }
+    if (pr.pre) store_row((T *)pr.pre + m * pr.ldpre + n, z, valid);
+    apply_act(z, pr.act);
+    if (res && !tail) {
+        load_row(res + m * pr.ldr + n, valid, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += (float)x[i];
+    }
+    if (in && !tail) {
+        load_row(in + m * pr.ldin + n, valid, x);
+        apply_slope(z, x, pr.in_act);
+    }
+    store_row((T *)pr.out + m * pr.ldo + n, z, valid);
 }
 
 template <typename T>
@@ -138,10 +146,10 @@ hipError_t grad_t(const GradProblem &pr, hipStream_t s) {
 // expert e, its four waves taking every fourth row. Each column's partial sum is
 // a float32 sum in a fixed order: a wave's rows in turn, the four waves, and
 // then (slope_sum_kernel) the parts.
-template <typename T, int V>
+template <typename T, int V, int ACT>
 __global__ __launch_bounds__(256) void slope_kernel(const T *__restrict__ dy, int64_t lddy,
                                                     const T *__restrict__ pre, int64_t ldpre,
-                                                    int act, const int *__restrict__ offsets,
+                                                    const int *__restrict__ offsets,
                                                     int experts, int64_t rows, int64_t outs,
                                                     T *__restrict__ dz, int64_t lddz,
                                                     T *__restrict__ dbias,
@@ -174,12 +182,12 @@ __global__ __launch_bounds__(256) void slope_kernel(const T *__restrict__ dy, in
             const int64_t r = rr + 4 * u < r1 ? rr + 4 * u : rr;  // no condition on the loads
             if (full) {
                 load_vec(dy + r * lddy + c, y[u]);
-                if (pre) load_vec(pre + r * ldpre + c, z[u]);
+                if (ACT != kActNone) load_vec(pre + r * ldpre + c, z[u]);
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     y[u][j] = c + j < outs ? dy[r * lddy + c + j] : (T)0.0f;
-                    z[u][j] = pre && c + j < outs ? pre[r * ldpre + c + j] : (T)0.0f;
+                    z[u][j] = ACT != kActNone && c + j < outs ? pre[r * ldpre + c + j] : (T)0.0f;
                 }
             }
         }
@@ -190,7 +198,7 @@ __global__ __launch_bounds__(256) void slope_kernel(const T *__restrict__ dy, in
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 float v = (float)y[u][j];
-                if (pre) v *= act_slope((float)z[u][j], act);
+                if (ACT != kActNone) v *= slope_of<ACT>((float)z[u][j]);
                 sum[j] += v;
                 y[u][j] = (T)v;
             }
@@ -240,9 +248,11 @@ hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
     const int splits = (int)slope_splits(rows, outs, experts);
     const int64_t width = dz && lddz > outs ? lddz : outs;
     const int64_t cb = cdiv(width, 64 * V);
-    slope_kernel<T, V><<<(unsigned)(cb * splits * experts), 256, 0, s>>>(
-        (const T *)dy, lddy, act == kActNone ? nullptr : (const T *)pre, ldpre, act, offsets,
-        experts, rows, outs, (T *)dz, lddz, (T *)dbias, partial, splits, (int)cb);
+    with_act(act, [&](auto tag) {
+        slope_kernel<T, V, decltype(tag)::value><<<(unsigned)(cb * splits * experts), 256, 0, s>>>(
+            (const T *)dy, lddy, (const T *)pre, ldpre, offsets, experts, rows, outs, (T *)dz, lddz,
+            (T *)dbias, partial, splits, (int)cb);
+    });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !dbias || splits == 1) return e;
     const int64_t n = (int64_t)experts * outs;
@@ -279,15 +289,17 @@ struct TileCost {
     double each, wait, edge;
 };
 constexpr TileCost kHalf[] = {{256, 256, 256, 1.65, 0.10, 8.0},
-                              {128, 128, 128, 0.50, 0.20, 2.5},
+                              {128, 128, 128, 0.50, 0.30, 2.5},
                               {64, 64, 64, 0.13, 0.40, 1.0}};
 constexpr TileCost kFloat[] = {{128, 128, 128, 1.75, 0.10, 5.0},
                                {64, 64, 64, 0.44, 0.15, 2.0},
                                {32, 32, 64, 0.23, 0.20, 1.5}};
 
-// tiles_of(rows, cols): the number of tiles of that size; sums: values to join.
+// tiles_of(rows, cols): the number of tiles of that size; bytes: of the operands;
+// sums: values to join; setup: what a round costs more where its blocks look their
+// rows up.
 template <class F>
-Cut best_cut(int dtype, int64_t stages, int64_t sums, F tiles_of) {
+Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, double setup, F tiles_of) {
     Cut best = {64, 1, false};
     double least = 1e300;
     for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
@@ -295,7 +307,9 @@ Cut best_cut(int dtype, int64_t stages, int64_t sums, F tiles_of) {
         for (int parts = 1; parts <= 16; parts *= 2) {
             if (parts > 1 && (c.tile != 64 || stages / parts < 4 || tiles * parts > 1024)) break;
             const double rounds = (double)cdiv(tiles * parts, 256);
-            double t = (double)cdiv(stages, parts) * (rounds * c.each + c.wait) + rounds * c.edge;
+            double t = (double)cdiv(stages, parts) * (rounds * c.each + c.wait);
+            const double memory = (double)bytes / 5.5e6;
+            t = (t < memory ? memory : t) + rounds * (c.edge + setup);
             if (parts > 1) t += 4.0 + (double)parts * (double)sums * 8.0 / 3e6;
             if (t < least) {
                 least = t;
@@ -321,14 +335,19 @@ Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped
     // Few rows and too few tiles to stream w with: 16 x 4096 with depth 4096 10 us
     // against 15 in eight parts of 64s; but 16 x 4096 of 16 experts 45 against 43.
     if (!p_rows && each <= 32 && groups * cdiv(cols, 64) < 256) return {each <= 16 ? 16 : 32, 1, true};
-    Cut c = best_cut(dtype, cdiv(depth, dtype == 0 ? 32 : 64), rows * cols, tiles);
-    if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
+    const int64_t size = dtype == 0 ? 4 : 2;
+    Cut c = best_cut(dtype, cdiv(depth * size, 128), (rows + groups * cols) * depth * size, rows * cols,
+                     grouped ? 1.0 : 0.0, tiles);
+    const int64_t most = most_row_tiles(rows, 128, grouped, experts) * cdiv(cols, 128);
+    if (c.tile == 128 && dtype != 0 && most <= 256) c.tile = 129;
     return c;
 }
 
 Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts) {
     auto tiles = [&](int64_t m, int64_t n) { return cdiv(m_cols, m) * cdiv(n_cols, n) * experts; };
-    Cut c = best_cut(dtype, cdiv(rows / experts, dtype == 0 ? 32 : 64), m_cols * n_cols * experts, tiles);
+    const int64_t size = dtype == 0 ? 4 : 2;
+    Cut c = best_cut(dtype, cdiv(rows / experts * size, 128), rows * (m_cols + n_cols) * size,
+                     m_cols * n_cols * experts, 0.0, tiles);
     if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
     return c;
 }
