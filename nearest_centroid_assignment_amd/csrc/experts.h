@@ -39,6 +39,20 @@ __device__ __forceinline__ void load_vec(const T *p, T (&out)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) out[i] = x[i];
 }
+// The same past the caches' replacement order: for what this kernel touches once.
+template <typename T, int V>
+__device__ __forceinline__ void load_once(const T *p, T (&out)[V]) {
+    const auto x = __builtin_nontemporal_load(reinterpret_cast<const typename Unaligned<T, V>::type *>(p));
+#pragma unroll
+    for (int i = 0; i < V; ++i) out[i] = x[i];
+}
+template <typename T, int V>
+__device__ __forceinline__ void store_once(T *p, const T (&in)[V]) {
+    typename Unaligned<T, V>::type x;
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = in[i];
+    __builtin_nontemporal_store(x, reinterpret_cast<typename Unaligned<T, V>::type *>(p));
+}
 template <typename T, int V>
 __device__ __forceinline__ void store_vec(T *p, const T (&in)[V]) {
     typename Unaligned<T, V>::type x;

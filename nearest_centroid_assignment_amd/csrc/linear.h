@@ -223,8 +223,11 @@ struct Shape {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
     static constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     static constexpr int kStage = (BM + BN) * kRow;
-    // Tiles of one block a compute unit fetch what their epilogue reads ahead of it.
-    static constexpr bool kTouch = BM * BN * (int)sizeof(T) >= 1 << 17;
+    // The largest tiles belong to products whose outputs, residuals and input
+    // activations pass through once and would push the operands out of L2:
+    // 32768 x 4096 with depth 2048 and an input activation 597 -> 513 us,
+    // 8192^3 dx 883 -> 793 us.
+    static constexpr bool kOnce = BM * BN >= 1 << 16;
     typedef T type;
     typedef Tile<T, PMC, BN, NW> TileP;
     typedef Tile<T, QMC, BM, NW> TileQ;
@@ -290,16 +293,14 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((loads & 15) | (7 << 4) | ((loads >> 4) << 14));
 }
 
-constexpr int kSoon = 6;  // stages
-
 // acc[tm][tn] += the tile's product over the whole depth. NS stages in LDS and two
 // half-stages of fragments in registers: while one half is multiplied, the next
 // is read, and in the second half of a stage, whose buffer every wave has read
-// by then, the stage NS later moves in. `soon` runs a few stages before the end.
-template <class S, class F>
+// by then, the stage NS later moves in.
+template <class S>
 __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
                                         typename S::TileQ &tq, int depth, int wave, int lane,
-                                        f32x4 (&acc)[S::TM][S::TN], F soon) {
+                                        f32x4 (&acc)[S::TM][S::TN]) {
     typename S::ReadP rp;
     typename S::ReadQ rq;
     rp.init((wave % S::WN) * (S::BN / S::WN), lane);
@@ -341,12 +342,8 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
     };
     // Stage it + NS moves in during stage it: the ragged one, if any, is the last.
     const int plain = ragged ? stages - S::NS - 1 : stages;
-    const int tell = stages > kSoon ? stages - kSoon : 0;
     int it = 0;
-    for (; it < plain; ++it) {
-        if (it == tell) soon();
-        stage(false);
-    }
+    for (; it < plain; ++it) stage(false);
 #pragma unroll 1
     for (; it < stages; ++it) stage(true);
     __builtin_amdgcn_s_waitcnt(0);
@@ -418,6 +415,17 @@ struct Groups {
         return r;
     }
 };
+
+template <bool ONCE, typename T>
+__device__ __forceinline__ void store_whole(T *p, const float (&v)[8]) {
+    T x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (T)v[i];
+    if (ONCE)
+        store_once(p, x);
+    else
+        store_vec(p, x);
+}
 
 // Hands the wave's tile to `use(row, col, values, aux)`, eight consecutive
 // columns at a time: 16 rows at a time go through LDS (each wave's own part of the
@@ -493,7 +501,7 @@ __device__ __forceinline__ void walk(int id, int tiles_m, int tiles_n, int gm, i
 template <class S>
 __global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
     typedef typename S::type T;
-    __shared__ __align__(1024) char memory[S::NS * S::kStage + (S::kTouch ? 256 : 0)];
+    __shared__ __align__(1024) char memory[S::NS * S::kStage];
     lds_char *smem = (lds_char *)memory;
     const RowsProblem &pr = a.pr;
     const int lane = threadIdx.x & 63;
@@ -544,33 +552,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
         typename S::TileQ tq;
         tp.init(p, pr.ldp, S::p_mc ? pr.p_cols - n0 : (int64_t)cols - n0, len, wave, lane);
         tq.init(q, pr.ldq, gr.hi - m0, len, wave, lane);
-        // The residual's or the input activation's tile: one word of each of its lines
-        // goes to a spare corner of LDS while the last stages are multiplied, so that
-        // the epilogue finds it in L2. Read there first, every compute unit would ask for
-        // its tile at the same time with nothing to multiply meanwhile
-        // (32768 x 4096 with depth 2048: 683 us against 518 without the read).
-        product<S>(smem, tp, tq, len, wave, lane, acc, [&]() {
-            if constexpr (S::kTouch) {
-                const T *extra = (const T *)(pr.residual ? pr.residual : pr.in_pre);
-                if (!extra || pr.splits > 1) return;
-                const int64_t ldx = pr.residual ? pr.ldr : pr.ldin;
-                const int valid = gr.hi - m0 < S::BM ? gr.hi - m0 : S::BM;
-                const int width = cols - n0 < S::BN ? cols - n0 : S::BN;
-                const uint64_t at = (uint64_t)(extra + (int64_t)m0 * ldx + n0);
-                const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-                    (void *)(((uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(at >> 32)) << 32) |
-                             (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)at)),
-                    0, (int)(((valid - 1) * ldx + width) * (int)sizeof(T)) & ~3, 0x00020000);
-                constexpr int kLines = S::BN * (int)sizeof(T) / 128;
-#pragma unroll
-                for (int i = 0; i < S::BM * kLines / 64 / S::NW; ++i) {
-                    const int l = (wave * (S::BM * kLines / 64 / S::NW) + i) * 64 + lane;
-                    const uint32_t o = (uint32_t)((l / kLines) * (int)ldx * (int)sizeof(T) + l % kLines * 128) & ~3u;
-                    __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                        rsrc, (lds_void *)(smem + S::NS * S::kStage), 4, (int)o, 0, 0, 0);
-                }
-            }
-        });
+        product<S>(smem, tp, tq, len, wave, lane, acc);
     }
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
@@ -612,7 +594,11 @@ __global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
                 smem, wave, lane, acc,
                 [&](int row, int col) {
                     Aux x;
-                    if (EXTRA) load_vec(extra + (int64_t)(wm + row) * ldx + wn + col, x.v);
+                    const T *at = extra + (int64_t)(wm + row) * ldx + wn + col;
+                    if (EXTRA && S::kOnce)
+                        load_once(at, x.v);
+                    else if (EXTRA)
+                        load_vec(at, x.v);
                     return x;
                 },
                 [&](int row, int col, float (&z)[8], const Aux &x) {
@@ -625,14 +611,14 @@ __global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) z[i] += b[i];
-                        if (pre) store_row(pre + m * pr.ldpre + n, z, 8);
+                        if (pre) store_whole<S::kOnce>(pre + m * pr.ldpre + n, z);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             z[i] = act_of<ACT>(z[i]);
                             if (EXTRA) z[i] += (float)x.v[i];
                         }
                     }
-                    store_row(out + m * pr.ldo + n, z, 8);
+                    store_whole<S::kOnce>(out + m * pr.ldo + n, z);
                 });
         };
         if (S::p_mc) {
@@ -720,22 +706,29 @@ __global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
             hi - lo, wave, lane);
     tq.init((const char *)pr.dz + ((int64_t)lo * pr.lddz + m0) * sizeof(T), pr.lddz,
             pr.dz_cols - m0, hi - lo, wave, lane);
-    product<S>(smem, tp, tq, hi - lo, wave, lane, acc, []() {});
+    product<S>(smem, tp, tq, hi - lo, wave, lane, acc);
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     T *out = (T *)pr.out + (int64_t)e * mc * nc;
     float *partial = pr.partial + ((int64_t)part * pr.experts + e) * mc * nc;
     struct None {};
-    by_rows<S, None>(
-        smem, wave, lane, acc, [](int, int) { return None{}; },
-        [&](int row, int col, float (&z)[8], const None &) {
-            const int m = wm + row, n = wn + col;
-            if (m >= mc || n >= nc) return;
-            if (pr.splits > 1)
-                store_row(partial + (int64_t)m * nc + n, z, nc - n);
-            else
-                store_row(out + (int64_t)m * nc + n, z, nc - n);
-        });
+    auto write = [&](auto *to, bool whole) {
+        by_rows<S, None>(
+            smem, wave, lane, acc, [](int, int) { return None{}; },
+            [&](int row, int col, float (&z)[8], const None &) {
+                const int m = wm + row, n = wn + col;
+                if (whole)
+                    store_whole<S::kOnce>(to + (int64_t)m * nc + n, z);
+                else if (m < mc && n < nc)
+                    store_row(to + (int64_t)m * nc + n, z, nc - n);
+            });
+    };
+    if (pr.splits > 1)
+        write(partial, false);
+    else if (m0 + S::BM <= mc && n0 + S::BN <= nc)
+        write(out, true);
+    else
+        write(out, false);
 }
 
 template <class S>

@@ -305,7 +305,7 @@ Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, double setu
     for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
         const int64_t tiles = tiles_of(c.rows, c.cols);
         for (int parts = 1; parts <= 16; parts *= 2) {
-            if (parts > 1 && (c.tile != 64 || stages / parts < 4 || tiles * parts > 1024)) break;
+            if (parts > 1 && (stages / parts < 4 || tiles * parts > 1024)) break;
             const double rounds = (double)cdiv(tiles * parts, 256);
             double t = (double)cdiv(stages, parts) * (rounds * c.each + c.wait);
             const double memory = (double)bytes / 5.5e6;
