@@ -370,11 +370,12 @@ hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t c
     return hipGetLastError();
 }
 
-// Parts of an expert's rows: about 4096 blocks in all, 64 rows a part at least.
+// Parts of an expert's rows: about 4096 blocks in all, 16 rows a part at least (one
+// group of loads a wave).
 int64_t slope_splits(int64_t rows, int64_t outs, int64_t experts) {
     const int64_t blocks = cdiv(outs, 256) * experts;
     int64_t n = 4096 / blocks;
-    const int64_t most = rows / experts / 64;
+    const int64_t most = rows / experts / 16;
     n = n > most ? most : n;
     return n < 1 ? 1 : n > 128 ? 128 : n;
 }

@@ -1,11 +1,13 @@
 // tokens.hip - pairs of (token, slot) sorted by expert, the token rows gathered
 // in that order, the experts' rows summed back with weights, and gradients.
 //
-// The sort is the counting sort of the centroid update (a stable rank per tile
-// of 1024 pairs and that tile's histogram, launch_rank_hist), then a prefix over
-// the tiles per expert, a prefix over the experts, and a scatter that writes
-// both the order and its inverse. At most kSmallPairs pairs are sorted by one
-// block in one launch.
+// The sort is a stable counting sort. A wave ranks its 64 pairs among themselves
+// by ballots over the bits of the expert numbers, leaves its count of each expert in
+// LDS, and the ranks of a whole block follow from a prefix over its waves; then a
+// prefix over blocks and experts gives the places. At most kSmallPairs pairs are
+// sorted by one block in one launch; up to kPlaceTiles blocks of 1024 pairs by two
+// launches (the second sums the blocks' counts in every block: 65536 x 2 pairs of
+// 1024 experts 23 us in four launches, 11 in two); more by four.
 //
 // The row kernels give one wave (or, with few tokens, one block) to a token: its
 // own row is read once, and the rows of its `top` pairs are reached through the
@@ -19,7 +21,59 @@ namespace {
 constexpr int kTile = (int)km::kSortTileRows;
 constexpr int kSmallTiles = 4;                     // tiles that the one-block sort takes
 constexpr int kSmallPairs = kSmallTiles * 1024;
-constexpr int kSmallExperts = 4096;
+constexpr int kWaveCounts = 65536;                 // counts of (wave, expert) in LDS: 128 KB
+constexpr int kPlaceTiles = 128, kPlaceExperts = 4096;
+
+// Rank of the lane's expert among the wave's lanes with the same one and a lower
+// index, and how many have it; both 0 where expert < 0. `bits`: of the largest expert.
+__device__ __forceinline__ void wave_rank(int expert, int bits, int &rank, int &count) {
+    const int lane = threadIdx.x & 63;
+    unsigned long long same = __ballot(expert >= 0);
+    for (int b = 0; b < bits; ++b) {
+        const bool set = (expert >> b) & 1;
+        const unsigned long long with = __ballot(set);
+        same &= set ? with : ~with;
+    }
+    rank = expert < 0 ? 0 : __popcll(same & ((1ull << lane) - 1ull));
+    count = expert < 0 ? 0 : __popcll(same);
+}
+__device__ __forceinline__ int bits_of(int64_t experts) { return 64 - __clzll((unsigned long long)experts); }
+
+__device__ __forceinline__ int expert_of(const int64_t *ids, int64_t i, int64_t pairs, int64_t experts) {
+    if (i >= pairs) return -1;
+    const int64_t e = ids[i];
+    return e >= 0 && e < experts ? (int)e : -1;
+}
+
+// One block per tile of 1024 pairs: rank of every pair in its tile, and the
+// tile's count of every expert.
+__global__ __launch_bounds__(1024) void plan_rank_kernel(const int64_t *__restrict__ ids,
+                                                         int64_t pairs, int experts,
+                                                         int *__restrict__ tile_hist,
+                                                         unsigned short *__restrict__ rank_out) {
+    extern __shared__ unsigned short counts[];  // 16 x experts, by wave
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int64_t i = (int64_t)blockIdx.x * 1024 + tid;
+    const int expert = expert_of(ids, i, pairs, experts);
+    for (int j = tid; j < 16 * experts; j += 1024) counts[j] = 0;
+    int rank, count;
+    wave_rank(expert, bits_of(experts), rank, count);
+    __syncthreads();
+    if (expert >= 0 && rank == 0) counts[wave * experts + expert] = (unsigned short)count;
+    __syncthreads();
+    for (int e = tid; e < experts; e += 1024) {
+        int run = 0;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+            const int c = counts[w * experts + e];
+            counts[w * experts + e] = (unsigned short)run;
+            run += c;
+        }
+        tile_hist[(int64_t)blockIdx.x * experts + e] = run;
+    }
+    __syncthreads();
+    if (expert >= 0) rank_out[i] = (unsigned short)(rank + counts[wave * experts + expert]);
+}
 
 // Per expert (a thread): the exclusive prefix of its tile counts, in place, and
 // its size. Loads of 16 tiles are in flight before the first store.
@@ -75,6 +129,56 @@ __global__ __launch_bounds__(1024) void plan_scan_kernel(const int *__restrict__
     if (threadIdx.x == 0) offsets[experts] = carry;
 }
 
+// One block per tile: every expert's count in all tiles and in the tiles before
+// this one, a prefix over the experts, and the tile's pairs put in their places.
+// The sums are the same in every block; block 0 writes the offsets.
+__global__ __launch_bounds__(1024) void plan_place_kernel(
+    const int64_t *__restrict__ ids, int64_t pairs, int experts, int tiles,
+    const int *__restrict__ tile_hist, const unsigned short *__restrict__ rank,
+    int *__restrict__ order, int *__restrict__ place, int *__restrict__ offsets) {
+    __shared__ int base[kPlaceExperts];
+    const int tid = threadIdx.x, b = blockIdx.x;
+    int carry = 0;
+    for (int e0 = 0; e0 < experts; e0 += 1024) {
+        const int e = e0 + tid;
+        int before = 0, all = 0;
+        if (e < experts) {
+            constexpr int U = 32;  // counts in flight
+            for (int t0 = 0; t0 < tiles; t0 += U) {
+                int v[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    v[u] = tile_hist[(int64_t)(t0 + u < tiles ? t0 + u : tiles - 1) * experts + e];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int c = t0 + u < tiles ? v[u] : 0;
+                    before += t0 + u < b ? c : 0;
+                    all += c;
+                }
+            }
+        }
+        int total;
+        const int at = carry + block_scan(all, total);
+        if (e < experts) {
+            base[e] = at + before;
+            if (b == 0) offsets[e] = at;
+        }
+        carry += total;
+    }
+    if (b == 0 && tid == 0) offsets[experts] = carry;
+    __syncthreads();
+    const int64_t i = (int64_t)b * 1024 + tid;
+    if (i >= pairs) return;
+    const int expert = expert_of(ids, i, pairs, experts);
+    int at = -1;
+    if (expert >= 0) {
+        at = base[expert] + rank[i];
+        order[at] = (int)i;
+    }
+    place[i] = at;
+    if (i >= carry) order[i] = -1;
+}
+
 __global__ __launch_bounds__(256) void plan_scatter_kernel(
     const int64_t *__restrict__ ids, int64_t pairs, int64_t experts,
     const int *__restrict__ tile_prefix, const unsigned short *__restrict__ rank,
@@ -91,61 +195,44 @@ __global__ __launch_bounds__(256) void plan_scatter_kernel(
     if (i >= offsets[experts]) order[i] = -1;
 }
 
-// The whole sort in one block. Waves rank their own 64 pairs (the lanes with an
-// equal expert, found by ballots) and take turns, in pair order, to add the
-// expert's count so far; the counts become starts by one block scan.
+// The whole sort in one block, `tiles` rounds of 1024 pairs.
 __global__ __launch_bounds__(1024) void plan_small_kernel(const int64_t *__restrict__ ids, int pairs,
                                                           int experts, int *__restrict__ order,
                                                           int *__restrict__ place,
                                                           int *__restrict__ offsets) {
-    __shared__ int table[kSmallExperts];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    for (int e = tid; e < experts; e += 1024) table[e] = 0;
-    int expert[kSmallTiles], rank[kSmallTiles];
+    extern __shared__ unsigned short counts[];  // waves x experts
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int waves = (pairs + 63) / 64;  // of pairs, 16 to a round
+    for (int j = tid; j < waves * experts; j += 1024) counts[j] = 0;
+    int expert[kSmallTiles], rank[kSmallTiles], count[kSmallTiles];
+#pragma unroll
+    for (int t = 0; t < kSmallTiles; ++t) expert[t] = expert_of(ids, t * 1024 + tid, pairs, experts);
 #pragma unroll
     for (int t = 0; t < kSmallTiles; ++t) {
-        const int i = t * 1024 + tid;
-        expert[t] = -1;
-        rank[t] = 0;
-        if (i < pairs) {
-            const int64_t e = ids[i];
-            if (e >= 0 && e < experts) expert[t] = (int)e;
-        }
+        rank[t] = count[t] = 0;
+        if (t * 1024 < pairs) wave_rank(expert[t], bits_of(experts), rank[t], count[t]);
     }
+    __syncthreads();
 #pragma unroll
-    for (int t = 0; t < kSmallTiles; ++t) {
-        if (t * 1024 >= pairs) break;
-        unsigned long long todo = __ballot(expert[t] >= 0);
-        int count = 0;
-        while (todo) {
-            const int e = __builtin_amdgcn_readlane(expert[t], __builtin_ctzll(todo));
-            const unsigned long long same = __ballot(expert[t] == e);
-            if (expert[t] == e) {
-                rank[t] = __popcll(same & ((1ull << lane) - 1ull));
-                count = __popcll(same);
-            }
-            todo &= ~same;
-        }
-        const int left = pairs - t * 1024;
-        const int waves = left < 1024 ? (left + 63) / 64 : 16;
-        for (int w = 0; w < waves; ++w) {
-            __syncthreads();
-            if (wave == w && expert[t] >= 0) {
-                const int before = table[expert[t]];
-                if (rank[t] == count - 1) table[expert[t]] = before + count;
-                rank[t] += before;
-            }
-        }
-    }
+    for (int t = 0; t < kSmallTiles; ++t)
+        if (expert[t] >= 0 && rank[t] == 0)
+            counts[(t * 16 + wave) * experts + expert[t]] = (unsigned short)count[t];
     __syncthreads();
     int carry = 0;
     for (int e0 = 0; e0 < experts; e0 += 1024) {
         const int e = e0 + tid;
+        int all = 0;
+        if (e < experts)
+            for (int w = 0; w < waves; ++w) all += counts[w * experts + e];
         int total;
-        const int at = carry + block_scan(e < experts ? table[e] : 0, total);
+        int at = carry + block_scan(all, total);
         if (e < experts) {
-            table[e] = at;
             offsets[e] = at;
+            for (int w = 0; w < waves; ++w) {  // (places are below 4096)
+                const int c = counts[w * experts + e];
+                counts[w * experts + e] = (unsigned short)at;
+                at += c;
+            }
         }
         carry += total;
     }
@@ -157,7 +244,7 @@ __global__ __launch_bounds__(1024) void plan_small_kernel(const int64_t *__restr
         if (i >= pairs) break;
         int at = -1;
         if (expert[t] >= 0) {
-            at = table[expert[t]] + rank[t];
+            at = counts[(t * 16 + wave) * experts + expert[t]] + rank[t];
             order[at] = i;
         }
         place[i] = at;
@@ -175,19 +262,25 @@ constexpr int vec() {
     return 16 / (int)sizeof(T);
 }
 
-template <typename T, int V>
+template <bool ONCE, typename T, int V>
 __device__ __forceinline__ void load_part(const T *p, int64_t left, T (&v)[V]) {
     if (left >= V) {
-        load_vec(p, v);
+        if (ONCE)
+            load_once(p, v);
+        else
+            load_vec(p, v);
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = j < left ? p[j] : (T)0.0f;
     }
 }
-template <typename T, int V>
+template <bool ONCE, typename T, int V>
 __device__ __forceinline__ void store_part(T *p, int64_t left, const T (&v)[V]) {
     if (left >= V) {
-        store_vec(p, v);
+        if (ONCE)
+            store_once(p, v);
+        else
+            store_vec(p, v);
     } else {
 #pragma unroll
         for (int j = 0; j < V; ++j)
@@ -213,11 +306,11 @@ __device__ __forceinline__ void clear_empty(const int *order, int64_t t, int64_t
     for (int64_t s = t * top; s < t * top + top; ++s) {
         if (order[s] >= 0) continue;
         for (int64_t c = (threadIdx.x % NT) * V; c < width; c += NT * V)
-            store_part<T, V>(rows + s * ld + c, width - c, zero);
+            store_part<false, T, V>(rows + s * ld + c, width - c, zero);
     }
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool ONCE>
 __global__ __launch_bounds__(256) void dispatch_kernel(const T *__restrict__ x, int64_t ldx,
                                                        int64_t tokens, int64_t top, int64_t width,
                                                        const int *__restrict__ order,
@@ -229,16 +322,16 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const T *__restrict__ x, 
     const int64_t pairs = tokens * top;
     for (int64_t c = (threadIdx.x % NT) * V; c < width; c += NT * V) {
         T v[V];
-        load_part<T, V>(x + t * ldx + c, width - c, v);
+        load_part<false, T, V>(x + t * ldx + c, width - c, v);
         for (int64_t s = 0; s < top; ++s) {
             const int64_t p = place[t * top + s];
-            if (p >= 0 && p < pairs) store_part<T, V>(xs + p * ldxs + c, width - c, v);
+            if (p >= 0 && p < pairs) store_part<ONCE, T, V>(xs + p * ldxs + c, width - c, v);
         }
     }
     clear_empty<T, NT>(order, t, top, xs, ldxs, width);
 }
 
-template <typename T, int NT, bool WEIGHTS>
+template <typename T, int NT, bool ONCE, bool WEIGHTS>
 __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ ys, int64_t ldys,
                                                       const float *__restrict__ weights,
                                                       int64_t tokens, int64_t top, int64_t width,
@@ -258,14 +351,14 @@ __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ ys, 
             if (p < 0 || p >= pairs) continue;
             const float w = WEIGHTS ? weights[t * top + s] : 1.0f;
             T v[V];
-            load_part<T, V>(ys + p * ldys + c, width - c, v);
+            load_part<ONCE, T, V>(ys + p * ldys + c, width - c, v);
 #pragma unroll
             for (int j = 0; j < V; ++j) sum[j] += w * (float)v[j];
         }
         T r[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) r[j] = (T)sum[j];
-        store_part<T, V>(y + t * ldy + c, width - c, r);
+        store_part<false, T, V>(y + t * ldy + c, width - c, r);
     }
 }
 
@@ -284,7 +377,7 @@ __device__ __forceinline__ float token_sum(float v) {
     return v;
 }
 
-template <typename T, int NT>
+template <typename T, int NT, bool ONCE>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
     const T *__restrict__ dy, int64_t lddy, const T *__restrict__ ys, int64_t ldys,
     const float *__restrict__ weights, int64_t tokens, int64_t top, int64_t width,
@@ -303,16 +396,16 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
 #pragma unroll 2
             for (int64_t c = (threadIdx.x % NT) * V; c < width; c += NT * V) {
                 T g[V], v[V];
-                load_part<T, V>(dy + t * lddy + c, width - c, g);
+                load_part<false, T, V>(dy + t * lddy + c, width - c, g);
                 if (dweights) {
-                    load_part<T, V>(ys + p * ldys + c, width - c, v);
+                    load_part<ONCE, T, V>(ys + p * ldys + c, width - c, v);
 #pragma unroll
                     for (int j = 0; j < V; ++j) dot += (float)g[j] * (float)v[j];
                 }
                 if (dys) {
 #pragma unroll
                     for (int j = 0; j < V; ++j) g[j] = (T)(w * (float)g[j]);
-                    store_part<T, V>(dys + p * lddys + c, width - c, g);
+                    store_part<ONCE, T, V>(dys + p * lddys + c, width - c, g);
                 }
             }
         }
@@ -324,66 +417,85 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
     if (dys) clear_empty<T, NT>(order, t, top, dys, lddys, width);
 }
 
-// A wave a token once the tokens fill the chip, a block before that.
-inline bool wave_per_token(int64_t tokens) { return tokens >= 4096; }
+// A wave a token once the tokens fill the chip, a block before that. Rows of the
+// pairs that are more than the 256 MB of the memory-side cache pass the caches by,
+// where they are whole lines of 128 bytes: 131072 x 2048 bf16 rows, dispatch 159 ->
+// 123 us (its stores), combine 167 -> 138 (its loads), its gradient 280 -> 234 (both);
+// 15009 x 1001 f16 rows (30 MB), the gradient 18 -> 25.
+struct How {
+    bool wave, once;
+};
+template <typename T>
+How how(int64_t tokens, int64_t top, int64_t width, int64_t ld) {
+    const bool lines = width * (int64_t)sizeof(T) % 128 == 0 && ld * (int64_t)sizeof(T) % 128 == 0;
+    return {tokens >= 4096, lines && tokens * top * width * (int64_t)sizeof(T) > 256 << 20};
+}
+
+#define KX_ROWS(kernel, ...)                                                                    \
+    do {                                                                                        \
+        if (h.wave && h.once)                                                                   \
+            kernel<T, 64, true __VA_ARGS__><<<(unsigned)cdiv(tokens, 4), 256, 0, s>>> KX_ARGS;  \
+        else if (h.wave)                                                                        \
+            kernel<T, 64, false __VA_ARGS__><<<(unsigned)cdiv(tokens, 4), 256, 0, s>>> KX_ARGS; \
+        else                                                                                    \
+            kernel<T, 256, false __VA_ARGS__><<<(unsigned)tokens, 256, 0, s>>> KX_ARGS;         \
+        return hipGetLastError();                                                               \
+    } while (0)
 
 template <typename T>
 struct Rows {
     static hipError_t dispatch(const void *x, int64_t ldx, int64_t tokens, int64_t top,
                                int64_t width, const int *order, const int *place, void *xs,
                                int64_t ldxs, hipStream_t s) {
-        if (wave_per_token(tokens))
-            dispatch_kernel<T, 64><<<(unsigned)cdiv(tokens, 4), 256, 0, s>>>(
-                (const T *)x, ldx, tokens, top, width, order, place, (T *)xs, ldxs);
-        else
-            dispatch_kernel<T, 256><<<(unsigned)tokens, 256, 0, s>>>(
-                (const T *)x, ldx, tokens, top, width, order, place, (T *)xs, ldxs);
-        return hipGetLastError();
-    }
-    template <bool W>
-    static hipError_t combine_w(const void *ys, int64_t ldys, const float *weights, int64_t tokens,
-                                int64_t top, int64_t width, const int *place, void *y, int64_t ldy,
-                                hipStream_t s) {
-        if (wave_per_token(tokens))
-            combine_kernel<T, 64, W><<<(unsigned)cdiv(tokens, 4), 256, 0, s>>>(
-                (const T *)ys, ldys, weights, tokens, top, width, place, (T *)y, ldy);
-        else
-            combine_kernel<T, 256, W><<<(unsigned)tokens, 256, 0, s>>>(
-                (const T *)ys, ldys, weights, tokens, top, width, place, (T *)y, ldy);
-        return hipGetLastError();
+        const How h = how<T>(tokens, top, width, ldxs);
+#define KX_ARGS ((const T *)x, ldx, tokens, top, width, order, place, (T *)xs, ldxs)
+        KX_ROWS(dispatch_kernel);
+#undef KX_ARGS
     }
     static hipError_t combine(const void *ys, int64_t ldys, const float *weights, int64_t tokens,
                               int64_t top, int64_t width, const int *place, void *y, int64_t ldy,
                               hipStream_t s) {
-        return weights ? combine_w<true>(ys, ldys, weights, tokens, top, width, place, y, ldy, s)
-                       : combine_w<false>(ys, ldys, weights, tokens, top, width, place, y, ldy, s);
+        const How h = how<T>(tokens, top, width, ldys);
+#define KX_ARGS ((const T *)ys, ldys, weights, tokens, top, width, place, (T *)y, ldy)
+        if (weights)
+            KX_ROWS(combine_kernel, , true);
+        else
+            KX_ROWS(combine_kernel, , false);
+#undef KX_ARGS
     }
     static hipError_t backward(const void *dy, int64_t lddy, const void *ys, int64_t ldys,
                                const float *weights, int64_t tokens, int64_t top, int64_t width,
                                const int *order, const int *place, void *dys, int64_t lddys,
                                float *dweights, hipStream_t s) {
-        if (wave_per_token(tokens))
-            combine_backward_kernel<T, 64><<<(unsigned)cdiv(tokens, 4), 256, 0, s>>>(
-                (const T *)dy, lddy, (const T *)ys, ldys, weights, tokens, top, width, order, place,
-                (T *)dys, lddys, dweights);
-        else
-            combine_backward_kernel<T, 256><<<(unsigned)tokens, 256, 0, s>>>(
-                (const T *)dy, lddy, (const T *)ys, ldys, weights, tokens, top, width, order, place,
-                (T *)dys, lddys, dweights);
-        return hipGetLastError();
+        const How h = how<T>(tokens, top, width, dys ? lddys : ldys);
+#define KX_ARGS                                                                               \
+    ((const T *)dy, lddy, (const T *)ys, ldys, weights, tokens, top, width, order, place, (T *)dys, \
+     lddys, dweights)
+        KX_ROWS(combine_backward_kernel);
+#undef KX_ARGS
     }
 };
 
 }  // namespace
 
 bool plan_is_small(int64_t pairs, int64_t experts) {
-    return pairs <= kSmallPairs && experts <= kSmallExperts;
+    return pairs <= kSmallPairs && cdiv(pairs, 64) * experts <= kWaveCounts;
 }
 
 hipError_t launch_plan(const int64_t *ids, int64_t pairs, int64_t experts, int *order, int *place,
                        int *offsets, const PlanScratch &ws, hipStream_t s) {
     if (plan_is_small(pairs, experts)) {
-        plan_small_kernel<<<1, 1024, 0, s>>>(ids, (int)pairs, (int)experts, order, place, offsets);
+        const size_t lds = (size_t)cdiv(pairs, 64) * experts * sizeof(unsigned short);
+        plan_small_kernel<<<1, 1024, lds, s>>>(ids, (int)pairs, (int)experts, order, place, offsets);
+        return hipGetLastError();
+    }
+    if (ws.tiles <= kPlaceTiles && experts <= kPlaceExperts) {
+        const size_t lds = (size_t)16 * experts * sizeof(unsigned short);
+        plan_rank_kernel<<<(unsigned)ws.tiles, 1024, lds, s>>>(ids, pairs, (int)experts,
+                                                               ws.tile_hist, ws.rank);
+        plan_place_kernel<<<(unsigned)ws.tiles, 1024, 0, s>>>(ids, pairs, (int)experts, (int)ws.tiles,
+                                                              ws.tile_hist, ws.rank, order, place,
+                                                              offsets);
         return hipGetLastError();
     }
     km::UpdateScratch us = {};
