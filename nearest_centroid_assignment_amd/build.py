@@ -21,6 +21,9 @@ SOURCES = ["api.hip", "assign.hip", "update.hip", "fit.hip", "kmeanspp.hip",
 CALIB_NAME = "libkm_calib.so"
 CALIB_PATH = os.path.join(HERE, CALIB_NAME)
 CALIB_SOURCES = ["calib.hip"]
+# Marshalling of torch tensors for experts.py: a Python extension module.
+TORCH_MODULE_PATH = os.path.join(HERE, "_experts_torch.so")
+TORCH_MODULE_SOURCE = "experts_torch.cpp"
 
 # Per-source additional flags. The assignment kernel uses LLVM's iterative
 # occupancy-driven scheduler (measured, same-box A/B on the large shapes:
@@ -61,7 +64,7 @@ def _run(cmd, cwd=None, verbose=False):
     if msgs and (verbose or proc.returncode):
         print("\n".join(msgs), file=sys.stderr)
     if proc.returncode != 0:
-        raise RuntimeError(f"hipcc failed with exit code {proc.returncode}: {' '.join(cmd)}")
+        raise RuntimeError(f"the compiler failed with exit code {proc.returncode}: {' '.join(cmd)}")
 
 
 def _compile(sources, out_path, verbose: bool, save_temps: bool, extra_flags=None) -> str:
@@ -94,11 +97,37 @@ def _compile(sources, out_path, verbose: bool, save_temps: bool, extra_flags=Non
     return out_path
 
 
+def build_torch_module(verbose: bool = False) -> str:
+    """Compile the module that marshals torch tensors to the experts' entry
+    points (host code against torch's C++ headers; it links torch alone)."""
+    import sysconfig
+
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        raise RuntimeError("g++ not found")
+    out_tmp = TORCH_MODULE_PATH + ".tmp"
+    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+          "-DUSE_ROCM=1", *(f"-isystem{p}" for p in include_paths()), "-isystem/opt/rocm/include",
+          f"-isystem{sysconfig.get_paths()['include']}", os.path.join(CSRC, TORCH_MODULE_SOURCE),
+          *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+          "-lc10_hip", "-o", out_tmp], verbose=verbose)
+    os.replace(out_tmp, TORCH_MODULE_PATH)
+    return TORCH_MODULE_PATH
+
+
 def build(verbose: bool = False, save_temps: bool = False) -> str:
-    """Compile the k-means library and the calibration library; returns the
-    path of the k-means library."""
-    _compile(CALIB_SOURCES, CALIB_PATH, verbose, save_temps)
-    return _compile(SOURCES, LIB_PATH, verbose, save_temps, EXTRA_FLAGS)
+    """Compile the k-means library, the calibration library and the torch
+    module; returns the path of the k-means library."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    with ThreadPoolExecutor(max_workers=1) as pool:
+        module = pool.submit(build_torch_module, verbose)
+        _compile(CALIB_SOURCES, CALIB_PATH, verbose, save_temps)
+        path = _compile(SOURCES, LIB_PATH, verbose, save_temps, EXTRA_FLAGS)
+        module.result()
+    return path
 
 
 if __name__ == "__main__":

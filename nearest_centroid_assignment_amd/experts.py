@@ -19,11 +19,14 @@ returns; gradients are explicit calls, given what the forward call returned.
 from __future__ import annotations
 
 import ctypes
+import functools
+import importlib.util
+import os
 from typing import NamedTuple
 
 import torch
 
-from .binding import KMeansError, _check, _record, _side_stream, _stream, lib as _kmeans_lib
+from .binding import HERE, KMeansError, _check, _record, _side_stream, _stream, lib as _kmeans_lib
 
 ACTS = {"none": 0, "relu": 1, "gelu_tanh": 2, "silu": 3}
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -34,13 +37,29 @@ __all__ = ["KMeansError", "Plan", "plan", "dispatch", "dispatch_backward", "comb
            "adamw_moments"]
 
 _lib = None
+_native = None  # the torch module, once lib() has loaded it
+
+
+def _load_native(L, names):
+    """The module that takes the ordinary calls natively (csrc/experts_torch.cpp),
+    bound to the library's entry points."""
+    path = os.path.join(HERE, "_experts_torch.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
+                           "`python -m nearest_centroid_assignment_amd.build`")
+    spec = importlib.util.spec_from_file_location("_experts_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names})
+    return module
 
 
 def lib() -> ctypes.CDLL:
     """The HIP library with the experts' entry points declared."""
-    global _lib
+    global _lib, _native
     if _lib is None:
         L = _kmeans_lib()
+        names = []
         i64, vp, sz, i32, f64 = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int,
                                  ctypes.c_double)
         for name, res, args in (
@@ -65,14 +84,24 @@ def lib() -> ctypes.CDLL:
         ):
             f = getattr(L, name)
             f.restype, f.argtypes = res, args
+            names.append(name)
+        _native = _load_native(L, names)
         _lib = L
     return _lib
 
 
+def _module():
+    lib()
+    return _native
+
+
 # ------------------------------------------------------------- marshalling
 #
-# The smallest calls cost more on the host than on the GPU, so the checks below
-# ask a tensor for as little as they can and word a refusal only once there is one.
+# The smallest calls cost more on the host than on the GPU. A call with fresh
+# outputs on the current stream is therefore first offered to the native module,
+# which takes it or, where anything about it is unusual, leaves it to the Python
+# below (None): other streams, given outputs and workspaces, empty matrices, and
+# everything that is to be refused. Both end in the same C entry point.
 
 
 def _refuse(t, dtype, shape, dev, name):
@@ -161,18 +190,17 @@ def _mark(stream, dev, *tensors):
 
 def _on_device(fn):
     """Run fn with its first tensor's device current: the library launches there."""
-    import functools
 
     @functools.wraps(fn)
-    def call(*args, **kwargs):
-        t = args[0] if args else None
-        if isinstance(t, (list, tuple)):
-            t = t[0] if t else None
-        dev = t.get_device() if isinstance(t, torch.Tensor) else -1
-        if dev < 0 or dev == torch._C._cuda_getDevice():
-            return fn(*args, **kwargs)
+    def call(t, *args, **kwargs):
+        first = t
+        if isinstance(first, (list, tuple)):
+            first = first[0] if first else None
+        dev = first.get_device() if isinstance(first, torch.Tensor) else -1
+        if dev < 0 or dev == torch.cuda.current_device():
+            return fn(t, *args, **kwargs)
         with torch.cuda.device(dev):
-            return fn(*args, **kwargs)
+            return fn(t, *args, **kwargs)
 
     return call
 
@@ -190,10 +218,18 @@ class Plan(NamedTuple):
     offsets: torch.Tensor
 
 
-@_on_device
 def plan(ids, experts, workspace=None, stream=None) -> Plan:
     """Sort the (tokens, top) or (tokens,) int64 expert numbers; numbers
     outside [0, experts) are dropped. Stable: an expert's pairs stay in order."""
+    if workspace is None and stream is None:
+        got = (_native or _module()).plan(ids, experts)
+        if got is not None:
+            return Plan(*got)
+    return _plan(ids, experts, workspace, stream)
+
+
+@_on_device
+def _plan(ids, experts, workspace, stream):
     if not isinstance(ids, torch.Tensor):
         raise TypeError("ids must be a torch.Tensor")
     if not ids.is_cuda:
@@ -223,10 +259,18 @@ def _sizes(plan):
     return tokens, top, tokens * top
 
 
-@_on_device
 def dispatch(x, plan, out=None, stream=None):
     """The rows of x (tokens, width) in sorted order: (tokens * top, width).
     Places without a pair get zero rows."""
+    if out is None and stream is None:
+        got = (_native or _module()).dispatch(x, plan)
+        if got is not None:
+            return got
+    return _dispatch(x, plan, out, stream)
+
+
+@_on_device
+def _dispatch(x, plan, out, stream):
     dev, code = _first(x, "x", 2)
     tokens, top, pairs = _sizes(plan)
     width, dtype = x.shape[1], x.dtype
@@ -246,9 +290,17 @@ def dispatch(x, plan, out=None, stream=None):
     return out
 
 
-@_on_device
 def dispatch_backward(dxs, plan, out=None, stream=None):
     """Gradient of dispatch: each token's sum of its pairs' rows of dxs."""
+    if out is None and stream is None:
+        got = (_native or _module()).dispatch_backward(dxs, plan)
+        if got is not None:
+            return got
+    return _dispatch_backward(dxs, plan, out, stream)
+
+
+@_on_device
+def _dispatch_backward(dxs, plan, out, stream):
     dev, code = _first(dxs, "dxs", 2)
     tokens, top, pairs = _sizes(plan)
     width, dtype = dxs.shape[1], dxs.dtype
@@ -267,10 +319,18 @@ def dispatch_backward(dxs, plan, out=None, stream=None):
     return out
 
 
-@_on_device
 def combine(ys, weights, plan, out=None, stream=None):
     """Each token's weighted sum of its pairs' rows of ys (tokens * top, width);
     weights (tokens, top) float32."""
+    if out is None and stream is None:
+        got = (_native or _module()).combine(ys, weights, plan)
+        if got is not None:
+            return got
+    return _combine(ys, weights, plan, out, stream)
+
+
+@_on_device
+def _combine(ys, weights, plan, out, stream):
     dev, code = _first(ys, "ys", 2)
     tokens, top, pairs = _sizes(plan)
     width, dtype = ys.shape[1], ys.dtype
@@ -290,9 +350,17 @@ def combine(ys, weights, plan, out=None, stream=None):
     return out
 
 
-@_on_device
 def combine_backward(dy, ys, weights, plan, need_dys=True, need_dweights=True, stream=None):
     """Gradients of combine: (dys, dweights), None for the one not needed."""
+    if need_dys and need_dweights and stream is None:
+        got = (_native or _module()).combine_backward(dy, ys, weights, plan)
+        if got is not None:
+            return got
+    return _combine_backward(dy, ys, weights, plan, need_dys, need_dweights, stream)
+
+
+@_on_device
+def _combine_backward(dy, ys, weights, plan, need_dys, need_dweights, stream):
     dev, code = _first(dy, "dy", 2)
     tokens, top, pairs = _sizes(plan)
     width, dtype = dy.shape[1], dy.dtype
@@ -344,7 +412,6 @@ def _misplaced(px, ldx, pw, ins):
     return ((px or 0) | (pw or 0)) % 4 != 0 or (ldx | ins) % 2 != 0
 
 
-@_on_device
 def linear(x, w, bias=None, residual=None, act="none", offsets=None, save_pre=False, out=None,
            workspace=None, stream=None):
     """act(x w^T + bias) + residual for x (rows, ins).
@@ -354,6 +421,16 @@ def linear(x, w, bias=None, residual=None, act="none", offsets=None, save_pre=Fa
     offsets[e] to offsets[e + 1], and rows past the last expert's become zero.
     act: "none", "relu", "gelu_tanh", "silu". With ``save_pre`` returns (out,
     x w^T + bias), the latter for linear_backward."""
+    if out is None and workspace is None and stream is None:
+        got = (_native or _module()).linear(x, w, bias, residual, ACTS.get(act, -1), offsets,
+                                            save_pre)
+        if got is not None:
+            return got
+    return _linear(x, w, bias, residual, act, offsets, save_pre, out, workspace, stream)
+
+
+@_on_device
+def _linear(x, w, bias, residual, act, offsets, save_pre, out, workspace, stream):
     dev, code = _first(x, "x", 2)
     dtype, act_code = x.dtype, _act_code(act)
     pw, outs, ins, experts, pf = _weights(w, dtype, offsets, dev)
@@ -380,13 +457,25 @@ def linear(x, w, bias=None, residual=None, act="none", offsets=None, save_pre=Fa
     return (out, pre) if save_pre else out
 
 
-@_on_device
 def linear_backward(dy, x, w, pre=None, act="none", offsets=None, in_pre=None, in_act="none",
                     need_dx=True, need_dw=True, need_dbias=True, workspace=None, stream=None):
     """Gradients of linear: (dx, dw, dbias), None for those not needed; the
     residual's is dy itself. ``pre`` is what linear returned with save_pre (not
     needed without an activation). With ``in_pre`` (rows, ins), dx is multiplied by
     in_act'(in_pre): given the layer before's pre, dx is that layer's dz."""
+    if workspace is None and stream is None:
+        got = (_native or _module()).linear_backward(
+            dy, x, w, pre, ACTS.get(act, -1), offsets, in_pre, ACTS.get(in_act, -1), need_dx,
+            need_dw, need_dbias)
+        if got is not None:
+            return got
+    return _linear_backward(dy, x, w, pre, act, offsets, in_pre, in_act, need_dx, need_dw,
+                            need_dbias, workspace, stream)
+
+
+@_on_device
+def _linear_backward(dy, x, w, pre, act, offsets, in_pre, in_act, need_dx, need_dw, need_dbias,
+                     workspace, stream):
     dev, code = _first(dy, "dy", 2)
     dtype, act_code, in_code = dy.dtype, _act_code(act), _act_code(in_act, "in_act")
     pw, outs, ins, experts, pf = _weights(w, dtype, offsets, dev)
@@ -456,7 +545,6 @@ def _pointers(tensors, dtype, params, dev, name):
     return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
 
 
-@_on_device
 def adamw_step(params, grads, m, v, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=1,
                m_scale=None, v_scale=None, copies=None, grad_scale=None, stream=None):
     """One AdamW step, in place, over lists of tensors (one dtype for the
@@ -464,6 +552,17 @@ def adamw_step(params, grads, m, v, lr, betas=(0.9, 0.999), eps=1e-8, weight_dec
     as made by adamw_state. ``copies``: bfloat16 tensors that receive the new
     parameters. ``grad_scale``: a float32 GPU tensor of one element that
     multiplies the gradients (clipping, loss scaling). step counts from 1."""
+    if stream is None and (_native or _module()).adamw_step(
+            params, grads, m, v, lr, betas[0], betas[1], eps, weight_decay, step, m_scale, v_scale,
+            copies, grad_scale):
+        return
+    _adamw_step(params, grads, m, v, lr, betas, eps, weight_decay, step, m_scale, v_scale, copies,
+                grad_scale, stream)
+
+
+@_on_device
+def _adamw_step(params, grads, m, v, lr, betas, eps, weight_decay, step, m_scale, v_scale, copies,
+                grad_scale, stream):
     if not params:
         return
     if len(grads) != len(params):
@@ -494,9 +593,13 @@ def adamw_step(params, grads, m, v, lr, betas=(0.9, 0.999), eps=1e-8, weight_dec
         _mark(stream, dev, *params, *grads, *(copies or ()), m, v, m_scale, v_scale, grad_scale)
 
 
-@_on_device
 def adamw_moments(m, v, m_scale, v_scale, stream=None):
     """The float32 values of 8-bit moments: (m, v)."""
+    return _adamw_moments(m, v, m_scale, v_scale, stream)
+
+
+@_on_device
+def _adamw_moments(m, v, m_scale, v_scale, stream):
     if not isinstance(m, torch.Tensor) or not m.is_cuda:
         raise TypeError("m must be a GPU tensor")
     total, dev = m.numel(), m.get_device()
