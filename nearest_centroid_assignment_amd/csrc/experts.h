@@ -220,9 +220,10 @@ inline int64_t most_row_tiles(int64_t rows, int64_t bm, bool grouped, int64_t ex
     return rows / bm + (experts + 1 < rows ? experts + 1 : rows);
 }
 
-// dtype: 0 float, 1 bf16, 2 f16. False when the launch grid would not fit.
-bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, int experts);
-bool grad_grid_ok(int dtype, int64_t m_cols, int64_t n_cols, int experts);
+// dtype: 0 float, 1 bf16, 2 f16. False when a launch's grid would not fit.
+bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped,
+                  int64_t experts, bool p_rows);
+bool grad_grid_ok(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts);
 hipError_t launch_rows(int dtype, const RowsProblem &pr, bool thin, hipStream_t s);
 hipError_t launch_grad(int dtype, const GradProblem &pr, hipStream_t s);
 

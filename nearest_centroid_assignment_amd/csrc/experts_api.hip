@@ -94,11 +94,16 @@ bool linear_shape_ok(int64_t rows, int64_t outs, int64_t ins, int64_t experts) {
     return rows >= 0 && rows <= kMaxRows && outs >= 1 && outs <= kMaxWidth && ins >= 1 &&
            ins <= kMaxWidth && experts >= 1 && experts <= kMaxExperts;
 }
-bool linear_grid_ok(int dtype, int64_t rows, int64_t outs, int64_t ins, int64_t experts) {
-    return kx::rows_grid_ok(dtype, rows, outs, ins, (int)experts) &&
-           kx::rows_grid_ok(dtype, rows, ins, outs, (int)experts) &&
-           kx::grad_grid_ok(dtype, outs, ins, (int)experts) &&
-           cdiv(outs, 256) * experts * 256 * 2 <= kMaxGridThreads;
+bool linear_grid_ok(int dtype, int op, int64_t rows, int64_t outs, int64_t ins, bool grouped,
+                    int64_t experts) {
+    // The padded copies take a thread for every eight values.
+    if (dtype != EXPERTS_F32 && (rows * cdiv(ins, 8) + 256 > kMaxGridThreads ||
+                                 experts * outs * cdiv(ins, 8) + 256 > kMaxGridThreads))
+        return false;
+    if (op == 0) return kx::rows_grid_ok(dtype, rows, outs, ins, grouped, experts, false);
+    return kx::rows_grid_ok(dtype, rows, ins, outs, grouped, experts, true) &&
+           kx::grad_grid_ok(dtype, rows, outs, ins, experts) &&
+           cdiv(outs + 8, 256) * experts * kx::slope_splits(rows, outs, experts) <= kMaxGridThreads / 512;
 }
 int64_t pad8(int64_t n) { return cdiv(n, 8) * 8; }
 bool ld_ok(const void *p, int64_t ld, int64_t len) {
@@ -282,7 +287,7 @@ int experts_combine_backward(const void *dy, int64_t lddy, const void *ys, int64
 size_t experts_linear_workspace_bytes(int64_t rows, int64_t outs, int64_t ins, int64_t experts,
                                       int dtype, int op, int unaligned) {
     if (!linear_shape_ok(rows, outs, ins, experts) || !dtype_ok(dtype) || op < 0 || op > 1 ||
-        !linear_grid_ok(dtype, rows, outs, ins, experts))
+        !linear_grid_ok(dtype, op, rows, outs, ins, true, experts))
         return 0;
     // Without offsets a single expert may be cut differently; both fit.
     const bool pads = dtype != EXPERTS_F32 && (unaligned || ins % 2 != 0);
@@ -298,7 +303,7 @@ int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,
                    size_t workspace_bytes, void *stream) {
     if (!dtype_ok(dtype) || !act_ok(act)) return KM_ERR_OP;
     if (!linear_shape_ok(rows, outs, ins, experts) || (!offsets && experts != 1) ||
-        !linear_grid_ok(dtype, rows, outs, ins, experts))
+        !linear_grid_ok(dtype, 0, rows, outs, ins, offsets != nullptr, experts))
         return KM_ERR_SHAPE;
     if (!w || (rows > 0 && (!x || !out))) return KM_ERR_NULL;
     if (!ld_ok(x, ldx, ins) || !ld_ok(out, ldo, outs) || !ld_ok(residual, ldr, outs) ||
@@ -367,7 +372,7 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
                             size_t workspace_bytes, void *stream) {
     if (!dtype_ok(dtype) || !act_ok(act) || !act_ok(in_act)) return KM_ERR_OP;
     if (!linear_shape_ok(rows, outs, ins, experts) || (!offsets && experts != 1) ||
-        !linear_grid_ok(dtype, rows, outs, ins, experts))
+        !linear_grid_ok(dtype, 1, rows, outs, ins, offsets != nullptr, experts))
         return KM_ERR_SHAPE;
     if (!dx && !dw && !dbias) return KM_ERR_NULL;
     if (rows > 0 && (!dy || (act != EXPERTS_ACT_NONE && !pre) || (dx && !w) || (dw && !x)))

@@ -181,8 +181,12 @@ __global__ __launch_bounds__(256) void slope_kernel(const T *__restrict__ dy, in
         for (int u = 0; u < kRows; ++u) {
             const int64_t r = rr + 4 * u < r1 ? rr + 4 * u : rr;  // no condition on the loads
             if (full) {
-                load_vec(dy + r * lddy + c, y[u]);
-                if (ACT != kActNone) load_vec(pre + r * ldpre + c, z[u]);
+                if (ACT != kActNone) {  // the products read dz, not these
+                    load_once(dy + r * lddy + c, y[u]);
+                    load_once(pre + r * ldpre + c, z[u]);
+                } else {
+                    load_vec(dy + r * lddy + c, y[u]);
+                }
             } else {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -262,19 +266,6 @@ hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
 
 }  // namespace
 
-// The most blocks that any cut launches: 16 x 16 with 512 threads, or 32 x 64 with
-// 256 (a depth is split only where there are at most 1024 blocks).
-bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, int experts) {
-    (void)dtype;
-    (void)depth;
-    const int64_t thin = (rows / 16 + experts + 1) * cdiv(cols, 16);
-    return thin <= kMaxGridThreads / 512;
-}
-bool grad_grid_ok(int dtype, int64_t m_cols, int64_t n_cols, int experts) {
-    (void)dtype;
-    return cdiv(m_cols, 32) * cdiv(n_cols, 64) * experts <= kMaxGridThreads / 512;
-}
-
 namespace {
 
 // What a cut costs, in microseconds, from measured runs: a tile's stage costs
@@ -350,6 +341,20 @@ Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t e
                      m_cols * n_cols * experts, 0.0, tiles);
     if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
     return c;
+}
+
+bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped,
+                  int64_t experts, bool p_rows) {
+    const Cut c = rows_plan(dtype, rows, cols, depth, grouped, experts, p_rows);
+    const int64_t m = c.tile == 129 ? 128 : c.tile, n = c.thin ? 16 : c.tile == 32 ? 64 : m;
+    const int64_t blocks = most_row_tiles(rows, m, grouped, experts) * cdiv(cols, n) * c.splits;
+    return blocks + 8 <= kMaxGridThreads / 512 && cdiv(rows * cdiv(cols, 8), 256) <= kMaxGridThreads / 256;
+}
+bool grad_grid_ok(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts) {
+    const Cut c = grad_plan(dtype, rows, m_cols, n_cols, experts);
+    const int64_t m = c.tile == 129 ? 128 : c.tile, n = c.tile == 32 ? 64 : m;
+    const int64_t blocks = cdiv(m_cols, m) * cdiv(n_cols, n) * experts * c.splits;
+    return blocks + 128 <= kMaxGridThreads / 512;
 }
 
 hipError_t launch_rows(int dtype, const RowsProblem &pr, bool thin, hipStream_t s) {
