@@ -262,11 +262,11 @@ int experts_combine_backward(const void *dy, int64_t lddy, const void *ys, int64
                              int64_t lddys, float *dweights, void *stream) {
     if (!dtype_ok(dtype)) return KM_ERR_OP;
     if (!rows_shape_ok(tokens, top, width) || lddy < width || (dweights && ldys < width) ||
-        (dys && lddys < width) || tokens * 256 > kMaxGridThreads)
+        (dys && lddys < width) || tokens * top * 64 > kMaxGridThreads - 256)
         return KM_ERR_SHAPE;
     if (!dys && !dweights) return KM_ERR_NULL;
     if (tokens == 0) return KM_OK;
-    if (!dy || !place || (dys && (!weights || !order)) || (dweights && !ys)) return KM_ERR_NULL;
+    if (!dy || !place || !order || (dys && !weights) || (dweights && !ys)) return KM_ERR_NULL;
     const size_t b = size_of(dtype);
     if (!aligned(dy, b) || !aligned(ys, b) || !aligned(weights, 4) || !aligned(dys, b) ||
         !aligned(dweights, 4) || !aligned(order, 4) || !aligned(place, 4))
