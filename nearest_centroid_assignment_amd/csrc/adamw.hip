@@ -293,7 +293,7 @@ hipError_t launch_adamw(void *const *params, const void *const *grads, void *con
             Tensor &t = b.t[b.count];
             t.p = (char *)params[i] + done * psize;
             t.g = (const char *)grads[i] + done * gsize;
-            t.copy = copies ? (bf16 *)copies[i] + done : nullptr;
+            t.copy = copies && copies[i] != params[i] ? (bf16 *)copies[i] + done : nullptr;
             t.n = n;
             t.at = at + done;
             b.first[b.count + 1] = b.first[b.count] + (int)cdiv(n, kChunk);

@@ -513,8 +513,10 @@ int experts_adamw_step(void *const *params, const void *const *grads, void *cons
         if (!params[i] || !grads[i] || (copies && !copies[i])) return KM_ERR_NULL;
         if (!aligned(params[i], ps) || !aligned(grads[i], gs) || (copies && !aligned(copies[i], 2)))
             return KM_ERR_ALIGN;
+        // A bfloat16 parameter may be its own copy.
+        const bool same = copies && copies[i] == params[i] && param_dtype == EXPERTS_BF16;
         const Span own[] = {{params[i], 1, 0, numels[i], ps},
-                            {copies ? copies[i] : nullptr, 1, 0, numels[i], 2}};
+                            {copies && !same ? copies[i] : nullptr, 1, 0, numels[i], 2}};
         const Span in[] = {{grads[i], 1, 0, numels[i], gs}, state[0], state[1], state[2], state[3],
                            scale[0]};
         if (int rc = check_alias(own, 2, in, 6)) return rc;

@@ -466,6 +466,19 @@ def test_adamw(bits, pt, gt, copies):
             assert np.array_equal(np32(state["m"]), m) and np.array_equal(np32(state["v"]), v)
 
 
+def test_adamw_own_copy():
+    """A bfloat16 parameter given as its own copy is updated once; a float32 one's
+    memory is refused."""
+    p = [randn(1, 1000, dtype=torch.bfloat16)]
+    q, g = [p[0].clone()], [randn(2, 1000)]
+    for params, copies in ((p, p), (q, None)):
+        experts.adamw_step(params, g, lr=0.1, copies=copies, **experts.adamw_state(params))
+    assert torch.equal(p[0], q[0])
+    r = [randn(1, 1000)]
+    with pytest.raises(binding.KMeansError):
+        experts.adamw_step(r, g, lr=0.1, copies=[r[0].view(torch.bfloat16)[:1000]], **experts.adamw_state(r))
+
+
 def test_adamw_8_bit_codes():
     """A second moment above zero never gets code 0, a block of zeros stays
     zeros, and a NaN or an infinity marks its block and no other."""
