@@ -8,9 +8,9 @@
 //   by column (MC)  rows of k, the output dimension contiguous (w of dx; x and
 //                   dz of dw)
 // so no operand is ever transposed in memory. A stage is 128 bytes of k per
-// output row or column (64 16-bit values, 32 floats), moved from global memory
-// straight into LDS (buffer_load ... lds); whatever lies outside an operand is
-// dropped by the buffer's range check and reads as zero.
+// output row or column (64 16-bit values, 32 floats; 64 bytes in product_in_turns),
+// moved from global memory straight into LDS (buffer_load ... lds); whatever lies
+// outside an operand is dropped by the buffer's range check and reads as zero.
 //
 // The matrix instruction's row operand is P and its column operand Q: a lane
 // then holds four consecutive output columns of one output row, so bias,
@@ -39,7 +39,6 @@ typedef __attribute__((address_space(3))) void lds_void;
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
-constexpr int kRow = 128;                // bytes of k per stage
 constexpr uint32_t kNowhere = 1u << 31;  // an offset past every buffer (records < 2^31)
 
 template <typename T>
@@ -71,13 +70,22 @@ struct Frag<float> {
     }
 };
 
+// Rows of 64 bytes: the key of row r. Four rows share a line of 64 banks, so rows r,
+// r + 4, r + 8, r + 12 get different keys, in an order that also keeps apart the two
+// chunks that a read's groups of 16 lanes mix (rows 0-3 and 12-15 of one, 4-11 of
+// the next).
+__device__ __forceinline__ int kc_key64(int r) {
+    const int n = (r >> 2) & 3;
+    return ((n & 1) << 1) ^ ((n >> 1) * 3);
+}
+
 // One operand's stage: R output rows (or columns) x 128 bytes of k, moved by
 // NW waves with 16 bytes a lane and instruction. Rows may start on any 4 bytes:
 // the buffer's range check works in 4-byte words, so a chunk that leaves the
 // operand is cut there. A chunk that leaves its row reads the next row's start,
 // which in an MC operand only reaches columns that are not stored; a KC row that
 // ends inside a chunk has its last stage moved in 4-byte pieces (`ragged`).
-template <typename T, bool MC, int R, int NW>
+template <typename T, bool MC, int R, int NW, int kRow>
 struct Tile {
     static constexpr int kSize = (int)sizeof(T);
     static constexpr int kBytes = R * kRow;
@@ -97,7 +105,8 @@ struct Tile {
     }
     // Byte q of the stage in LDS: its byte of the row in memory (KC).
     static __device__ __forceinline__ int kc_byte(int q) {
-        return ((((q & (kRow - 1)) >> 4) ^ ((q >> 8) & 7)) << 4) | (q & 15);
+        const int key = kRow == 128 ? (q >> 8) & 7 : kc_key64(q / 64);
+        return ((((q & (kRow - 1)) >> 4) ^ key) << 4) | (q & 15);
     }
     static __device__ __forceinline__ int lds_byte(int wave, int lane, int i) {
         return ((wave * kIssues + i) * 64 + lane) * 16;
@@ -123,7 +132,7 @@ struct Tile {
                 const int src = (((c >> 4) ^ swizzle(k)) << 4) | (c & 15);
                 off[i] = src < extent ? (uint32_t)(k * ld + src) : kNowhere;
             } else {
-                off[i] = (q >> 7) * ld + kc_byte(q);
+                off[i] = q / kRow * ld + kc_byte(q);
             }
         }
         kc[0] = kc_byte(lds_byte(wave, lane, 0));
@@ -152,7 +161,7 @@ struct Tile {
 #pragma unroll 1
             for (int i = 0; i < kIssues * 4; ++i) {
                 const int q = (wave * kIssues * 4 + i) * 256 + lane * 4, k = kc_byte(q);
-                const uint32_t o = k < left ? (uint32_t)((q >> 7) * ld + k) : kNowhere;
+                const uint32_t o = k < left ? (uint32_t)(q / kRow * ld + k) : kNowhere;
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + i * 256), 4, (int)o,
                                                          0, 0, 0);
             }
@@ -171,7 +180,7 @@ struct Tile {
 };
 
 // Fragment reads of one operand: `first` = the wave's first output row/column.
-template <typename T, bool MC, int R, int N>
+template <typename T, bool MC, int R, int N, int kRow>
 struct Reader {
     typedef typename Frag<T>::type frag;
     typedef __attribute__((address_space(3))) const frag lds_frag;
@@ -182,7 +191,9 @@ struct Reader {
         const int i = lane & 15, g = lane >> 4;
         if (!MC) {
 #pragma unroll
-            for (int s = 0; s < 2; ++s) at[s] = (first + i) * kRow + (((4 * s + g) ^ (i >> 1)) << 4);
+            for (int s = 0; s < 2; ++s)
+                at[s] = (first + i) * kRow +
+                        ((kRow == 128 ? (4 * s + g) ^ (i >> 1) : g ^ kc_key64(i)) << 4);
         } else {
 #pragma unroll
             for (int t = 0; t < N; ++t) {
@@ -218,21 +229,21 @@ struct Reader {
     }
 };
 
-template <typename T, bool PMC, bool QMC, int BM_, int BN_, int WM_, int WN_, int NS_>
+template <typename T, bool PMC, bool QMC, int BM_, int BN_, int WM_, int WN_, int NS_, int ROW = 128>
 struct Shape {
-    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+    static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, kRow = ROW;
     static constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
-    static constexpr int kStage = (BM + BN) * kRow;
+    static constexpr int kStage = (BM + BN) * ROW;
     // The largest tiles belong to products whose outputs, residuals and input
     // activations pass through once and would push the operands out of L2:
     // 32768 x 4096 with depth 2048 and an input activation 597 -> 513 us,
     // 8192^3 dx 883 -> 793 us.
     static constexpr bool kOnce = BM * BN >= 1 << 16;
     typedef T type;
-    typedef Tile<T, PMC, BN, NW> TileP;
-    typedef Tile<T, QMC, BM, NW> TileQ;
-    typedef Reader<T, PMC, BN, TN> ReadP;
-    typedef Reader<T, QMC, BM, TM> ReadQ;
+    typedef Tile<T, PMC, BN, NW, ROW> TileP;
+    typedef Tile<T, QMC, BM, NW, ROW> TileQ;
+    typedef Reader<T, PMC, BN, TN, ROW> ReadP;
+    typedef Reader<T, QMC, BM, TM, ROW> ReadQ;
     static constexpr bool p_mc = PMC, q_mc = QMC;
 };
 
@@ -247,7 +258,7 @@ __device__ __forceinline__ void read_half(const typename S::ReadP &rp, const typ
 #pragma unroll
     for (int t = 0; t < S::TN; ++t) f.p[t] = rp.read(stage, t, s);
 #pragma unroll
-    for (int t = 0; t < S::TM; ++t) f.q[t] = rq.read(stage + S::BN * kRow, t, s);
+    for (int t = 0; t < S::TM; ++t) f.q[t] = rq.read(stage + S::BN * S::kRow, t, s);
 }
 template <class S>
 __device__ __forceinline__ void multiply(const Frags<S> &f, f32x4 (&acc)[S::TM][S::TN]) {
@@ -293,6 +304,73 @@ __device__ __forceinline__ void wait_loads() {
     __builtin_amdgcn_s_waitcnt((loads & 15) | (7 << 4) | ((loads >> 4) << 14));
 }
 
+// The product of the largest tiles, whose compute unit holds one block of eight
+// waves, two to a SIMD. Stages are 64 bytes of k, four in LDS. A wave alternates
+// between reading a stage's fragments and multiplying them, and the second four waves
+// run one phase behind the first four: on every SIMD one wave multiplies without a
+// pause while the other reads, moves the stage three later in and waits for the next
+// one. A barrier ends each phase.
+// 8192^3 bf16, against `product` with two stages of 128 bytes: 9 % fewer cycles (the
+// matrix units busy 73 % of them, before 67 %), but 1.5 % less time, 813 us, since the
+// clock falls to 1.76 GHz from 1.87: at this rate the chip's power sets the pace (a
+// loop of nothing but these matrix instructions reaches 2.1 PFLOP/s). Shorter
+// products gain more (17 experts, 32768 x 4096 with depth 2048, 658 -> 625 us). dw,
+// both of whose operands are read by column, has 8192^3 2 % and 8192 x 2048 with depth
+// 8192 6 % slower this way, 17 experts 2 % faster: it keeps `product`.
+template <class S>
+__device__ __forceinline__ void product_in_turns(lds_char *smem, typename S::TileP &tp,
+                                                 typename S::TileQ &tq, int depth, int wave,
+                                                 int lane, f32x4 (&acc)[S::TM][S::TN]) {
+    static_assert(S::NS == 4 && S::kRow == 64 && S::NW == 8, "four short stages, eight waves");
+    typename S::ReadP rp;
+    typename S::ReadQ rq;
+    rp.init((wave % S::WN) * (S::BN / S::WN), lane);
+    rq.init((wave / S::WN) * (S::BM / S::WM), lane);
+    const int stages = __builtin_amdgcn_readfirstlane((depth + S::TileP::kDepth - 1) / S::TileP::kDepth);
+    if (stages == 0) return;
+    constexpr int kMoves = S::TileP::kIssues + S::TileQ::kIssues;
+    const bool ragged = tp.ragged() || tq.ragged();
+    auto meet = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        tp.issue(smem + i * S::kStage, wave, lane, true);
+        tq.issue(smem + i * S::kStage + S::BN * S::kRow, wave, lane, true);
+    }
+    wait_loads<2 * kMoves>();
+    meet();
+    if (wave >= 4) meet();  // one phase behind
+    Frags<S> f;
+    int at = 0;
+    auto stage = [&](bool last) {
+        lds_char *cur = smem + at * S::kStage, *free = smem + ((at + 3) & 3) * S::kStage;
+        read_half<S>(rp, rq, cur, 0, f);
+        // Its last readers, the waves behind, were done a phase ago.
+        tp.issue(free, wave, lane, last);
+        tq.issue(free + S::BN * S::kRow, wave, lane, last);
+        wait_loads<2 * kMoves>();  // the next stage has landed; the fragments are here
+        meet();
+        __builtin_amdgcn_s_setprio(1);
+        multiply<S>(f, acc);
+        __builtin_amdgcn_s_setprio(0);
+        meet();
+        at = (at + 1) & 3;
+    };
+    const int plain = ragged ? stages - 4 : stages;  // stage it + 3 moves in during stage it
+    int it = 0;
+    for (; it < plain; ++it) stage(false);
+#pragma unroll 1
+    for (; it < stages; ++it) stage(true);
+    if (wave < 4) meet();
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();  // the stages' memory is free
+}
+
 // acc[tm][tn] += the tile's product over the whole depth. NS stages in LDS and two
 // half-stages of fragments in registers: while one half is multiplied, the next
 // is read, and in the second half of a stage, whose buffer every wave has read
@@ -312,7 +390,7 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
 #pragma unroll
     for (int i = 0; i < S::NS; ++i) {
         tp.issue(smem + i * S::kStage, wave, lane, true);
-        tq.issue(smem + i * S::kStage + S::BN * kRow, wave, lane, true);
+        tq.issue(smem + i * S::kStage + S::BN * S::kRow, wave, lane, true);
     }
     wait_loads<(S::NS - 1) * kMoves>();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -335,7 +413,7 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         read_half<S>(rp, rq, nxt, 0, f[0]);
         tp.issue(cur, wave, lane, last);
-        tq.issue(cur + S::BN * kRow, wave, lane, last);
+        tq.issue(cur + S::BN * S::kRow, wave, lane, last);
         multiply<S>(f[1], acc);
         if (!last) spread<S>(true);
         cur = nxt;
@@ -348,6 +426,16 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
     for (; it < stages; ++it) stage(true);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();  // the stages' memory is free
+}
+
+template <class S>
+__device__ __forceinline__ void run_product(lds_char *smem, typename S::TileP &tp,
+                                            typename S::TileQ &tq, int depth, int wave, int lane,
+                                            f32x4 (&acc)[S::TM][S::TN]) {
+    if constexpr (S::kRow == 64)
+        product_in_turns<S>(smem, tp, tq, depth, wave, lane, acc);
+    else
+        product<S>(smem, tp, tq, depth, wave, lane, acc);
 }
 
 // Block b of a grid of `total` tiles: XCD b % 8 takes pieces of `piece`
@@ -552,7 +640,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
         typename S::TileQ tq;
         tp.init(p, pr.ldp, S::p_mc ? pr.p_cols - n0 : (int64_t)cols - n0, len, wave, lane);
         tq.init(q, pr.ldq, gr.hi - m0, len, wave, lane);
-        product<S>(smem, tp, tq, len, wave, lane, acc);
+        run_product<S>(smem, tp, tq, len, wave, lane, acc);
     }
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
@@ -706,7 +794,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
             hi - lo, wave, lane);
     tq.init((const char *)pr.dz + ((int64_t)lo * pr.lddz + m0) * sizeof(T), pr.lddz,
             pr.dz_cols - m0, hi - lo, wave, lane);
-    product<S>(smem, tp, tq, hi - lo, wave, lane, acc);
+    run_product<S>(smem, tp, tq, hi - lo, wave, lane, acc);
     const int wm = m0 + (wave / S::WN) * (S::BM / S::WM);
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     T *out = (T *)pr.out + (int64_t)e * mc * nc;
@@ -753,7 +841,7 @@ hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
 template <typename T, bool PMC>
 hipError_t pick_rows(const RowsProblem &pr, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (pr.tile == 256) return run_rows<Shape<T, PMC, false, 256, 256, 2, 4, 2>>(pr, s);
+        if (pr.tile == 256) return run_rows<Shape<T, PMC, false, 256, 256, 2, 4, 4, 64>>(pr, s);
         if (pr.tile == 129) return run_rows<Shape<T, PMC, false, 128, 128, 2, 4, 3>>(pr, s);
     } else {
         if (pr.tile == 32) return run_rows<Shape<T, PMC, false, 32, 64, 2, 2, 2>>(pr, s);
