@@ -232,16 +232,24 @@ __global__ __launch_bounds__(256) void slope_kernel(const T *__restrict__ dy, in
     }
 }
 
+// 64 columns a block; each of its four waves adds a quarter of the parts.
 template <typename T>
 __global__ __launch_bounds__(256) void slope_sum_kernel(const float *__restrict__ partial,
                                                         int splits, int64_t n,
                                                         T *__restrict__ dbias) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
+    __shared__ float quarter[4][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+    const int per = (splits + 3) / 4, end = (wave + 1) * per < splits ? (wave + 1) * per : splits;
     float v = 0.0f;
+    if (i < n) {
 #pragma unroll 8
-    for (int s = 0; s < splits; ++s) v += partial[s * n + i];
-    dbias[i] = (T)v;
+        for (int s = wave * per; s < end; ++s) v += partial[s * n + i];
+    }
+    quarter[wave][lane] = v;
+    __syncthreads();
+    if (wave == 0 && i < n)
+        dbias[i] = (T)((quarter[0][lane] + quarter[1][lane]) + (quarter[2][lane] + quarter[3][lane]));
 }
 
 template <typename T>
@@ -260,7 +268,7 @@ hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !dbias || splits == 1) return e;
     const int64_t n = (int64_t)experts * outs;
-    slope_sum_kernel<T><<<(unsigned)cdiv(n, 256), 256, 0, s>>>(partial, splits, n, (T *)dbias);
+    slope_sum_kernel<T><<<(unsigned)cdiv(n, 64), 256, 0, s>>>(partial, splits, n, (T *)dbias);
     return hipGetLastError();
 }
 
