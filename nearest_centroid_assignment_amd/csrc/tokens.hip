@@ -7,7 +7,7 @@
 // prefix over blocks and experts gives the places. At most kSmallPairs pairs are
 // sorted by one block in one launch; up to kPlaceTiles blocks of 1024 pairs by two
 // launches (the second sums the blocks' counts in every block: 65536 x 2 pairs of
-// 1024 experts 23 us in four launches, 11 in two); more by four.
+// 1024 experts 23 us in four launches, 21 in two); more by four.
 //
 // The row kernels give one wave (or, with few tokens, one block) to a token: its
 // own row is read once, and the rows of its `top` pairs are reached through the
