@@ -208,10 +208,14 @@ struct GradProblem {
 struct Cut {
     int tile, splits;
     bool thin;
+    double cost;  // microseconds, by the cost model
 };
 Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped, int64_t experts,
               bool p_rows);
 Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts);
+// The tile of dx and dw in one launch, 0 where the two launches are better.
+int both_plan(int dtype, int64_t rows, int64_t outs, int64_t ins, bool grouped, int64_t experts,
+              const Cut &dx, const Cut &dw);
 
 // Row tiles of all groups at most: every group that has a row may end in a
 // partial tile, and the rows past the last expert's are one more group.
@@ -226,6 +230,8 @@ bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, bool gro
 bool grad_grid_ok(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts);
 hipError_t launch_rows(int dtype, const RowsProblem &pr, bool thin, hipStream_t s);
 hipError_t launch_grad(int dtype, const GradProblem &pr, hipStream_t s);
+// dx and dw in one launch, with both_plan's tile in both and neither split.
+hipError_t launch_both(int dtype, const RowsProblem &r, const GradProblem &g, hipStream_t s);
 
 // dst rows of ldd elements (a multiple of 8) = src rows with zeros from cols on.
 hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst,

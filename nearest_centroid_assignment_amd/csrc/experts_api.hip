@@ -419,55 +419,65 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
                                               lddz, dbias, (float *)(base + L.partial), s);
         if (e != hipSuccess) return KM_ERR_HIP;
     }
-    if (dx && rows > 0) {
+    const bool dx_runs = dx && rows > 0;
+    kx::RowsProblem r = {};
+    kx::GradProblem g = {};
+    kx::Cut rcut = {}, gcut = {};
+    if (dx_runs) {
         const Operand wp = operand(w, ins, experts * outs, ins, dtype, base + L.w, s);
         if (wp.e != hipSuccess) return KM_ERR_HIP;
-        const kx::Cut cut = kx::rows_plan(dtype, rows, ins, outs, grouped, experts, true);
-        kx::RowsProblem pr = {};
-        pr.tile = cut.tile;
-        pr.splits = cut.splits;
-        pr.partial = (float *)(base + L.partial);
-        pr.q = dz;
-        pr.ldq = lddz;
-        pr.p = wp.p;
-        pr.ldp = wp.ld;
-        pr.p_expert = outs * wp.ld;
-        pr.rows = rows;
-        pr.cols = ins;
-        pr.depth = outs;
-        pr.p_cols = wp.cols;
-        pr.p_rows = true;
-        pr.offsets = offsets;
-        pr.experts = (int)experts;
-        pr.in_pre = in_pre;
-        pr.ldin = ldin;
-        pr.in_act = in_act;
-        pr.out = dx;
-        pr.ldo = lddx;
-        if (kx::launch_rows(dtype, pr, cut.thin, s) != hipSuccess) return KM_ERR_HIP;
+        rcut = kx::rows_plan(dtype, rows, ins, outs, grouped, experts, true);
+        r.tile = rcut.tile;
+        r.splits = rcut.splits;
+        r.partial = (float *)(base + L.partial);
+        r.q = dz;
+        r.ldq = lddz;
+        r.p = wp.p;
+        r.ldp = wp.ld;
+        r.p_expert = outs * wp.ld;
+        r.rows = rows;
+        r.cols = ins;
+        r.depth = outs;
+        r.p_cols = wp.cols;
+        r.p_rows = true;
+        r.offsets = offsets;
+        r.experts = (int)experts;
+        r.in_pre = in_pre;
+        r.ldin = ldin;
+        r.in_act = in_act;
+        r.out = dx;
+        r.ldo = lddx;
     }
     if (dw) {
         const Operand xp = operand(x, ldx, rows, ins, dtype, base + L.x, s);
         if (xp.e != hipSuccess) return KM_ERR_HIP;
-        const kx::Cut cut = kx::grad_plan(dtype, rows, outs, ins, experts);
-        kx::GradProblem pr = {};
-        pr.tile = cut.tile;
-        pr.splits = cut.splits;
-        pr.partial = (float *)(base + L.partial);
-        pr.x = xp.p;
-        pr.ldx = xp.ld;
-        pr.x_cols = xp.cols;
-        pr.dz = dz;
-        pr.lddz = lddz;
-        pr.dz_cols = dz_cols;
-        pr.rows = rows;
-        pr.m_cols = outs;
-        pr.n_cols = ins;
-        pr.offsets = offsets;
-        pr.experts = (int)experts;
-        pr.out = dw;
-        if (kx::launch_grad(dtype, pr, s) != hipSuccess) return KM_ERR_HIP;
+        gcut = kx::grad_plan(dtype, rows, outs, ins, experts);
+        g.tile = gcut.tile;
+        g.splits = gcut.splits;
+        g.partial = (float *)(base + L.partial);
+        g.x = xp.p;
+        g.ldx = xp.ld;
+        g.x_cols = xp.cols;
+        g.dz = dz;
+        g.lddz = lddz;
+        g.dz_cols = dz_cols;
+        g.rows = rows;
+        g.m_cols = outs;
+        g.n_cols = ins;
+        g.offsets = offsets;
+        g.experts = (int)experts;
+        g.out = dw;
     }
+    if (dx_runs && dw) {
+        const int tile = kx::both_plan(dtype, rows, outs, ins, grouped, experts, rcut, gcut);
+        if (tile) {
+            r.tile = g.tile = tile;
+            r.splits = g.splits = 1;
+            return status(kx::launch_both(dtype, r, g, s));
+        }
+    }
+    if (dx_runs && kx::launch_rows(dtype, r, rcut.thin, s) != hipSuccess) return KM_ERR_HIP;
+    if (dw && kx::launch_grad(dtype, g, s) != hipSuccess) return KM_ERR_HIP;
     return KM_OK;
 }
 

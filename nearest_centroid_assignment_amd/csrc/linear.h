@@ -446,8 +446,8 @@ __device__ __forceinline__ void run_product(lds_char *smem, typename S::TileP &t
 // Block b of a grid of `total` tiles: XCD b % 8 takes pieces of `piece`
 // consecutive tiles, so that tiles which share operands share an L2; piece 0: one
 // piece, an eighth of the tiles. -1: no tile. (total, piece < 2^31)
-__device__ __forceinline__ int xcd_tile(int total, int piece) {
-    const int b = blockIdx.x, x = b & 7, j = b >> 3;
+__device__ __forceinline__ int xcd_tile(int b, int total, int piece) {
+    const int x = b & 7, j = b >> 3;
     const int per = (total + 7) / 8;
     const int id = piece ? ((j / piece) * 8 + x) * piece + j % piece : j < per ? x * per + j : total;
     return id < total ? id : -1;
@@ -568,6 +568,8 @@ __device__ __forceinline__ void by_rows(lds_char *smem, int wave, int lane,
     }
 }
 
+constexpr int kWalk = 8;
+
 struct RowsArgs {
     RowsProblem pr;
     int gm;  // row tiles walked per column tile, so that a group's operands stay in L2
@@ -592,10 +594,8 @@ __device__ __forceinline__ void walk(int id, int tiles_m, int tiles_n, int gm, i
 }
 
 template <class S>
-__global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
+__device__ __forceinline__ void rows_block(const RowsArgs &a, int block, lds_char *smem) {
     typedef typename S::type T;
-    __shared__ __align__(1024) char memory[S::NS * S::kStage];
-    lds_char *smem = (lds_char *)memory;
     const RowsProblem &pr = a.pr;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -604,7 +604,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
     Groups groups = {pr.offsets, pr.experts, rows, S::BM};
     const int tiles_m = pr.offsets ? groups.total() : (rows + S::BM - 1) / S::BM;
     const int tiles = tiles_m * tiles_n;
-    int id = xcd_tile(tiles * pr.splits, 0);
+    int id = xcd_tile(block, tiles * pr.splits, 0);
     if (id < 0) return;
     const int part = __builtin_amdgcn_readfirstlane(id / tiles);
     id -= part * tiles;
@@ -756,10 +756,8 @@ __global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
 constexpr int kPiece = 16;  // tiles: 4 x 4 of the walk
 
 template <class S>
-__global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
+__device__ __forceinline__ void grad_block(const GradProblem &pr, int block, lds_char *smem) {
     typedef typename S::type T;
-    __shared__ __align__(1024) char memory[S::NS * S::kStage];
-    lds_char *smem = (lds_char *)memory;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int mc = (int)pr.m_cols, nc = (int)pr.n_cols, rows = (int)pr.rows;
@@ -768,7 +766,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
     // Experts' tiles cost as many stages as the expert has rows: dealt out in
     // small pieces, every XCD gets tiles of every large expert.
     const int tiles = each * pr.experts;
-    int id = xcd_tile(tiles * pr.splits, pr.offsets ? kPiece : 0);
+    int id = xcd_tile(block, tiles * pr.splits, pr.offsets ? kPiece : 0);
     if (id < 0) return;
     const int part = __builtin_amdgcn_readfirstlane(id / tiles);
     id -= part * tiles;
@@ -825,46 +823,118 @@ __global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
 }
 
 template <class S>
-hipError_t run_rows(const RowsProblem &pr, hipStream_t s) {
-    RowsArgs a;
-    a.pr = pr;
-    a.gm = 8;
-    const int64_t tiles = most_row_tiles(pr.rows, S::BM, pr.offsets != nullptr, pr.experts) *
-                          cdiv(pr.cols, S::BN) * pr.splits;
-    rows_kernel<S><<<(unsigned)(cdiv(tiles, 8) * 8), S::NW * 64, 0, s>>>(a);
-    return hipGetLastError();
+__global__ __launch_bounds__(S::NW * 64, 2) void rows_kernel(RowsArgs a) {
+    __shared__ __align__(1024) char memory[S::NS * S::kStage];
+    rows_block<S>(a, blockIdx.x, (lds_char *)memory);
+}
+template <class S>
+__global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
+    __shared__ __align__(1024) char memory[S::NS * S::kStage];
+    grad_block<S>(pr, blockIdx.x, (lds_char *)memory);
+}
+
+// dx and dw of one call (where both_plan finds it better): the blocks of the one follow
+// those of the other, the deeper (longer) ones first.
+template <class SR, class SG>
+__global__ __launch_bounds__(SR::NW * 64, 2) void both_kernel(RowsArgs a, GradProblem g, int first,
+                                                              bool rows_first) {
+    static_assert(SR::NW == SG::NW, "one block size");
+    constexpr int kBytes = SR::NS * SR::kStage > SG::NS * SG::kStage ? SR::NS * SR::kStage
+                                                                     : SG::NS * SG::kStage;
+    __shared__ __align__(1024) char memory[kBytes];
+    const int b = blockIdx.x;
+    const int in = b < first ? b : b - first;
+    if ((b < first) == rows_first)
+        rows_block<SR>(a, in, (lds_char *)memory);
+    else
+        grad_block<SG>(g, in, (lds_char *)memory);
 }
 
 template <class S>
-hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
+int64_t rows_blocks(const RowsProblem &pr) {
+    const int64_t tiles = most_row_tiles(pr.rows, S::BM, pr.offsets != nullptr, pr.experts) *
+                          cdiv(pr.cols, S::BN) * pr.splits;
+    return cdiv(tiles, 8) * 8;
+}
+template <class S>
+int64_t grad_blocks(const GradProblem &pr) {
     const int64_t tiles = cdiv(pr.m_cols, S::BM) * cdiv(pr.n_cols, S::BN) * pr.experts * pr.splits;
     const int64_t unit = pr.offsets ? 8 * kPiece : 8;
-    grad_kernel<S><<<(unsigned)(cdiv(tiles, unit) * unit), S::NW * 64, 0, s>>>(pr);
+    return cdiv(tiles, unit) * unit;
+}
+
+template <class S>
+hipError_t run_rows(const RowsProblem &pr, hipStream_t s) {
+    rows_kernel<S><<<(unsigned)rows_blocks<S>(pr), S::NW * 64, 0, s>>>(RowsArgs{pr, kWalk});
     return hipGetLastError();
 }
+template <class S>
+hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
+    grad_kernel<S><<<(unsigned)grad_blocks<S>(pr), S::NW * 64, 0, s>>>(pr);
+    return hipGetLastError();
+}
+template <class SR, class SG>
+hipError_t run_both(const RowsProblem &r, const GradProblem &g, hipStream_t s) {
+    const int64_t nr = rows_blocks<SR>(r), ng = grad_blocks<SG>(g);
+    const bool rows_first = r.depth * g.experts >= g.rows;
+    both_kernel<SR, SG><<<(unsigned)(nr + ng), SR::NW * 64, 0, s>>>(
+        RowsArgs{r, kWalk}, g, (int)(rows_first ? nr : ng), rows_first);
+    return hipGetLastError();
+}
+
+// The tiles of a type: forward product (PMC false), dx (PMC true), dw.
+template <typename T, bool PMC>
+using Rows256 = Shape<T, PMC, false, 256, 256, 2, 4, 4, 64>;
+template <typename T, bool PMC>
+using Rows129 = Shape<T, PMC, false, 128, 128, 2, 4, 3>;
+template <typename T, bool PMC>
+using Rows128 = Shape<T, PMC, false, 128, 128, 2, 4, 2>;
+template <typename T, bool PMC>
+using Rows64 = Shape<T, PMC, false, 64, 64, 2, 2, 2>;
+template <typename T, bool PMC>
+using Rows32 = Shape<T, PMC, false, 32, 64, 2, 2, 2>;
+template <typename T>
+using Grad256 = Shape<T, true, true, 256, 256, 2, 4, 2>;
+template <typename T>
+using Grad129 = Shape<T, true, true, 128, 128, 2, 4, 3>;
+template <typename T>
+using Grad128 = Shape<T, true, true, 128, 128, 2, 4, 2>;
+template <typename T>
+using Grad64 = Shape<T, true, true, 64, 64, 2, 2, 2>;
+template <typename T>
+using Grad32 = Shape<T, true, true, 32, 64, 2, 2, 2>;
 
 template <typename T, bool PMC>
 hipError_t pick_rows(const RowsProblem &pr, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (pr.tile == 256) return run_rows<Shape<T, PMC, false, 256, 256, 2, 4, 4, 64>>(pr, s);
-        if (pr.tile == 129) return run_rows<Shape<T, PMC, false, 128, 128, 2, 4, 3>>(pr, s);
+        if (pr.tile == 256) return run_rows<Rows256<T, PMC>>(pr, s);
+        if (pr.tile == 129) return run_rows<Rows129<T, PMC>>(pr, s);
     } else {
-        if (pr.tile == 32) return run_rows<Shape<T, PMC, false, 32, 64, 2, 2, 2>>(pr, s);
+        if (pr.tile == 32) return run_rows<Rows32<T, PMC>>(pr, s);
     }
-    if (pr.tile == 128) return run_rows<Shape<T, PMC, false, 128, 128, 2, 4, 2>>(pr, s);
-    return run_rows<Shape<T, PMC, false, 64, 64, 2, 2, 2>>(pr, s);
+    if (pr.tile == 128) return run_rows<Rows128<T, PMC>>(pr, s);
+    return run_rows<Rows64<T, PMC>>(pr, s);
 }
 
 template <typename T>
 hipError_t pick_grad(const GradProblem &pr, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (pr.tile == 256) return run_grad<Shape<T, true, true, 256, 256, 2, 4, 2>>(pr, s);
-        if (pr.tile == 129) return run_grad<Shape<T, true, true, 128, 128, 2, 4, 3>>(pr, s);
+        if (pr.tile == 256) return run_grad<Grad256<T>>(pr, s);
+        if (pr.tile == 129) return run_grad<Grad129<T>>(pr, s);
     } else {
-        if (pr.tile == 32) return run_grad<Shape<T, true, true, 32, 64, 2, 2, 2>>(pr, s);
+        if (pr.tile == 32) return run_grad<Grad32<T>>(pr, s);
     }
-    if (pr.tile == 128) return run_grad<Shape<T, true, true, 128, 128, 2, 4, 2>>(pr, s);
-    return run_grad<Shape<T, true, true, 64, 64, 2, 2, 2>>(pr, s);
+    if (pr.tile == 128) return run_grad<Grad128<T>>(pr, s);
+    return run_grad<Grad64<T>>(pr, s);
+}
+
+template <typename T>
+hipError_t pick_both(const RowsProblem &r, const GradProblem &g, hipStream_t s) {
+    if constexpr (sizeof(T) == 2) {
+        if (r.tile == 256) return run_both<Rows256<T, true>, Grad256<T>>(r, g, s);
+    }
+    if (r.tile == 128) return run_both<Rows128<T, true>, Grad128<T>>(r, g, s);
+    return run_both<Rows64<T, true>, Grad64<T>>(r, g, s);
 }
 
 // Products with few rows an expert (BM = 16 MT of them to a block): bound by
@@ -996,5 +1066,7 @@ template <typename T>
 hipError_t launch_thin_t(const RowsProblem &pr, hipStream_t s);
 template <typename T>
 hipError_t launch_grad_t(const GradProblem &pr, hipStream_t s);
+template <typename T>
+hipError_t launch_both_t(const RowsProblem &r, const GradProblem &g, hipStream_t s);
 
 }  // namespace kx

@@ -11,6 +11,8 @@ template <typename T>
 hipError_t launch_thin_t(const RowsProblem &pr, hipStream_t s);
 template <typename T>
 hipError_t launch_grad_t(const GradProblem &pr, hipStream_t s);
+template <typename T>
+hipError_t launch_both_t(const RowsProblem &r, const GradProblem &g, hipStream_t s);
 
 namespace {
 
@@ -299,7 +301,7 @@ constexpr TileCost kFloat[] = {{128, 128, 128, 1.75, 0.10, 5.0},
 // rows up.
 template <class F>
 Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, double setup, F tiles_of) {
-    Cut best = {64, 1, false};
+    Cut best = {64, 1, false, 0.0};
     double least = 1e300;
     for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
         const int64_t tiles = tiles_of(c.rows, c.cols);
@@ -312,7 +314,7 @@ Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, double setu
             if (parts > 1) t += 4.0 + (double)parts * (double)sums * 8.0 / 3e6;
             if (t < least) {
                 least = t;
-                best = {c.tile, parts, false};
+                best = {c.tile, parts, false, t};
             }
         }
     }
@@ -321,19 +323,26 @@ Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, double setu
 
 }  // namespace
 
+namespace {
+// Groups that may have rows, and the row tiles to expect: half a tile lost per group.
+int64_t groups_of(int64_t rows, bool grouped, int64_t experts) {
+    const int64_t groups = grouped ? (experts < rows ? experts : rows) : 1;
+    return groups < 1 ? 1 : groups;
+}
+int64_t row_tiles(int64_t rows, int64_t bm, bool grouped, int64_t experts) {
+    return cdiv(rows, bm) + (grouped ? groups_of(rows, grouped, experts) / 2 : 0);
+}
+}  // namespace
+
 Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped, int64_t experts,
               bool p_rows) {
-    // Rows that a group has on average (every expert that has one), and the
-    // row tiles to expect: half a tile lost per expert.
-    int64_t groups = grouped ? (experts < rows ? experts : rows) : 1;
-    if (groups < 1) groups = 1;
-    const int64_t each = rows / groups;
+    const int64_t groups = groups_of(rows, grouped, experts), each = rows / groups;
     auto tiles = [&](int64_t m, int64_t n) {
-        return (cdiv(rows, m) + (grouped ? groups / 2 : 0)) * cdiv(cols, n);
+        return row_tiles(rows, m, grouped, experts) * cdiv(cols, n);
     };
     // Few rows and too few tiles to stream w with: 16 x 4096 with depth 4096 10 us
     // against 15 in eight parts of 64s; but 16 x 4096 of 16 experts 45 against 43.
-    if (!p_rows && each <= 32 && groups * cdiv(cols, 64) < 256) return {each <= 16 ? 16 : 32, 1, true};
+    if (!p_rows && each <= 32 && groups * cdiv(cols, 64) < 256) return {each <= 16 ? 16 : 32, 1, true, 0.0};
     const int64_t size = dtype == 0 ? 4 : 2;
     Cut c = best_cut(dtype, cdiv(depth * size, 128), (rows + groups * cols) * depth * size, rows * cols,
                      grouped ? 1.0 : 0.0, tiles);
@@ -349,6 +358,52 @@ Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t e
                      m_cols * n_cols * experts, 0.0, tiles);
     if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
     return c;
+}
+
+// One launch leaves no compute unit idle between the two and saves a launch. Blocks
+// that all run at once meet the compute units in turn, the longer ones first; more of
+// them even out.
+//   (dx and dw, two launches -> one: 1000 x 1111 x 777 float32 54 us -> 45, bf16 1024^3
+//   17 -> 12, 2048^3 60 -> 39, 256 x 2048 x 2048 20 -> 17, 16 experts 8192 x 4096 x 1024
+//   220 -> 163; but 512 x 2048 x 1000 float32, dx four times as long as dw, 51 -> 57.)
+int both_plan(int dtype, int64_t rows, int64_t outs, int64_t ins, bool grouped, int64_t experts,
+              const Cut &dx, const Cut &dw) {
+    const int64_t size = dtype == 0 ? 4 : 2;
+    const double depth_dx = (double)cdiv(outs * size, 128);
+    const double depth_dw = (double)cdiv(rows / experts * size, 128);
+    const double bytes = (double)(2 * rows * (outs + ins) + 2 * experts * outs * ins) * size;
+    double least = 0.97 * (dx.cost + dw.cost + 2.0);
+    int best = 0;
+    for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
+        if (c.tile == 32) continue;
+        const int64_t ndx = row_tiles(rows, c.rows, grouped, experts) * cdiv(ins, c.cols);
+        const int64_t ndw = cdiv(outs, c.rows) * cdiv(ins, c.cols) * experts;
+        const int64_t most = most_row_tiles(rows, c.rows, grouped, experts) * cdiv(ins, c.cols) + ndw;
+        if (most + 256 > kMaxGridThreads / 512) continue;
+        const double tdx = depth_dx * c.each + c.edge + (grouped ? 1.0 : 0.0);
+        const double tdw = depth_dw * c.each + c.edge;
+        const bool dx_long = tdx >= tdw;
+        const double tl = dx_long ? tdx : tdw, ts = dx_long ? tdw : tdx;
+        const int64_t nl = dx_long ? ndx : ndw, n = ndx + ndw;
+        // Bound by memory past the caches, nothing idles: 16 rows of 16 experts, 4096 x
+        // 2048, 84 us -> 90.
+        const double busy = ((double)ndx * depth_dx + (double)ndw * depth_dw) * c.each / 256;
+        if (bytes > 256 << 20 && busy < bytes / 5.5e6) continue;
+        const int together = c.tile == 256 ? 1 : c.tile == 128 ? 2 : 4;  // blocks on a compute unit
+        double t;
+        if (n <= 256 * together)
+            t = (double)cdiv(nl, 256) * tl + (double)(cdiv(n, 256) - cdiv(nl, 256)) * ts;
+        else
+            t = ((double)ndx * tdx + (double)ndw * tdw) / 256;
+        if (t < tl) t = tl;
+        if (n > 256 * together) t += 0.5 * ts;
+        t += (depth_dx > depth_dw ? depth_dx : depth_dw) * c.wait;
+        if (t < least) {
+            least = t;
+            best = c.tile;
+        }
+    }
+    return best;
 }
 
 bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped,
@@ -373,6 +428,10 @@ hipError_t launch_rows(int dtype, const RowsProblem &pr, bool thin, hipStream_t 
 hipError_t launch_grad(int dtype, const GradProblem &pr, hipStream_t s) {
     if (dtype == 0) return grad_t<float>(pr, s);
     return dtype == 1 ? grad_t<bf16>(pr, s) : grad_t<f16>(pr, s);
+}
+hipError_t launch_both(int dtype, const RowsProblem &r, const GradProblem &g, hipStream_t s) {
+    if (dtype == 0) return launch_both_t<float>(r, g, s);
+    return dtype == 1 ? launch_both_t<bf16>(r, g, s) : launch_both_t<f16>(r, g, s);
 }
 
 hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst,

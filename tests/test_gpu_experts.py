@@ -319,6 +319,40 @@ def test_linear_few_rows(dtype, rows, outs, ins, counts):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,outs,ins,counts", [
+    (200, 72, 1100, None), (2000, 2100, 136, None), (258, 642, 2046, None), (1300, 40, 56, None), (269, 67, 1959, None),
+    (700, 1000, 333, None), (65, 1030, 2000, None), (0, 72, 1096, [100, 0, 700, 33]), (0, 1048, 136, [65, 0, 130]),
+    (0, 333, 520, [200, 700, 0, 120, 1]), (0, 130, 1954, [100, 400, 0, 900, 600, 15, 700, 300])])
+def test_linear_gradients_apart(dtype, rows, outs, ins, counts):
+    """dx and dw asked for alone, and together (one launch for most sizes)."""
+    gu.announce(f"linear gradients apart {dtype} {rows} x {outs} x {ins} {counts}")
+    tail = 0 if counts is None else 11
+    live = rows if counts is None else sum(counts)
+    n, e = live + tail, 1 if counts is None else len(counts)
+    offsets = None if counts is None else torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32).cuda()
+    x, dy, ip = randn(1, n, ins, dtype=dtype), randn(2, n, outs, dtype=dtype), randn(3, n, ins, dtype=dtype)
+    w = randn(4, *(() if counts is None else (e,)), outs, ins, dtype=dtype, scale=ins ** -0.5)
+    for t in (x, dy, ip):
+        t[live:] = float("nan")
+    call = lambda **k: experts.linear_backward(dy, x, w, offsets=offsets, in_pre=ip, in_act="silu", need_dbias=False, **k)  # noqa: E731
+    ways = [call(), (call(need_dw=False)[0], call(need_dx=False)[1])]
+    bounds = [0, n] if counts is None else [0] + list(np.cumsum(counts))
+    for i in range(e):
+        lo, hi = int(bounds[i]), int(bounds[i + 1])
+        wi, xi, gi, q = f64(w if counts is None else w[i]), f64(x[lo:hi]), f64(dy[lo:hi]), f64(ip[lo:hi])
+        si = slope64(q, "silu")
+        want = gi @ wi
+        err = summed(outs) * (gi.abs() @ wi.abs()) * si.abs() + want.abs() * 2.0 ** -19 * (1 + q.abs())
+        want = want * si
+        dw, dwerr = gi.t() @ xi, summed(hi - lo) * (gi.abs().t() @ xi.abs())
+        for got in ways:
+            close(got[0][lo:hi], want, err, f"dx of {i}")
+            close(got[1] if counts is None else got[1][i], dw, dwerr, f"dw of {i}")
+    for got in ways:
+        assert not got[0][live:].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_linear_options(dtype):
     """Row strides on and off 16 bytes, no bias, and gradients one at a time."""
     rows, outs, ins = 70, 88, 104
