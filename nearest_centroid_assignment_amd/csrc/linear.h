@@ -83,8 +83,8 @@ __device__ __forceinline__ int kc_key64(int r) {
 // NW waves with 16 bytes a lane and instruction. Rows may start on any 4 bytes:
 // the buffer's range check works in 4-byte words, so a chunk that leaves the
 // operand is cut there. A chunk that leaves its row reads the next row's start,
-// which in an MC operand only reaches columns that are not stored; a KC row that
-// ends inside a chunk has its last stage moved in 4-byte pieces (`ragged`).
+// which in an MC operand only reaches columns that are not stored; where a KC row ends
+// inside a chunk (`ragged`), the last stage's fragments are cut in registers (cut).
 template <typename T, bool MC, int R, int NW, int kRow>
 struct Tile {
     static constexpr int kSize = (int)sizeof(T);
@@ -139,13 +139,12 @@ struct Tile {
         kc[1] = kc_byte(lds_byte(wave, lane, kIssues > 1 ? 1 : 0));
     }
 
-    // Whether the last stage has to be moved in 4-byte pieces.
+    // Whether the last stage's fragments have to be cut.
     __device__ __forceinline__ bool ragged() const { return !MC && (left & 15) != 0; }
 
     // Moves this stage into LDS and steps to the next. Past the last stage
-    // every lane is out of range, and zeros arrive. `last`: this may be the
-    // ragged stage.
-    __device__ __forceinline__ void issue(lds_char *lds, int wave, int lane, bool last) {
+    // every lane is out of range, and zeros arrive.
+    __device__ __forceinline__ void issue(lds_char *lds, int wave) {
         int records = 0;
         if (MC) {
             const int rows = left < kDepth ? left : kDepth;
@@ -157,22 +156,12 @@ struct Tile {
         const __amdgpu_buffer_rsrc_t rsrc =
             __builtin_amdgcn_make_buffer_rsrc((void *)at, 0, records, 0x00020000);
         lds_char *to = lds + wave * kIssues * 1024;
-        if (!MC && last && left < kRow && (left & 15)) {
-#pragma unroll 1
-            for (int i = 0; i < kIssues * 4; ++i) {
-                const int q = (wave * kIssues * 4 + i) * 256 + lane * 4, k = kc_byte(q);
-                const uint32_t o = k < left ? (uint32_t)(q / kRow * ld + k) : kNowhere;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + i * 256), 4, (int)o,
-                                                         0, 0, 0);
-            }
-        } else {
 #pragma unroll
-            for (int i = 0; i < kIssues; ++i) {
-                uint32_t o = off[i];
-                if (!MC) o = kc[i & 1] < left ? o : kNowhere;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + i * 1024), 16, (int)o,
-                                                         0, 0, 0);
-            }
+        for (int i = 0; i < kIssues; ++i) {
+            uint32_t o = off[i];
+            if (!MC) o = kc[i & 1] < left ? o : kNowhere;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)(to + i * 1024), 16, (int)o, 0,
+                                                     0, 0);
         }
         at += MC ? (uint64_t)ld * kDepth : (uint64_t)kRow;
         left -= MC ? kDepth : kRow;
@@ -260,6 +249,22 @@ __device__ __forceinline__ void read_half(const typename S::ReadP &rp, const typ
 #pragma unroll
     for (int t = 0; t < S::TM; ++t) f.q[t] = rq.read(stage + S::BN * S::kRow, t, s);
 }
+// Zero for what the last stage's half s holds past its `valid` values of k, in
+// the operands whose rows hold k.
+template <class S>
+__device__ __forceinline__ void cut(Frags<S> &f, int s, int valid, int lane) {
+    constexpr int kLane = 16 / (int)sizeof(typename S::type);
+    const int left = valid - (s * 4 + (lane >> 4)) * kLane;
+#pragma unroll
+    for (int j = 0; j < kLane; ++j) {
+        if (!S::p_mc)
+#pragma unroll
+            for (int t = 0; t < S::TN; ++t) f.p[t][j] = j < left ? f.p[t][j] : 0;
+        if (!S::q_mc)
+#pragma unroll
+            for (int t = 0; t < S::TM; ++t) f.q[t][j] = j < left ? f.q[t][j] : 0;
+    }
+}
 template <class S>
 __device__ __forceinline__ void multiply(const Frags<S> &f, f32x4 (&acc)[S::TM][S::TN]) {
     // One accumulator's instructions lie a whole block apart: back to back each
@@ -339,33 +344,33 @@ __device__ __forceinline__ void product_in_turns(lds_char *smem, typename S::Til
     };
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        tp.issue(smem + i * S::kStage, wave, lane, true);
-        tq.issue(smem + i * S::kStage + S::BN * S::kRow, wave, lane, true);
+        tp.issue(smem + i * S::kStage, wave);
+        tq.issue(smem + i * S::kStage + S::BN * S::kRow, wave);
     }
     wait_loads<2 * kMoves>();
     meet();
     if (wave >= 4) meet();  // one phase behind
     Frags<S> f;
     int at = 0;
+    const int valid = depth - (stages - 1) * S::TileP::kDepth;  // of the last stage
     auto stage = [&](bool last) {
         lds_char *cur = smem + at * S::kStage, *free = smem + ((at + 3) & 3) * S::kStage;
         read_half<S>(rp, rq, cur, 0, f);
         // Its last readers, the waves behind, were done a phase ago.
-        tp.issue(free, wave, lane, last);
-        tq.issue(free + S::BN * S::kRow, wave, lane, last);
+        tp.issue(free, wave);
+        tq.issue(free + S::BN * S::kRow, wave);
         wait_loads<2 * kMoves>();  // the next stage has landed; the fragments are here
         meet();
+        if (last) cut<S>(f, 0, valid, lane);
         __builtin_amdgcn_s_setprio(1);
         multiply<S>(f, acc);
         __builtin_amdgcn_s_setprio(0);
         meet();
         at = (at + 1) & 3;
     };
-    const int plain = ragged ? stages - 4 : stages;  // stage it + 3 moves in during stage it
-    int it = 0;
-    for (; it < plain; ++it) stage(false);
-#pragma unroll 1
-    for (; it < stages; ++it) stage(true);
+    const int plain = ragged ? stages - 1 : stages;
+    for (int it = 0; it < plain; ++it) stage(false);
+    if (ragged) stage(true);
     if (wave < 4) meet();
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();  // the stages' memory is free
@@ -389,8 +394,8 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
     const bool ragged = tp.ragged() || tq.ragged();
 #pragma unroll
     for (int i = 0; i < S::NS; ++i) {
-        tp.issue(smem + i * S::kStage, wave, lane, true);
-        tq.issue(smem + i * S::kStage + S::BN * S::kRow, wave, lane, true);
+        tp.issue(smem + i * S::kStage, wave);
+        tq.issue(smem + i * S::kStage + S::BN * S::kRow, wave);
     }
     wait_loads<(S::NS - 1) * kMoves>();
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -399,9 +404,11 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
     Frags<S> f[2];
     read_half<S>(rp, rq, smem, 0, f[0]);
     lds_char *cur = smem;
+    const int valid = depth - (stages - 1) * S::TileP::kDepth;  // of the last stage
     auto stage = [&](bool last) {
         lds_char *nxt = cur + S::kStage == smem + S::NS * S::kStage ? smem : cur + S::kStage;
         read_half<S>(rp, rq, cur, 1, f[1]);
+        if (last) cut<S>(f[0], 0, valid, lane);
         multiply<S>(f[0], acc);
         spread<S>(false);
         // Left alone, the compiler waits and meets after a quarter of these
@@ -409,7 +416,6 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
         // (64 x 64) the loads then have too little time: 1000 x 777 with depth 1111 float32
         // 29 -> 26.5 us. Larger tiles are as fast either way, or faster left alone.
         if (S::BM * S::BN <= 64 * 64 && S::BM == S::BN) __builtin_amdgcn_sched_barrier(0);
-        // (A ragged stage has more loads than kMoves: then this waits for more.)
         wait_loads<(S::NS - 2) * kMoves>();
         // The next stage has landed, and this one is in registers. (Loads of later
         // stages stay in flight across the barrier; __syncthreads would wait.)
@@ -417,18 +423,16 @@ __device__ __forceinline__ void product(lds_char *smem, typename S::TileP &tp,
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         read_half<S>(rp, rq, nxt, 0, f[0]);
-        tp.issue(cur, wave, lane, last);
-        tq.issue(cur + S::BN * S::kRow, wave, lane, last);
+        tp.issue(cur, wave);
+        tq.issue(cur + S::BN * S::kRow, wave);
+        if (last) cut<S>(f[1], 1, valid, lane);
         multiply<S>(f[1], acc);
-        if (!last) spread<S>(true);
+        spread<S>(true);
         cur = nxt;
     };
-    // Stage it + NS moves in during stage it: the ragged one, if any, is the last.
-    const int plain = ragged ? stages - S::NS - 1 : stages;
-    int it = 0;
-    for (; it < plain; ++it) stage(false);
-#pragma unroll 1
-    for (; it < stages; ++it) stage(true);
+    const int plain = ragged ? stages - 1 : stages;
+    for (int it = 0; it < plain; ++it) stage(false);
+    if (ragged) stage(true);
     __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();  // the stages' memory is free
 }
