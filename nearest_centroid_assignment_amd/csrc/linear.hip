@@ -278,39 +278,48 @@ hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
 
 namespace {
 
-// What a cut costs, in microseconds, from measured runs: a tile's stage costs
-// `each` on a compute unit that is kept busy by its tiles, and `wait` on top per
-// stage for latency that nothing hides; a round of tiles costs `edge` for its first
-// loads and its epilogue; joining split depths writes and reads the sums.
-//   (bf16, before -> chosen: 2048 x 2048 x 2048 30 us in 256 tiles of 128 -> 25 with three stages
-//   in flight; 512 x 1024 with depth 4096 37 us in 128 tiles of 64 -> 20 in four parts;
-//   188 x 4096 with depth 776 8 us in 64s against 15 in two parts or in 128s.)
+// What a cut costs, in microseconds: a tile's stage costs `each` on a compute unit that
+// is kept busy by its tiles (`apart` times that where rows do not start on lines of 128
+// bytes, and a stage's rows touch two), and `wait` on top per stage for latency that
+// nothing hides; a round of tiles costs `edge` for its first loads and its epilogue;
+// joining split depths writes and reads the sums. The constants are fitted to 354 sizes
+// (64 to 8192 a side, up to 16 experts), each in every tile and in 1 to 8 parts: what the
+// model takes is 3 % slower than the best of them in the geometric mean.
+//   (bf16: 512 x 1024 with depth 4096 37 us in 128 tiles of 64, 20 in four parts; 188 x
+//   4096 with depth 776 8 us in 64s, 15 in two parts or in 128s; 8192 x 4098 with
+//   depth 2050 312 us in 64s, 215 in 256s.)
 struct TileCost {
     int tile, rows, cols;
-    double each, wait, edge;
+    double each, wait, edge, apart;
 };
-constexpr TileCost kHalf[] = {{256, 256, 256, 1.65, 0.10, 8.0},
-                              {128, 128, 128, 0.50, 0.30, 2.5},
-                              {64, 64, 64, 0.13, 0.40, 1.0}};
-constexpr TileCost kFloat[] = {{128, 128, 128, 1.75, 0.10, 5.0},
-                               {64, 64, 64, 0.44, 0.15, 2.0},
-                               {32, 32, 64, 0.23, 0.20, 1.5}};
+constexpr TileCost kHalf[] = {{256, 256, 256, 1.30, 0.10, 10.0, 1.2},
+                              {128, 128, 128, 0.50, 0.35, 2.5, 1.0},
+                              {64, 64, 64, 0.14, 0.40, 0.9, 1.5}};
+constexpr TileCost kFloat[] = {{128, 128, 128, 2.25, 0.10, 7.5, 1.0},
+                               {64, 64, 64, 0.42, 0.20, 2.0, 1.0},
+                               {32, 32, 64, 0.23, 0.20, 1.4, 1.0}};
+constexpr double kBytes = 6.0e6;  // that operands pass at, a microsecond
+constexpr double kSetup = 0.8;    // what a round costs more where its blocks look their rows up
+
+bool lines(int64_t len, int64_t size) { return len * size % 128 == 0; }
 
 // tiles_of(rows, cols): the number of tiles of that size; bytes: of the operands;
-// sums: values to join; setup: what a round costs more where its blocks look their
-// rows up.
+// sums: values to join.
 template <class F>
-Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, double setup, F tiles_of) {
+Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, bool grouped,
+             bool on_lines, F tiles_of) {
     Cut best = {64, 1, false, 0.0};
     double least = 1e300;
     for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
         const int64_t tiles = tiles_of(c.rows, c.cols);
-        for (int parts = 1; parts <= 16; parts *= 2) {
+        for (int parts = 1; parts <= 8; parts *= 2) {
             if (parts > 1 && (stages / parts < 4 || tiles * parts > 1024)) break;
             const double rounds = (double)cdiv(tiles * parts, 256);
-            double t = (double)cdiv(stages, parts) * (rounds * c.each + c.wait);
-            const double memory = (double)bytes / 5.5e6;
-            t = (t < memory ? memory : t) + rounds * (c.edge + setup);
+            const double each = c.each * (on_lines ? 1.0 : c.apart);
+            const double edge = c.edge + (grouped ? kSetup : 0.0);
+            const double memory = (double)bytes / kBytes + edge;
+            double t = (double)cdiv(stages, parts) * (rounds * each + c.wait) + rounds * edge;
+            if (t < memory) t = memory;
             if (parts > 1) t += 4.0 + (double)parts * (double)sums * 8.0 / 3e6;
             if (t < least) {
                 least = t;
@@ -321,16 +330,16 @@ Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, double setu
     return best;
 }
 
-}  // namespace
-
-namespace {
-// Groups that may have rows, and the row tiles to expect: half a tile lost per group.
+// Groups that may have rows, and the row tiles to expect: half a tile lost per group,
+// and one to each at least.
 int64_t groups_of(int64_t rows, bool grouped, int64_t experts) {
     const int64_t groups = grouped ? (experts < rows ? experts : rows) : 1;
     return groups < 1 ? 1 : groups;
 }
 int64_t row_tiles(int64_t rows, int64_t bm, bool grouped, int64_t experts) {
-    return cdiv(rows, bm) + (grouped ? groups_of(rows, grouped, experts) / 2 : 0);
+    if (!grouped) return cdiv(rows, bm);
+    const int64_t groups = groups_of(rows, grouped, experts), n = rows / bm + groups / 2;
+    return n < groups ? groups : n;
 }
 }  // namespace
 
@@ -345,7 +354,7 @@ Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped
     if (!p_rows && each <= 32 && groups * cdiv(cols, 64) < 256) return {each <= 16 ? 16 : 32, 1, true, 0.0};
     const int64_t size = dtype == 0 ? 4 : 2;
     Cut c = best_cut(dtype, cdiv(depth * size, 128), (rows + groups * cols) * depth * size, rows * cols,
-                     grouped ? 1.0 : 0.0, tiles);
+                     grouped, lines(depth, size) && (!p_rows || lines(cols, size)), tiles);
     const int64_t most = most_row_tiles(rows, 128, grouped, experts) * cdiv(cols, 128);
     if (c.tile == 128 && dtype != 0 && most <= 256) c.tile = 129;
     return c;
@@ -355,7 +364,8 @@ Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t e
     auto tiles = [&](int64_t m, int64_t n) { return cdiv(m_cols, m) * cdiv(n_cols, n) * experts; };
     const int64_t size = dtype == 0 ? 4 : 2;
     Cut c = best_cut(dtype, cdiv(rows / experts * size, 128), rows * (m_cols + n_cols) * size,
-                     m_cols * n_cols * experts, 0.0, tiles);
+                     m_cols * n_cols * experts, false, lines(m_cols, size) && lines(n_cols, size),
+                     tiles);
     if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
     return c;
 }
@@ -371,8 +381,9 @@ int both_plan(int dtype, int64_t rows, int64_t outs, int64_t ins, bool grouped, 
     const int64_t size = dtype == 0 ? 4 : 2;
     const double depth_dx = (double)cdiv(outs * size, 128);
     const double depth_dw = (double)cdiv(rows / experts * size, 128);
+    const bool on_lines = lines(outs, size) && lines(ins, size);
     const double bytes = (double)(2 * rows * (outs + ins) + 2 * experts * outs * ins) * size;
-    double least = 0.97 * (dx.cost + dw.cost + 2.0);
+    double least = dx.cost + dw.cost + 2.0;
     int best = 0;
     for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
         if (c.tile == 32) continue;
@@ -380,15 +391,16 @@ int both_plan(int dtype, int64_t rows, int64_t outs, int64_t ins, bool grouped, 
         const int64_t ndw = cdiv(outs, c.rows) * cdiv(ins, c.cols) * experts;
         const int64_t most = most_row_tiles(rows, c.rows, grouped, experts) * cdiv(ins, c.cols) + ndw;
         if (most + 256 > kMaxGridThreads / 512) continue;
-        const double tdx = depth_dx * c.each + c.edge + (grouped ? 1.0 : 0.0);
-        const double tdw = depth_dw * c.each + c.edge;
+        const double each = c.each * (on_lines ? 1.0 : c.apart);
+        const double tdx = depth_dx * each + c.edge + (grouped ? kSetup : 0.0);
+        const double tdw = depth_dw * each + c.edge;
         const bool dx_long = tdx >= tdw;
         const double tl = dx_long ? tdx : tdw, ts = dx_long ? tdw : tdx;
         const int64_t nl = dx_long ? ndx : ndw, n = ndx + ndw;
         // Bound by memory past the caches, nothing idles: 16 rows of 16 experts, 4096 x
         // 2048, 84 us -> 90.
-        const double busy = ((double)ndx * depth_dx + (double)ndw * depth_dw) * c.each / 256;
-        if (bytes > 256 << 20 && busy < bytes / 5.5e6) continue;
+        const double busy = ((double)ndx * depth_dx + (double)ndw * depth_dw) * each / 256;
+        if (bytes > 256 << 20 && busy < bytes / kBytes) continue;
         const int together = c.tile == 256 ? 1 : c.tile == 128 ? 2 : 4;  // blocks on a compute unit
         double t;
         if (n <= 256 * together)
