@@ -230,8 +230,38 @@ bool rows_grid_ok(int dtype, int64_t rows, int64_t cols, int64_t depth, bool gro
 bool grad_grid_ok(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts);
 hipError_t launch_rows(int dtype, const RowsProblem &pr, bool thin, hipStream_t s);
 hipError_t launch_grad(int dtype, const GradProblem &pr, hipStream_t s);
-// dx and dw in one launch, with both_plan's tile in both and neither split.
-hipError_t launch_both(int dtype, const RowsProblem &r, const GradProblem &g, hipStream_t s);
+// The parts of dbias still to be added: out[i] = sum over s of partial[s * n + i].
+struct SlopeSum {
+    const float *partial;
+    int splits;  // 0: none
+    int64_t n;
+    void *out;
+};
+// 64 columns a block; each of its first four waves adds a quarter of the parts.
+// `quarter`: 256 floats of LDS.
+template <typename T>
+__device__ __forceinline__ void slope_sum(const SlopeSum &sum, int block, float *quarter) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t i = (int64_t)block * 64 + lane;
+    if (wave < 4) {
+        const int per = (sum.splits + 3) / 4;
+        const int end = (wave + 1) * per < sum.splits ? (wave + 1) * per : sum.splits;
+        float v = 0.0f;
+        if (i < sum.n) {
+#pragma unroll 8
+            for (int s = wave * per; s < end; ++s) v += sum.partial[s * sum.n + i];
+        }
+        quarter[threadIdx.x] = v;
+    }
+    __syncthreads();
+    if (wave == 0 && i < sum.n)
+        ((T *)sum.out)[i] = (T)((quarter[lane] + quarter[64 + lane]) +
+                                (quarter[128 + lane] + quarter[192 + lane]));
+}
+
+// dx and dw in one launch, with both_plan's tile in both and neither split, and `sum`.
+hipError_t launch_both(int dtype, const RowsProblem &r, const GradProblem &g, const SlopeSum &sum,
+                       hipStream_t s);
 
 // dst rows of ldd elements (a multiple of 8) = src rows with zeros from cols on.
 hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst,
@@ -239,11 +269,13 @@ hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t c
 
 // dz = dy * act'(pre) rounded to dtype into dz (NULL: not written; rows of
 // lddz, zeros from outs to lddz), dbias[e] = column sums of the float32 dz
-// (NULL: not computed) with `partial` of slope_splits() x experts x outs floats.
+// (NULL: not computed) with `partial` of slope_splits() x experts x outs floats. With
+// `later`, parts that have to be added are left there to launch_both.
 int64_t slope_splits(int64_t rows, int64_t outs, int64_t experts);
 hipError_t launch_slope(int dtype, const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
                         int act, const int *offsets, int experts, int64_t rows, int64_t outs,
-                        void *dz, int64_t lddz, void *dbias, float *partial, hipStream_t s);
+                        void *dz, int64_t lddz, void *dbias, float *partial, SlopeSum *later,
+                        hipStream_t s);
 
 // ------------------------------------------------------------------ adamw
 struct AdamwStep {

@@ -413,22 +413,27 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
         dz = base + L.dz;
         lddz = dz_cols = half ? pad8(outs) : outs;
     }
+    const bool dx_runs = dx && rows > 0;
+    kx::Cut rcut = {}, gcut = {};
+    if (dx_runs) rcut = kx::rows_plan(dtype, rows, ins, outs, grouped, experts, true);
+    if (dw) gcut = kx::grad_plan(dtype, rows, outs, ins, experts);
+    const int tile =
+        dx_runs && dw ? kx::both_plan(dtype, rows, outs, ins, grouped, experts, rcut, gcut) : 0;
+    kx::SlopeSum sum = {};
     if (copy || dbias) {
         const hipError_t e = kx::launch_slope(dtype, dy, lddy, pre, ldpre, act, offsets,
                                               (int)experts, rows, outs, copy ? (void *)dz : nullptr,
-                                              lddz, dbias, (float *)(base + L.partial), s);
+                                              lddz, dbias, (float *)(base + L.partial),
+                                              tile ? &sum : nullptr, s);
         if (e != hipSuccess) return KM_ERR_HIP;
     }
-    const bool dx_runs = dx && rows > 0;
     kx::RowsProblem r = {};
     kx::GradProblem g = {};
-    kx::Cut rcut = {}, gcut = {};
     if (dx_runs) {
         const Operand wp = operand(w, ins, experts * outs, ins, dtype, base + L.w, s);
         if (wp.e != hipSuccess) return KM_ERR_HIP;
-        rcut = kx::rows_plan(dtype, rows, ins, outs, grouped, experts, true);
-        r.tile = rcut.tile;
-        r.splits = rcut.splits;
+        r.tile = tile ? tile : rcut.tile;
+        r.splits = tile ? 1 : rcut.splits;
         r.partial = (float *)(base + L.partial);
         r.q = dz;
         r.ldq = lddz;
@@ -451,9 +456,8 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
     if (dw) {
         const Operand xp = operand(x, ldx, rows, ins, dtype, base + L.x, s);
         if (xp.e != hipSuccess) return KM_ERR_HIP;
-        gcut = kx::grad_plan(dtype, rows, outs, ins, experts);
-        g.tile = gcut.tile;
-        g.splits = gcut.splits;
+        g.tile = tile ? tile : gcut.tile;
+        g.splits = tile ? 1 : gcut.splits;
         g.partial = (float *)(base + L.partial);
         g.x = xp.p;
         g.ldx = xp.ld;
@@ -468,14 +472,7 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
         g.experts = (int)experts;
         g.out = dw;
     }
-    if (dx_runs && dw) {
-        const int tile = kx::both_plan(dtype, rows, outs, ins, grouped, experts, rcut, gcut);
-        if (tile) {
-            r.tile = g.tile = tile;
-            r.splits = g.splits = 1;
-            return status(kx::launch_both(dtype, r, g, s));
-        }
-    }
+    if (tile) return status(kx::launch_both(dtype, r, g, sum, s));
     if (dx_runs && kx::launch_rows(dtype, r, rcut.thin, s) != hipSuccess) return KM_ERR_HIP;
     if (dw && kx::launch_grad(dtype, g, s) != hipSuccess) return KM_ERR_HIP;
     return KM_OK;

@@ -838,15 +838,21 @@ __global__ __launch_bounds__(S::NW * 64, 2) void grad_kernel(GradProblem pr) {
 }
 
 // dx and dw of one call (where both_plan finds it better): the blocks of the one follow
-// those of the other, the deeper (longer) ones first.
+// those of the other, the deeper (longer) ones first. The last blocks add the parts of
+// dbias.
 template <class SR, class SG>
 __global__ __launch_bounds__(SR::NW * 64, 2) void both_kernel(RowsArgs a, GradProblem g, int first,
-                                                              bool rows_first) {
+                                                              bool rows_first, int products,
+                                                              SlopeSum sum) {
     static_assert(SR::NW == SG::NW, "one block size");
     constexpr int kBytes = SR::NS * SR::kStage > SG::NS * SG::kStage ? SR::NS * SR::kStage
                                                                      : SG::NS * SG::kStage;
     __shared__ __align__(1024) char memory[kBytes];
     const int b = blockIdx.x;
+    if (b >= products) {
+        slope_sum<typename SR::type>(sum, b - products, (float *)memory);
+        return;
+    }
     const int in = b < first ? b : b - first;
     if ((b < first) == rows_first)
         rows_block<SR>(a, in, (lds_char *)memory);
@@ -878,11 +884,12 @@ hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
     return hipGetLastError();
 }
 template <class SR, class SG>
-hipError_t run_both(const RowsProblem &r, const GradProblem &g, hipStream_t s) {
+hipError_t run_both(const RowsProblem &r, const GradProblem &g, const SlopeSum &sum, hipStream_t s) {
     const int64_t nr = rows_blocks<SR>(r), ng = grad_blocks<SG>(g);
     const bool rows_first = r.depth * g.experts >= g.rows;
-    both_kernel<SR, SG><<<(unsigned)(nr + ng), SR::NW * 64, 0, s>>>(
-        RowsArgs{r, kWalk}, g, (int)(rows_first ? nr : ng), rows_first);
+    const int64_t ns = sum.splits ? cdiv(sum.n, 64) : 0;
+    both_kernel<SR, SG><<<(unsigned)(nr + ng + ns), SR::NW * 64, 0, s>>>(
+        RowsArgs{r, kWalk}, g, (int)(rows_first ? nr : ng), rows_first, (int)(nr + ng), sum);
     return hipGetLastError();
 }
 
@@ -933,12 +940,13 @@ hipError_t pick_grad(const GradProblem &pr, hipStream_t s) {
 }
 
 template <typename T>
-hipError_t pick_both(const RowsProblem &r, const GradProblem &g, hipStream_t s) {
+hipError_t pick_both(const RowsProblem &r, const GradProblem &g, const SlopeSum &sum,
+                     hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        if (r.tile == 256) return run_both<Rows256<T, true>, Grad256<T>>(r, g, s);
+        if (r.tile == 256) return run_both<Rows256<T, true>, Grad256<T>>(r, g, sum, s);
     }
-    if (r.tile == 128) return run_both<Rows128<T, true>, Grad128<T>>(r, g, s);
-    return run_both<Rows64<T, true>, Grad64<T>>(r, g, s);
+    if (r.tile == 128) return run_both<Rows128<T, true>, Grad128<T>>(r, g, sum, s);
+    return run_both<Rows64<T, true>, Grad64<T>>(r, g, sum, s);
 }
 
 // Products with few rows an expert (BM = 16 MT of them to a block): bound by
@@ -1071,6 +1079,7 @@ hipError_t launch_thin_t(const RowsProblem &pr, hipStream_t s);
 template <typename T>
 hipError_t launch_grad_t(const GradProblem &pr, hipStream_t s);
 template <typename T>
-hipError_t launch_both_t(const RowsProblem &r, const GradProblem &g, hipStream_t s);
+hipError_t launch_both_t(const RowsProblem &r, const GradProblem &g, const SlopeSum &sum,
+                         hipStream_t s);
 
 }  // namespace kx

@@ -12,7 +12,8 @@ hipError_t launch_thin_t(const RowsProblem &pr, hipStream_t s);
 template <typename T>
 hipError_t launch_grad_t(const GradProblem &pr, hipStream_t s);
 template <typename T>
-hipError_t launch_both_t(const RowsProblem &r, const GradProblem &g, hipStream_t s);
+hipError_t launch_both_t(const RowsProblem &r, const GradProblem &g, const SlopeSum &sum,
+                         hipStream_t s);
 
 namespace {
 
@@ -234,30 +235,16 @@ __global__ __launch_bounds__(256) void slope_kernel(const T *__restrict__ dy, in
     }
 }
 
-// 64 columns a block; each of its four waves adds a quarter of the parts.
 template <typename T>
-__global__ __launch_bounds__(256) void slope_sum_kernel(const float *__restrict__ partial,
-                                                        int splits, int64_t n,
-                                                        T *__restrict__ dbias) {
-    __shared__ float quarter[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t i = (int64_t)blockIdx.x * 64 + lane;
-    const int per = (splits + 3) / 4, end = (wave + 1) * per < splits ? (wave + 1) * per : splits;
-    float v = 0.0f;
-    if (i < n) {
-#pragma unroll 8
-        for (int s = wave * per; s < end; ++s) v += partial[s * n + i];
-    }
-    quarter[wave][lane] = v;
-    __syncthreads();
-    if (wave == 0 && i < n)
-        dbias[i] = (T)((quarter[0][lane] + quarter[1][lane]) + (quarter[2][lane] + quarter[3][lane]));
+__global__ __launch_bounds__(256) void slope_sum_kernel(SlopeSum sum) {
+    __shared__ float quarter[256];
+    slope_sum<T>(sum, blockIdx.x, quarter);
 }
 
 template <typename T>
 hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre, int act,
                    const int *offsets, int experts, int64_t rows, int64_t outs, void *dz,
-                   int64_t lddz, void *dbias, float *partial, hipStream_t s) {
+                   int64_t lddz, void *dbias, float *partial, SlopeSum *later, hipStream_t s) {
     constexpr int V = 16 / (int)sizeof(T);
     const int splits = (int)slope_splits(rows, outs, experts);
     const int64_t width = dz && lddz > outs ? lddz : outs;
@@ -269,8 +256,12 @@ hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
     });
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !dbias || splits == 1) return e;
-    const int64_t n = (int64_t)experts * outs;
-    slope_sum_kernel<T><<<(unsigned)cdiv(n, 64), 256, 0, s>>>(partial, splits, n, (T *)dbias);
+    const SlopeSum sum = {partial, splits, (int64_t)experts * outs, dbias};
+    if (later) {
+        *later = sum;
+        return e;
+    }
+    slope_sum_kernel<T><<<(unsigned)cdiv(sum.n, 64), 256, 0, s>>>(sum);
     return hipGetLastError();
 }
 
@@ -390,7 +381,7 @@ int both_plan(int dtype, int64_t rows, int64_t outs, int64_t ins, bool grouped, 
         const int64_t ndx = row_tiles(rows, c.rows, grouped, experts) * cdiv(ins, c.cols);
         const int64_t ndw = cdiv(outs, c.rows) * cdiv(ins, c.cols) * experts;
         const int64_t most = most_row_tiles(rows, c.rows, grouped, experts) * cdiv(ins, c.cols) + ndw;
-        if (most + 256 > kMaxGridThreads / 512) continue;
+        if (most + 256 + cdiv(experts * outs, 64) > kMaxGridThreads / 512) continue;
         const double each = c.each * (on_lines ? 1.0 : c.apart);
         const double tdx = depth_dx * each + c.edge + (grouped ? kSetup : 0.0);
         const double tdw = depth_dw * each + c.edge;
@@ -441,9 +432,10 @@ hipError_t launch_grad(int dtype, const GradProblem &pr, hipStream_t s) {
     if (dtype == 0) return grad_t<float>(pr, s);
     return dtype == 1 ? grad_t<bf16>(pr, s) : grad_t<f16>(pr, s);
 }
-hipError_t launch_both(int dtype, const RowsProblem &r, const GradProblem &g, hipStream_t s) {
-    if (dtype == 0) return launch_both_t<float>(r, g, s);
-    return dtype == 1 ? launch_both_t<bf16>(r, g, s) : launch_both_t<f16>(r, g, s);
+hipError_t launch_both(int dtype, const RowsProblem &r, const GradProblem &g, const SlopeSum &sum,
+                       hipStream_t s) {
+    if (dtype == 0) return launch_both_t<float>(r, g, sum, s);
+    return dtype == 1 ? launch_both_t<bf16>(r, g, sum, s) : launch_both_t<f16>(r, g, sum, s);
 }
 
 hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst,
@@ -466,15 +458,16 @@ int64_t slope_splits(int64_t rows, int64_t outs, int64_t experts) {
 
 hipError_t launch_slope(int dtype, const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
                         int act, const int *offsets, int experts, int64_t rows, int64_t outs,
-                        void *dz, int64_t lddz, void *dbias, float *partial, hipStream_t s) {
+                        void *dz, int64_t lddz, void *dbias, float *partial, SlopeSum *later,
+                        hipStream_t s) {
     if (dtype == 0)
         return slope_t<float>(dy, lddy, pre, ldpre, act, offsets, experts, rows, outs, dz, lddz,
-                              dbias, partial, s);
+                              dbias, partial, later, s);
     if (dtype == 1)
         return slope_t<bf16>(dy, lddy, pre, ldpre, act, offsets, experts, rows, outs, dz, lddz,
-                             dbias, partial, s);
+                             dbias, partial, later, s);
     return slope_t<f16>(dy, lddy, pre, ldpre, act, offsets, experts, rows, outs, dz, lddz, dbias,
-                        partial, s);
+                        partial, later, s);
 }
 
 }  // namespace kx

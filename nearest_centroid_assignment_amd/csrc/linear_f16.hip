@@ -17,8 +17,9 @@ hipError_t launch_grad_t<f16>(const GradProblem &pr, hipStream_t s) {
     return pick_grad<f16>(pr, s);
 }
 template <>
-hipError_t launch_both_t<f16>(const RowsProblem &r, const GradProblem &g, hipStream_t s) {
-    return pick_both<f16>(r, g, s);
+hipError_t launch_both_t<f16>(const RowsProblem &r, const GradProblem &g, const SlopeSum &sum,
+                              hipStream_t s) {
+    return pick_both<f16>(r, g, sum, s);
 }
 
 }  // namespace kx

@@ -16,8 +16,9 @@ hipError_t launch_grad_t<float>(const GradProblem &pr, hipStream_t s) {
     return pick_grad<float>(pr, s);
 }
 template <>
-hipError_t launch_both_t<float>(const RowsProblem &r, const GradProblem &g, hipStream_t s) {
-    return pick_both<float>(r, g, s);
+hipError_t launch_both_t<float>(const RowsProblem &r, const GradProblem &g, const SlopeSum &sum,
+                                hipStream_t s) {
+    return pick_both<float>(r, g, sum, s);
 }
 
 }  // namespace kx
