@@ -377,6 +377,22 @@ def test_linear_options(dtype):
     assert dx.shape == (0, ins) and not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,outs,ins", [(130, 94, 102), (70, 333, 37), (600, 1026, 518)])
+def test_linear_gaps(dtype, rows, outs, ins):
+    """Rows that end inside a 16-byte chunk, NaN between them: nothing of a gap counts."""
+    gu.announce(f"linear gaps {dtype} {rows} x {outs} x {ins}")
+    wide_x, wide_dy = randn(1, rows, ins + 6, dtype=dtype), randn(2, rows, outs + 6, dtype=dtype)
+    w = randn(3, outs, ins, dtype=dtype, scale=ins ** -0.5)
+    x, dy = wide_x[:, :ins], wide_dy[:, :outs]
+    want = (experts.linear(x.contiguous(), w), *experts.linear_backward(dy.contiguous(), x.contiguous(), w))
+    wide_x[:, ins:] = float("nan")
+    wide_dy[:, outs:] = float("nan")
+    got = (experts.linear(x, w), *experts.linear_backward(dy, x, w))
+    for name, g, v in zip(("out", "dx", "dw", "dbias"), got, want):
+        assert torch.equal(g, v), name
+
+
 def test_linear_values():
     """Infinities and NaN reach the outputs that depend on them, and no others."""
     x = torch.zeros(40, 24, dtype=torch.bfloat16, device="cuda")
