@@ -252,12 +252,8 @@ __global__ __launch_bounds__(256) void moments_kernel(const int8_t *__restrict__
 
 template <typename P, typename G>
 hipError_t run(const Batch &b, const AdamwStep &st, hipStream_t s) {
-    const unsigned blocks = (unsigned)b.first[b.count];
-    if (st.bits == 8)
-        adamw_kernel<P, G, true><<<blocks, 256, 0, s>>>(b, st);
-    else
-        adamw_kernel<P, G, false><<<blocks, 256, 0, s>>>(b, st);
-    return hipGetLastError();
+    return launch(st.bits == 8 ? adamw_kernel<P, G, true> : adamw_kernel<P, G, false>,
+                  b.first[b.count], 256, 0, s, b, st);
 }
 template <typename P>
 hipError_t run_grads(const Batch &b, const AdamwStep &st, hipStream_t s) {
@@ -309,9 +305,8 @@ hipError_t launch_moments(const int8_t *m, const uint8_t *v, const float *m_scal
                           const float *v_scale, int64_t elements, float *m_out, float *v_out,
                           hipStream_t s) {
     if (elements == 0) return hipSuccess;
-    moments_kernel<<<(unsigned)cdiv(elements, 1024), 256, 0, s>>>(m, v, m_scale, v_scale, elements,
-                                                                  m_out, v_out);
-    return hipGetLastError();
+    return launch(moments_kernel, cdiv(elements, 1024), 256, 0, s, m, v, m_scale, v_scale, elements,
+                  m_out, v_out);
 }
 
 }  // namespace kx

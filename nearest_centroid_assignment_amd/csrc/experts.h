@@ -6,7 +6,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "launch.h"
+
 namespace kx {
+
+using km::launch;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16;

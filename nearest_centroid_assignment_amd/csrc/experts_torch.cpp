@@ -5,9 +5,11 @@
 // of one call on the current stream with fresh outputs, and either makes that call
 // of the C ABI and returns its outputs, or, when anything is out of the ordinary
 // (a wrong type, shape or device, an empty or strange matrix, a refusal by the
-// library), returns None without having enqueued a kernel: experts.py then takes
-// the call, and words the error if there is one. The entry points are bound by
-// address, so this module links against torch alone.
+// library's checks of arguments), returns None without having enqueued a kernel:
+// experts.py then takes the call, and words the error if there is one. A HIP error
+// may come after a launch, so it is raised here: a step in place must not be made
+// again. The entry points are bound by address, so this module links against torch
+// alone.
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -33,6 +35,7 @@ decltype(&experts_linear) linear_call;
 decltype(&experts_linear_backward) linear_backward_call;
 decltype(&experts_adamw_state_elements) adamw_elements;
 decltype(&experts_adamw_step) adamw_call;
+PyObject *check;  // check(status, name of the entry point) raises
 
 constexpr int64_t kBlock = 256;  // slack of a workspace; elements that share a scale
 
@@ -126,6 +129,16 @@ PyObject *tuple_of(const at::Tensor &a, const at::Tensor &b, const at::Tensor &c
     return r;
 }
 
+// What a status of the C ABI other than KM_OK becomes.
+PyObject *failed(int status, const char *name) {
+    if (status == KM_ERR_HIP) {
+        PyObject *r = PyObject_CallFunction(check, "is", status, name);
+        Py_XDECREF(r);
+        if (!r) return nullptr;
+    }
+    Py_RETURN_NONE;
+}
+
 #define NOT_HERE Py_RETURN_NONE
 #define ARGS(n) \
     if (count != (n)) NOT_HERE
@@ -151,10 +164,10 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t count) {
     at::Tensor order = new_tensor({tokens * top}, at::kInt, dev);
     at::Tensor place = new_tensor({tokens, top}, at::kInt, dev);
     at::Tensor offsets = new_tensor({experts + 1}, at::kInt, dev);
-    if (plan_call((const int64_t *)ids->data_ptr(), tokens, top, experts, (int32_t *)order.data_ptr(),
-                  (int32_t *)place.data_ptr(), (int32_t *)offsets.data_ptr(), ws.p, ws.n,
-                  queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = plan_call(
+        (const int64_t *)ids->data_ptr(), tokens, top, experts, (int32_t *)order.data_ptr(),
+        (int32_t *)place.data_ptr(), (int32_t *)offsets.data_ptr(), ws.p, ws.n, queue(dev));
+    if (status != KM_OK) return failed(status, "experts_plan");
     return tuple_of(order, place, offsets);
     END_HANDLE_TH_ERRORS
 }
@@ -173,9 +186,10 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t count) {
         NOT_HERE;
     const int64_t width = x->size(1);
     at::Tensor xs = new_tensor({p.tokens * p.top, width}, x->scalar_type(), dev);
-    if (dispatch_call(rx.p, rx.ld, code, p.tokens, p.top, width, p.order, p.place, xs.data_ptr(),
-                      width, queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = dispatch_call(
+        rx.p, rx.ld, code, p.tokens, p.top, width, p.order, p.place, xs.data_ptr(), width,
+        queue(dev));
+    if (status != KM_OK) return failed(status, "experts_dispatch");
     return wrap(xs);
     END_HANDLE_TH_ERRORS
 }
@@ -194,9 +208,9 @@ PyObject *dispatch_backward(PyObject *, PyObject *const *a, Py_ssize_t count) {
         NOT_HERE;
     const int64_t width = g->size(1);
     at::Tensor dx = new_tensor({p.tokens, width}, g->scalar_type(), dev);
-    if (dispatch_backward_call(rg.p, rg.ld, code, p.tokens, p.top, width, p.place, dx.data_ptr(),
-                               width, queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = dispatch_backward_call(
+        rg.p, rg.ld, code, p.tokens, p.top, width, p.place, dx.data_ptr(), width, queue(dev));
+    if (status != KM_OK) return failed(status, "experts_dispatch_backward");
     return wrap(dx);
     END_HANDLE_TH_ERRORS
 }
@@ -217,9 +231,9 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (!w) NOT_HERE;
     const int64_t width = ys->size(1);
     at::Tensor y = new_tensor({p.tokens, width}, ys->scalar_type(), dev);
-    if (combine_call(ry.p, ry.ld, w, code, p.tokens, p.top, width, p.place, y.data_ptr(), width,
-                     queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = combine_call(
+        ry.p, ry.ld, w, code, p.tokens, p.top, width, p.place, y.data_ptr(), width, queue(dev));
+    if (status != KM_OK) return failed(status, "experts_combine");
     return wrap(y);
     END_HANDLE_TH_ERRORS
 }
@@ -242,10 +256,10 @@ PyObject *combine_backward(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (!w) NOT_HERE;
     at::Tensor dys = new_tensor({p.tokens * p.top, width}, dy->scalar_type(), dev);
     at::Tensor dw = new_tensor({p.tokens, p.top}, at::kFloat, dev);
-    if (combine_backward_call(rg.p, rg.ld, ry.p, ry.ld, w, code, p.tokens, p.top, width, p.order,
-                              p.place, dys.data_ptr(), width, (float *)dw.data_ptr(),
-                              queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = combine_backward_call(
+        rg.p, rg.ld, ry.p, ry.ld, w, code, p.tokens, p.top, width, p.order, p.place,
+        dys.data_ptr(), width, (float *)dw.data_ptr(), queue(dev));
+    if (status != KM_OK) return failed(status, "experts_combine_backward");
     return tuple_of(dys, dw);
     END_HANDLE_TH_ERRORS
 }
@@ -301,10 +315,11 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t count) {
     at::Tensor out = new_tensor({rows, w.outs}, type, dev), pre;
     const int save = PyObject_IsTrue(a[6]);
     if (save) pre = new_tensor({rows, w.outs}, type, dev);
-    if (linear_call(rx.p, rx.ld, w.w, bias, rr.p, rr.ld, w.offsets, code, act, rows, w.outs, w.ins,
-                    w.experts, out.data_ptr(), w.outs, save ? pre.data_ptr() : nullptr, w.outs, ws.p,
-                    ws.n, queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = linear_call(
+        rx.p, rx.ld, w.w, bias, rr.p, rr.ld, w.offsets, code, act, rows, w.outs, w.ins,
+        w.experts, out.data_ptr(), w.outs, save ? pre.data_ptr() : nullptr, w.outs, ws.p, ws.n,
+        queue(dev));
+    if (status != KM_OK) return failed(status, "experts_linear");
     return save ? tuple_of(out, pre) : wrap(out);
     END_HANDLE_TH_ERRORS
 }
@@ -339,12 +354,12 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (need_dx) dx = new_tensor({rows, w.ins}, type, dev);
     if (need_dw) dw = new_tensor(THPVariable_Unpack(a[2]).sizes(), type, dev);
     if (need_db) db = new_tensor(w.lead, type, dev);
-    if (linear_backward_call(rg.p, rg.ld, rx.p, rx.ld, w.w, rp.p, rp.ld, ri.p, ri.ld, w.offsets, code,
-                             act, in_act, rows, w.outs, w.ins, w.experts,
-                             need_dx ? dx.data_ptr() : nullptr, w.ins,
-                             need_dw ? dw.data_ptr() : nullptr, need_db ? db.data_ptr() : nullptr,
-                             ws.p, ws.n, queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = linear_backward_call(
+        rg.p, rg.ld, rx.p, rx.ld, w.w, rp.p, rp.ld, ri.p, ri.ld, w.offsets, code, act, in_act,
+        rows, w.outs, w.ins, w.experts, need_dx ? dx.data_ptr() : nullptr, w.ins,
+        need_dw ? dw.data_ptr() : nullptr, need_db ? db.data_ptr() : nullptr, ws.p, ws.n,
+        queue(dev));
+    if (status != KM_OK) return failed(status, "experts_linear_backward");
     return tuple_of(dx, dw, db);
     END_HANDLE_TH_ERRORS
 }
@@ -415,17 +430,18 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t count) {
         PyErr_Clear();
         NOT_HERE;
     }
-    if (adamw_call(pp.data(), pg.data(), a[12] == Py_None ? nullptr : pk.data(), numels.data(), n,
-                   code_of(pt), code_of(gt), pm, pv, ms, vs, bits, h[0], h[1], h[2], h[3], h[4], step,
-                   gs, queue(dev)) != KM_OK)
-        NOT_HERE;
+    const int status = adamw_call(
+        pp.data(), pg.data(), a[12] == Py_None ? nullptr : pk.data(), numels.data(), n,
+        code_of(pt), code_of(gt), pm, pv, ms, vs, bits, h[0], h[1], h[2], h[3], h[4], step, gs,
+        queue(dev));
+    if (status != KM_OK) return failed(status, "experts_adamw_step");
     Py_RETURN_TRUE;
     END_HANDLE_TH_ERRORS
 }
 
-// ({name: address of the C entry point}) -> None
+// ({name: address of the C entry point}, check) -> None
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t count) {
-    if (count != 1 || !PyDict_Check(a[0])) {
+    if (count < 1 || !PyDict_Check(a[0])) {
         PyErr_SetString(PyExc_TypeError, "bind takes a dict of addresses");
         return nullptr;
     }
@@ -451,6 +467,12 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t count) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: an entry point is missing");
         return nullptr;
     }
+    if (count != 2 || !PyCallable_Check(a[1])) {
+        PyErr_SetString(PyExc_TypeError, "bind takes a dict of addresses and the check of a status");
+        return nullptr;
+    }
+    Py_INCREF(a[1]);
+    Py_XSETREF(check, a[1]);
     Py_RETURN_NONE;
 }
 

@@ -875,22 +875,19 @@ int64_t grad_blocks(const GradProblem &pr) {
 
 template <class S>
 hipError_t run_rows(const RowsProblem &pr, hipStream_t s) {
-    rows_kernel<S><<<(unsigned)rows_blocks<S>(pr), S::NW * 64, 0, s>>>(RowsArgs{pr, kWalk});
-    return hipGetLastError();
+    return launch(rows_kernel<S>, rows_blocks<S>(pr), S::NW * 64, 0, s, RowsArgs{pr, kWalk});
 }
 template <class S>
 hipError_t run_grad(const GradProblem &pr, hipStream_t s) {
-    grad_kernel<S><<<(unsigned)grad_blocks<S>(pr), S::NW * 64, 0, s>>>(pr);
-    return hipGetLastError();
+    return launch(grad_kernel<S>, grad_blocks<S>(pr), S::NW * 64, 0, s, pr);
 }
 template <class SR, class SG>
 hipError_t run_both(const RowsProblem &r, const GradProblem &g, const SlopeSum &sum, hipStream_t s) {
     const int64_t nr = rows_blocks<SR>(r), ng = grad_blocks<SG>(g);
     const bool rows_first = r.depth * g.experts >= g.rows;
     const int64_t ns = sum.splits ? cdiv(sum.n, 64) : 0;
-    both_kernel<SR, SG><<<(unsigned)(nr + ng + ns), SR::NW * 64, 0, s>>>(
-        RowsArgs{r, kWalk}, g, (int)(rows_first ? nr : ng), rows_first, (int)(nr + ng), sum);
-    return hipGetLastError();
+    return launch(both_kernel<SR, SG>, nr + ng + ns, SR::NW * 64, 0, s, RowsArgs{r, kWalk}, g,
+                  (int)(rows_first ? nr : ng), rows_first, (int)(nr + ng), sum);
 }
 
 // The tiles of a type: forward product (PMC false), dx (PMC true), dw.
@@ -1062,8 +1059,7 @@ __global__ __launch_bounds__(512) void thin_kernel(RowsProblem pr) {
 template <typename T, int MT>
 hipError_t run_thin(const RowsProblem &pr, hipStream_t s) {
     const int64_t tiles = most_row_tiles(pr.rows, 16 * MT, pr.offsets != nullptr, pr.experts);
-    thin_kernel<T, MT><<<(unsigned)(tiles * cdiv(pr.cols, 16)), 512, 0, s>>>(pr);
-    return hipGetLastError();
+    return launch(thin_kernel<T, MT>, tiles * cdiv(pr.cols, 16), 512, 0, s, pr);
 }
 template <typename T>
 hipError_t pick_thin(const RowsProblem &pr, hipStream_t s) {

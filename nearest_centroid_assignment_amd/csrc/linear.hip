@@ -133,16 +133,14 @@ template <typename T>
 hipError_t rows_t(const RowsProblem &pr, bool thin, hipStream_t s) {
     const hipError_t e = thin ? launch_thin_t<T>(pr, s) : launch_rows_t<T>(pr, s);
     if (e != hipSuccess || pr.splits == 1) return e;
-    join_rows_kernel<T><<<(unsigned)cdiv(pr.rows * cdiv(pr.cols, 8), 256), 256, 0, s>>>(pr);
-    return hipGetLastError();
+    return launch(join_rows_kernel<T>, cdiv(pr.rows * cdiv(pr.cols, 8), 256), 256, 0, s, pr);
 }
 template <typename T>
 hipError_t grad_t(const GradProblem &pr, hipStream_t s) {
     const hipError_t e = launch_grad_t<T>(pr, s);
     if (e != hipSuccess || pr.splits == 1) return e;
     const int64_t n = pr.m_cols * pr.n_cols * pr.experts;
-    join_grad_kernel<T><<<(unsigned)cdiv(n, 1024), 256, 0, s>>>(pr.partial, pr.splits, n, (T *)pr.out);
-    return hipGetLastError();
+    return launch(join_grad_kernel<T>, cdiv(n, 1024), 256, 0, s, pr.partial, pr.splits, n, (T *)pr.out);
 }
 
 // One block: 64 * V columns (a lane has V of them) of the rows of part s of
@@ -249,20 +247,19 @@ hipError_t slope_t(const void *dy, int64_t lddy, const void *pre, int64_t ldpre,
     const int splits = (int)slope_splits(rows, outs, experts);
     const int64_t width = dz && lddz > outs ? lddz : outs;
     const int64_t cb = cdiv(width, 64 * V);
+    hipError_t e = hipSuccess;
     with_act(act, [&](auto tag) {
-        slope_kernel<T, V, decltype(tag)::value><<<(unsigned)(cb * splits * experts), 256, 0, s>>>(
-            (const T *)dy, lddy, (const T *)pre, ldpre, offsets, experts, rows, outs, (T *)dz, lddz,
-            (T *)dbias, partial, splits, (int)cb);
+        e = launch(slope_kernel<T, V, decltype(tag)::value>, cb * splits * experts, 256, 0, s,
+                   (const T *)dy, lddy, (const T *)pre, ldpre, offsets, experts, rows, outs, (T *)dz,
+                   lddz, (T *)dbias, partial, splits, (int)cb);
     });
-    hipError_t e = hipGetLastError();
     if (e != hipSuccess || !dbias || splits == 1) return e;
     const SlopeSum sum = {partial, splits, (int64_t)experts * outs, dbias};
     if (later) {
         *later = sum;
         return e;
     }
-    slope_sum_kernel<T><<<(unsigned)cdiv(sum.n, 64), 256, 0, s>>>(sum);
-    return hipGetLastError();
+    return launch(slope_sum_kernel<T>, cdiv(sum.n, 64), 256, 0, s, sum);
 }
 
 }  // namespace
@@ -441,9 +438,8 @@ hipError_t launch_both(int dtype, const RowsProblem &r, const GradProblem &g, co
 hipError_t launch_pad_rows(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst,
                            int64_t ldd, hipStream_t s) {
     if (rows == 0) return hipSuccess;
-    pad_rows_kernel<<<(unsigned)cdiv(rows * (ldd / 8), 256), 256, 0, s>>>(
-        (const uint16_t *)src, lds, rows, cols, (uint16_t *)dst, ldd);
-    return hipGetLastError();
+    return launch(pad_rows_kernel, cdiv(rows * (ldd / 8), 256), 256, 0, s, (const uint16_t *)src, lds,
+                  rows, cols, (uint16_t *)dst, ldd);
 }
 
 // Parts of an expert's rows: about 4096 blocks in all, 16 rows a part at least (one

@@ -460,15 +460,12 @@ How how(int64_t tokens, int64_t top, int64_t width, int64_t ld) {
     return {tokens >= 4096, lines && tokens * top * width * (int64_t)sizeof(T) > 256 << 20};
 }
 
-#define KX_ROWS(kernel, rows, ...)                                                            \
-    do {                                                                                      \
-        if (h.wave && h.once)                                                                 \
-            kernel<T, 64, true __VA_ARGS__><<<(unsigned)cdiv(rows, 4), 256, 0, s>>> KX_ARGS;  \
-        else if (h.wave)                                                                      \
-            kernel<T, 64, false __VA_ARGS__><<<(unsigned)cdiv(rows, 4), 256, 0, s>>> KX_ARGS; \
-        else                                                                                  \
-            kernel<T, 256, false __VA_ARGS__><<<(unsigned)(rows), 256, 0, s>>> KX_ARGS;       \
-        return hipGetLastError();                                                             \
+#define KX_ROWS(kernel, rows, ...)                                                              \
+    do {                                                                                        \
+        if (h.wave)                                                                             \
+            return launch(h.once ? kernel<T, 64, true __VA_ARGS__> : kernel<T, 64, false __VA_ARGS__>, \
+                          cdiv(rows, 4), 256, 0, s, KX_ARGS);                                   \
+        return launch(kernel<T, 256, false __VA_ARGS__>, rows, 256, 0, s, KX_ARGS);             \
     } while (0)
 
 template <typename T>
@@ -477,7 +474,7 @@ struct Rows {
                                int64_t width, const int *order, const int *place, void *xs,
                                int64_t ldxs, hipStream_t s) {
         const How h = how<T>(tokens, top, width, ldxs);
-#define KX_ARGS ((const T *)x, ldx, tokens, top, width, order, place, (T *)xs, ldxs)
+#define KX_ARGS (const T *)x, ldx, tokens, top, width, order, place, (T *)xs, ldxs
         KX_ROWS(dispatch_kernel, tokens);
 #undef KX_ARGS
     }
@@ -485,7 +482,7 @@ struct Rows {
                               int64_t top, int64_t width, const int *place, void *y, int64_t ldy,
                               hipStream_t s) {
         const How h = how<T>(tokens, top, width, ldys);
-#define KX_ARGS ((const T *)ys, ldys, weights, tokens, top, width, place, (T *)y, ldy)
+#define KX_ARGS (const T *)ys, ldys, weights, tokens, top, width, place, (T *)y, ldy
         if (weights)
             KX_ROWS(combine_kernel, tokens, , true);
         else
@@ -499,9 +496,9 @@ struct Rows {
         How h = how<T>(tokens, top, width, dys ? lddys : ldys);
         const int64_t pairs = tokens * top;
         h.wave = pairs >= 4096;
-#define KX_ARGS                                                                              \
-    ((const T *)dy, lddy, (const T *)ys, ldys, weights, pairs, top, width, order, place, (T *)dys, \
-     lddys, dweights)
+#define KX_ARGS                                                                                 \
+    (const T *)dy, lddy, (const T *)ys, ldys, weights, pairs, top, width, order, place, (T *)dys, \
+        lddys, dweights
         KX_ROWS(combine_backward_kernel, pairs);
 #undef KX_ARGS
     }
@@ -517,31 +514,29 @@ hipError_t launch_plan(const int64_t *ids, int64_t pairs, int64_t experts, int *
                        int *offsets, const PlanScratch &ws, hipStream_t s) {
     if (plan_is_small(pairs, experts)) {
         const size_t lds = (size_t)cdiv(pairs, 64) * experts * sizeof(unsigned short);
-        plan_small_kernel<<<1, 1024, lds, s>>>(ids, (int)pairs, (int)experts, order, place, offsets);
-        return hipGetLastError();
+        return launch(plan_small_kernel, 1, 1024, lds, s, ids, (int)pairs, (int)experts, order, place,
+                      offsets);
     }
     if (ws.tiles <= kPlaceTiles && experts <= kPlaceExperts) {
         const size_t lds = (size_t)16 * experts * sizeof(unsigned short);
-        plan_rank_kernel<<<(unsigned)ws.tiles, 1024, lds, s>>>(ids, pairs, (int)experts,
-                                                               ws.tile_hist, ws.rank);
-        plan_place_kernel<<<(unsigned)ws.tiles, 1024, 0, s>>>(ids, pairs, (int)experts, (int)ws.tiles,
-                                                              ws.tile_hist, ws.rank, order, place,
-                                                              offsets);
-        return hipGetLastError();
+        const hipError_t e = launch(plan_rank_kernel, ws.tiles, 1024, lds, s, ids, pairs, (int)experts,
+                                    ws.tile_hist, ws.rank);
+        if (e != hipSuccess) return e;
+        return launch(plan_place_kernel, ws.tiles, 1024, 0, s, ids, pairs, (int)experts, (int)ws.tiles,
+                      ws.tile_hist, ws.rank, order, place, offsets);
     }
     km::UpdateScratch us = {};
     us.tile_hist = ws.tile_hist;
     us.rank = ws.rank;
     us.n_tiles = ws.tiles;
-    const hipError_t e = km::launch_rank_hist(ids, pairs, experts, us, km::Gate{}, s);
-    if (e != hipSuccess) return e;
-    plan_tiles_kernel<<<(unsigned)cdiv(experts, 64), 64, 0, s>>>(ws.tile_hist, experts, ws.tiles,
-                                                                 ws.count);
-    plan_scan_kernel<<<1, 1024, 0, s>>>(ws.count, experts, offsets);
-    if (pairs > 0)
-        plan_scatter_kernel<<<(unsigned)cdiv(pairs, 256), 256, 0, s>>>(
-            ids, pairs, experts, ws.tile_hist, ws.rank, offsets, order, place);
-    return hipGetLastError();
+    hipError_t e = km::launch_rank_hist(ids, pairs, experts, us, km::Gate{}, s);
+    if (e == hipSuccess)
+        e = launch(plan_tiles_kernel, cdiv(experts, 64), 64, 0, s, ws.tile_hist, experts, ws.tiles,
+                   ws.count);
+    if (e == hipSuccess) e = launch(plan_scan_kernel, 1, 1024, 0, s, ws.count, experts, offsets);
+    if (e != hipSuccess || pairs == 0) return e;
+    return launch(plan_scatter_kernel, cdiv(pairs, 256), 256, 0, s, ids, pairs, experts, ws.tile_hist,
+                  ws.rank, offsets, order, place);
 }
 
 #define KX_BY_TYPE(call)                        \

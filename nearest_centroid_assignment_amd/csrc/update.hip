@@ -31,6 +31,7 @@
 // sample order, so the float64 sum and divide are exactly the plain definition
 // of the mean; larger clusters add sixteen contiguous parts of their rows.
 #include "kernels.h"
+#include "launch.h"
 
 namespace km {
 namespace {
@@ -852,13 +853,10 @@ hipError_t launch_rank_hist_impl(const int64_t *labels, unsigned long long *keys
                                  const UpdateScratch &ws, Gate gate, hipStream_t stream) {
     if (n <= 0) return hipSuccess;  // no tile (the tile prefix then gives every size 0)
     const unsigned blocks = (unsigned)ws.n_tiles;
-    if (k <= kRankLdsMax)
-        rank_hist_kernel<true, kFromKeys><<<blocks, kTile, (size_t)k * sizeof(int), stream>>>(
-            labels, keys, min_dist, add_norm, n, k, ws.tile_hist, ws.rank, gate);
-    else
-        rank_hist_kernel<false, kFromKeys><<<blocks, kTile, 0, stream>>>(
-            labels, keys, min_dist, add_norm, n, k, ws.tile_hist, ws.rank, gate);
-    return hipGetLastError();
+    const bool in_lds = k <= kRankLdsMax;
+    return launch(in_lds ? rank_hist_kernel<true, kFromKeys> : rank_hist_kernel<false, kFromKeys>,
+                  blocks, kTile, in_lds ? (size_t)k * sizeof(int) : 0, stream, labels, keys, min_dist,
+                  add_norm, n, k, ws.tile_hist, ws.rank, gate);
 }
 
 template <int kSplit>

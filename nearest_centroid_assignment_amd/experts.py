@@ -50,7 +50,7 @@ def _load_native(L, names):
     spec = importlib.util.spec_from_file_location("_experts_torch", path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
-    module.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names})
+    module.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _check)
     return module
 
 
@@ -101,7 +101,8 @@ def _module():
 # outputs on the current stream is therefore first offered to the native module,
 # which takes it or, where anything about it is unusual, leaves it to the Python
 # below (None): other streams, given outputs and workspaces, empty matrices, and
-# everything that is to be refused. Both end in the same C entry point.
+# everything that is to be refused. Both end in the same C entry point. An error of a
+# launch is raised by whichever made it, and the call is not made again.
 
 
 def _refuse(t, dtype, shape, dev, name):

@@ -1,0 +1,97 @@
+"""The expert operators at their edges: errors of a launch, extreme values, sizes
+between the ways that a call can be taken, and memory that is shared or viewed."""
+import ctypes
+import importlib.util
+import os
+import shutil
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from nearest_centroid_assignment_amd import binding, build, experts  # noqa: E402
+from tests import gpu_util as gu  # noqa: E402
+from tests.test_gpu_experts import (TYPES, close, encode, f64, make_ids, np32, randn,  # noqa: E402
+                                    summed)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+# ------------------------------------------------------------- failed launches
+
+
+def test_error_of_another_call():
+    """An error that some other call of the process has left behind is not this
+    step's: the step is applied, once."""
+    L = experts.lib()
+    ways = []
+    for stale in (False, True):
+        p, g = [randn(i, 3000) for i in range(70)], [randn(100 + i, 3000) for i in range(70)]
+        state = experts.adamw_state(p)
+        torch.cuda.synchronize()
+        if stale:
+            assert L.hipSetDevice(1 << 20) != 0
+        try:
+            experts.adamw_step(p, g, lr=0.1, **state)
+        finally:
+            L.hipGetLastError()
+        ways.append(p + list(state.values()))
+    for a, b in zip(*ways):
+        assert torch.equal(a, b)
+
+
+NATIVE = ("plan", "dispatch", "dispatch_backward", "combine", "combine_backward", "linear",
+          "linear_backward", "adamw_step")
+
+
+def native_copy(tmp_path, stubs):
+    """A second copy of the native module, some of whose entry points are `stubs`."""
+    path = shutil.copy(build.TORCH_MODULE_PATH, os.path.join(tmp_path, "_experts_torch.so"))
+    spec = importlib.util.spec_from_file_location("_experts_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    L = experts.lib()
+    address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+    names = [f"experts_{n}" for n in NATIVE] + [f"experts_{n}" for n in (
+        "plan_workspace_bytes", "linear_workspace_bytes", "adamw_state_elements")]
+    module.bind({n: address(stubs.get(n, getattr(L, n))) for n in names}, binding._check)
+    return module
+
+
+def ordinary_calls():
+    ids, x = make_ids(1, 10, 2, 3).cuda(), randn(1, 10, 16)
+    p = experts.plan(ids, 3)
+    xs, w, weights = randn(2, 20, 16), randn(3, 24, 16), randn(4, 10, 2)
+    q, g = [randn(5, 300)], [randn(6, 300)]
+    s = experts.adamw_state(q)
+    return dict(plan=(ids, 3), dispatch=(x, p), dispatch_backward=(xs, p), combine=(xs, weights, p),
+                combine_backward=(x, xs, weights, p), linear=(xs, w, None, None, 0, None, False),
+                linear_backward=(randn(7, 20, 24), xs, w, None, 0, None, None, 0, True, True, True),
+                adamw_step=(q, g, s["m"], s["v"], 0.1, 0.9, 0.99, 1e-8, 0.0, 1, None, None, None, None))
+
+
+@pytest.mark.parametrize("name", NATIVE)
+def test_failed_launch_is_not_repeated(name, tmp_path):
+    """A status that a launch may have preceded raises; one that validation gives
+    leaves the call to Python."""
+    counted, status = [], 0
+
+    def entry():
+        counted.append(name)
+        return status
+
+    stub = ctypes.CFUNCTYPE(ctypes.c_int)(entry)
+    native, args = native_copy(tmp_path, {f"experts_{name}": stub}), ordinary_calls()[name]
+    status = -2  # KM_ERR_SHAPE
+    assert getattr(native, name)(*args) is None and len(counted) == 1
+    status = -6  # KM_ERR_HIP
+    with pytest.raises(binding.KMeansError) as e:
+        getattr(native, name)(*args)
+    assert e.value.status == -6 and len(counted) == 2
