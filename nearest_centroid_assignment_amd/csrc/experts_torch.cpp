@@ -445,24 +445,25 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t count) {
         PyErr_SetString(PyExc_TypeError, "bind takes a dict of addresses");
         return nullptr;
     }
-    bool whole = true;
-    auto get = [&](const char *name, auto &f) {
-        PyObject *v = PyDict_GetItemString(a[0], name);
-        void *p = v ? PyLong_AsVoidPtr(v) : nullptr;
-        whole &= p != nullptr;
-        f = (std::remove_reference_t<decltype(f)>)p;
+    // All of them, or none: a module whose bind was refused stays as it was.
+    auto each = [&](auto visit) {
+        visit("experts_plan_workspace_bytes", plan_bytes);
+        visit("experts_plan", plan_call);
+        visit("experts_dispatch", dispatch_call);
+        visit("experts_dispatch_backward", dispatch_backward_call);
+        visit("experts_combine", combine_call);
+        visit("experts_combine_backward", combine_backward_call);
+        visit("experts_linear_workspace_bytes", linear_bytes);
+        visit("experts_linear", linear_call);
+        visit("experts_linear_backward", linear_backward_call);
+        visit("experts_adamw_state_elements", adamw_elements);
+        visit("experts_adamw_step", adamw_call);
     };
-    get("experts_plan_workspace_bytes", plan_bytes);
-    get("experts_plan", plan_call);
-    get("experts_dispatch", dispatch_call);
-    get("experts_dispatch_backward", dispatch_backward_call);
-    get("experts_combine", combine_call);
-    get("experts_combine_backward", combine_backward_call);
-    get("experts_linear_workspace_bytes", linear_bytes);
-    get("experts_linear", linear_call);
-    get("experts_linear_backward", linear_backward_call);
-    get("experts_adamw_state_elements", adamw_elements);
-    get("experts_adamw_step", adamw_call);
+    bool whole = true;
+    each([&](const char *name, auto &) {
+        PyObject *v = PyDict_GetItemString(a[0], name);
+        whole = whole && v && PyLong_AsVoidPtr(v);
+    });
     if (!whole) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "bind: an entry point is missing");
         return nullptr;
@@ -471,6 +472,9 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t count) {
         PyErr_SetString(PyExc_TypeError, "bind takes a dict of addresses and the check of a status");
         return nullptr;
     }
+    each([&](const char *name, auto &f) {
+        f = (std::remove_reference_t<decltype(f)>)PyLong_AsVoidPtr(PyDict_GetItemString(a[0], name));
+    });
     Py_INCREF(a[1]);
     Py_XSETREF(check, a[1]);
     Py_RETURN_NONE;

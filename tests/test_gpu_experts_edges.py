@@ -95,3 +95,13 @@ def test_failed_launch_is_not_repeated(name, tmp_path):
     with pytest.raises(binding.KMeansError) as e:
         getattr(native, name)(*args)
     assert e.value.status == -6 and len(counted) == 2
+
+
+def test_incomplete_bind(tmp_path):
+    """A bind that is refused leaves the entry points as they were."""
+    native = native_copy(tmp_path, {})
+    with pytest.raises(ValueError):
+        native.bind({})
+    ids = make_ids(1, 10, 2, 3).cuda()
+    for a, b in zip(native.plan(ids, 3), experts.plan(ids, 3)):
+        assert torch.equal(a, b)
