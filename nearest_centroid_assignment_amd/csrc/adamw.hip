@@ -117,12 +117,14 @@ __device__ __forceinline__ int encode_v(float v, float scale) {
 // Before rounding they are then within 6e-5 (m: 127 times 2.7e-7, and as IEEE's own
 // roundings 2e-5) or 1.2e-4 (v: 255 times 2.9e-7, and 4e-5) of what encode_m and
 // encode_v round, so a code can differ only within 2e-4 of a half: there, in one
-// block of ten, the wave takes the exact form. Scales below 1e-30, whose reciprocal
-// or quotients may leave the normal range, take it always.
+// block of ten, the wave takes the exact form. Blocks whose quotients or reciprocal of
+// the scale may leave the normal range (the hardware's reciprocal is 0 there) take it
+// always: scales below 1e-30 or above 8e37, just under 2^126, and NaN.
 // (189 million elements: all exact 740 us, VALU bound; so 540 to 575.)
 constexpr float kNearHalf = 0.4998f;
+__device__ __forceinline__ bool plain_scale(float scale) { return scale >= 1e-30f && scale <= 8e37f; }
 __device__ __forceinline__ void encode_m4(const float (&m)[4], float scale, int8_t (&q)[4]) {
-    bool exact = !(scale >= 1e-30f);
+    bool exact = !plain_scale(scale);
     const float inv = __builtin_amdgcn_rcpf(scale);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -137,7 +139,7 @@ __device__ __forceinline__ void encode_m4(const float (&m)[4], float scale, int8
     }
 }
 __device__ __forceinline__ void encode_v4(const float (&v)[4], float scale, uint8_t (&q)[4]) {
-    bool exact = !(scale >= 1e-30f);
+    bool exact = !plain_scale(scale);
     const float inv = __builtin_amdgcn_rcpf(scale);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {

@@ -105,3 +105,30 @@ def test_incomplete_bind(tmp_path):
     ids = make_ids(1, 10, 2, 3).cuda()
     for a, b in zip(native.plan(ids, 3), experts.plan(ids, 3)):
         assert torch.equal(a, b)
+
+
+# -------------------------------------------------------------- extreme values
+
+
+def test_adamw_8_bit_scales():
+    """Codes of blocks whose scales lie at either end of float32's range: those of
+    the float32 formulas. With beta = 0 a block's moments are g and g^2."""
+    sizes = [1e38, 3.2e38, 8.6e37, 8.4e37, 1.1e37, 9e36, 1.8e19, 1.2e19, 3.1e18, 1.0, 1e-15, 1e-16, 2e-19,
+             0.9e-30, 1e-31, 1e-37, 1e-40, 0.0]
+    rng = np.random.default_rng(5)
+    g = (rng.uniform(-1, 1, (len(sizes), 256)) * np.array(sizes)[:, None]).astype(np.float32).reshape(-1)
+    p = [torch.zeros(g.size, device="cuda")]
+    state = experts.adamw_state(p, 8)
+    experts.adamw_step(p, [torch.from_numpy(g).cuda()], lr=1e-3, betas=(0.0, 0.0), **state)
+    with np.errstate(over="ignore", under="ignore"):
+        mq, vq, ms, vs = encode(g, g * g)
+    finite = np.isfinite(vs)
+    vq = np.where(finite[:, None], vq.reshape(-1, 256), 0).reshape(-1)  # a NaN scale has codes 0
+    assert finite.sum() == len(sizes) - 6
+    assert np.array_equal(np32(state["m_scale"]), ms)
+    assert np.array_equal(np32(state["v_scale"])[finite], vs[finite])
+    assert np.isnan(np32(state["v_scale"])[~finite]).all()
+    for name, want in (("m", mq), ("v", vq)):
+        got = state[name].cpu().numpy()
+        for i, size in enumerate(sizes):
+            assert np.array_equal(got[256 * i:256 * i + 256], want[256 * i:256 * i + 256]), f"{name}, size {size}"
