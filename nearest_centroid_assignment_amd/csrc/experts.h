@@ -106,18 +106,21 @@ __device__ __forceinline__ float act_of(float z) {
     if (ACT == kActSilu) return z * sigmoid(z);
     return z;
 }
-// act'(z). With s = sigmoid(u(z)): (z s)' = s + z s (1 - s) u'.
+// act'(z). With s = sigmoid(u(z)): (z s)' = s + z s (1 - s) u'. Where s (1 - s) rounds to
+// 0 the slope is s, 0 or 1: the other factors may be infinite there (u' from 2e19 on, z
+// where a 16-bit pre was too large for its type), and 0 times them a NaN.
+__device__ __forceinline__ float slope_from(float z, float s, float du) {
+    const float bend = s * (1.0f - s);
+    return bend == 0.0f ? s : s + z * bend * du;
+}
 template <int ACT>
 __device__ __forceinline__ float slope_of(float z) {
     if (ACT == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
     if (ACT == kActGelu) {
         const float s = sigmoid(z * (kGelu1 + kGelu3 * z * z));
-        return s + z * s * (1.0f - s) * (kGelu1 + 3.0f * kGelu3 * z * z);
+        return slope_from(z, s, kGelu1 + 3.0f * kGelu3 * z * z);
     }
-    if (ACT == kActSilu) {
-        const float s = sigmoid(z);
-        return s + z * s * (1.0f - s);
-    }
+    if (ACT == kActSilu) return slope_from(z, sigmoid(z), 1.0f);
     return 1.0f;
 }
 template <int ACT>

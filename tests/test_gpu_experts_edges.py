@@ -132,3 +132,27 @@ def test_adamw_8_bit_scales():
         got = state[name].cpu().numpy()
         for i, size in enumerate(sizes):
             assert np.array_equal(got[256 * i:256 * i + 256], want[256 * i:256 * i + 256]), f"{name}, size {size}"
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+@pytest.mark.parametrize("rows", [1, 130, 700])
+def test_slope_far_from_zero(dtype, act, rows):
+    """Far from zero the slopes are 1 and 0, also where z^2 leaves the range and,
+    for a pre that was stored as an infinity, there."""
+    n = 264
+    far = [200.0, 65504.0, float("inf")] + ([] if dtype == torch.float16 else [1e13, 5e18, 2e19, 7e19, 1e25, 3.3e38])
+    far = torch.tensor(far + [-v for v in far]).to(dtype).cuda()
+    z = far[torch.arange(rows * n, device="cuda") % far.numel()].reshape(rows, n)
+    dy = randn(1, rows, n, dtype=dtype)
+    eye = torch.eye(n, device="cuda").to(dtype)
+    want = torch.where(z > 0, dy, torch.zeros_like(dy))
+    dx, dw, db = experts.linear_backward(dy, eye[:1].expand(rows, n).contiguous(), eye, pre=z, act=act)
+    assert torch.equal(dx, want)
+    close(db, f64(want).sum(0), summed(rows) * f64(want).abs().sum(0), "dbias")
+    close(dw[:, 0], f64(want).sum(0), summed(rows) * f64(want).abs().sum(0), "dw")
+    assert not dw[:, 1:].any()
+    dx = experts.linear_backward(dy, dy, eye, in_pre=z, in_act=act, need_dw=False, need_dbias=False)[0]
+    assert torch.equal(dx, want)
+    z[0, 0] = float("nan")
+    assert torch.isnan(experts.linear_backward(dy, dy, eye, pre=z, act=act)[0][0, 0])
