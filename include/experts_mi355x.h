@@ -152,7 +152,8 @@ int experts_linear_backward(const void *dy, int64_t lddy, const void *x, int64_t
  * all in float32; p is rounded once when its type is 16 bits wide.
  *   params, grads, copies  HOST arrays of `count` device pointers, read during
  *            the call; copies (or NULL) receives the new parameters in bfloat16.
- *            A bfloat16 parameter may be its own copy.
+ *            A bfloat16 parameter may be its own copy; else what is written
+ *            overlaps nothing of the call (a tied weight is given once).
  *            Elements are dense. param_dtype and grad_dtype hold for all.
  *   numels   HOST array of the tensors' lengths (>= 0).
  *   m, v     device moments of all tensors in one array each: a tensor's start

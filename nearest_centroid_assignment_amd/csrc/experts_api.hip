@@ -5,6 +5,9 @@
 // kernels on the caller's stream. Nothing here allocates, waits or keeps state.
 #include <math.h>
 
+#include <algorithm>
+#include <new>
+
 #include "../../include/experts_mi355x.h"
 #include "experts.h"
 #include "kernels.h"
@@ -57,6 +60,21 @@ int check_alias(const Span *outs, int n_outs, const Span *ins, int n_ins) {
             if (overlap(outs[i], outs[j])) return KM_ERR_ALIAS;
     }
     return KM_OK;
+}
+// Whether a range that is written overlaps any other range. Sorts them.
+struct Range {
+    uintptr_t lo, hi;
+    bool written;
+};
+bool any_overlap(Range *r, int64_t n) {
+    std::sort(r, r + n, [](const Range &a, const Range &b) { return a.lo < b.lo; });
+    uintptr_t written_to = 0, to = 0;  // ends of the ranges so far
+    for (int64_t i = 0; i < n; ++i) {
+        if (r[i].lo < (r[i].written ? to : written_to)) return true;
+        to = std::max(to, r[i].hi);
+        if (r[i].written) written_to = std::max(written_to, r[i].hi);
+    }
+    return false;
 }
 int status(hipError_t e) { return e == hipSuccess ? KM_OK : KM_ERR_HIP; }
 
@@ -508,27 +526,38 @@ int experts_adamw_step(void *const *params, const void *const *grads, void *cons
     if (!aligned(m, ms) || !aligned(v, ms) || !aligned(m_scale, 4) || !aligned(v_scale, 4) ||
         !aligned(grad_scale, 4))
         return KM_ERR_ALIGN;
-    const int64_t scales = bits == 8 ? total / 256 : 0;
-    const Span state[] = {{m, 1, 0, total, ms},
-                          {v, 1, 0, total, ms},
-                          {m_scale, 1, 0, scales, 4},
-                          {v_scale, 1, 0, scales, 4}};
-    const Span scale[] = {{grad_scale, 1, 0, 1, 4}};
-    if (int rc = check_alias(state, 4, scale, 1)) return rc;
     for (int64_t i = 0; i < count; ++i) {
         if (numels[i] == 0) continue;
         if (!params[i] || !grads[i] || (copies && !copies[i])) return KM_ERR_NULL;
         if (!aligned(params[i], ps) || !aligned(grads[i], gs) || (copies && !aligned(copies[i], 2)))
             return KM_ERR_ALIGN;
-        // A bfloat16 parameter may be its own copy.
-        const bool same = copies && copies[i] == params[i] && param_dtype == EXPERTS_BF16;
-        const Span own[] = {{params[i], 1, 0, numels[i], ps},
-                            {copies && !same ? copies[i] : nullptr, 1, 0, numels[i], 2}};
-        const Span in[] = {{grads[i], 1, 0, numels[i], gs}, state[0], state[1], state[2], state[3],
-                           scale[0]};
-        if (int rc = check_alias(own, 2, in, 6)) return rc;
-        if (int rc = check_alias(state, 4, in, 1)) return rc;
     }
+    // The ranges of all tensors: a tensor given twice would be stepped by two workgroups
+    // at once. (Up to 32 tensors on the stack.)
+    const int64_t scales = bits == 8 ? total / 256 : 0;
+    constexpr int64_t kOwn = 101;
+    Range own[kOwn], *ranges = own;
+    if (count > (kOwn - 5) / 3) ranges = new (std::nothrow) Range[3 * count + 5];
+    if (!ranges) return KM_ERR_HIP;  // no host memory left
+    int64_t n = 0;
+    auto add = [&](const void *p, int64_t len, size_t size, bool written) {
+        if (p && len > 0) ranges[n++] = {(uintptr_t)p, (uintptr_t)p + (size_t)len * size, written};
+    };
+    add(m, total, ms, true);
+    add(v, total, ms, true);
+    add(m_scale, scales, 4, true);
+    add(v_scale, scales, 4, true);
+    add(grad_scale, 1, 4, false);
+    for (int64_t i = 0; i < count; ++i) {
+        add(params[i], numels[i], ps, true);
+        add(grads[i], numels[i], gs, false);
+        // A bfloat16 parameter may be its own copy.
+        if (copies && !(copies[i] == params[i] && param_dtype == EXPERTS_BF16))
+            add(copies[i], numels[i], 2, true);
+    }
+    const bool overlapping = any_overlap(ranges, n);
+    if (ranges != own) delete[] ranges;
+    if (overlapping) return KM_ERR_ALIAS;
     kx::AdamwStep st;
     st.beta1 = (float)beta1;
     st.one_minus_beta1 = (float)(1.0 - beta1);

@@ -549,7 +549,7 @@ def _pointers(tensors, dtype, params, dev, name):
 def adamw_step(params, grads, m, v, lr, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, step=1,
                m_scale=None, v_scale=None, copies=None, grad_scale=None, stream=None):
     """One AdamW step, in place, over lists of tensors (one dtype for the
-    parameters, one for the gradients). m, v (and the scales of 8-bit moments)
+    parameters, one for the gradients; a tensor that is shared is given once). m, v (and the scales of 8-bit moments)
     as made by adamw_state. ``copies``: bfloat16 tensors that receive the new
     parameters. ``grad_scale``: a float32 GPU tensor of one element that
     multiplies the gradients (clipping, loss scaling). step counts from 1."""

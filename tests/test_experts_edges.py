@@ -1,0 +1,37 @@
+"""The experts' host side at its edges: what is validated, allocated and built
+(no GPU: every call here fails validation before a kernel launch, or has nothing to
+launch, or is let through where there is no device)."""
+import ctypes
+import os
+import types
+
+import pytest
+
+from nearest_centroid_assignment_amd import build
+from tests.test_experts_abi import (A, ALIAS, B, BF16, C, D, E, F, F16, F32, G, H, HIP, NULL, OK, SHAPE,  # noqa: F401
+                                    experts, lib, no_gpu)
+
+
+@no_gpu
+def test_adamw_tensors_overlap(lib):
+    """No tensor that is written may be given twice, or overlap any other tensor of
+    the call; gradients may be shared."""
+    def step(p, g, c=None, pt=F32, gt=F32, n=256, m=G, v=H):
+        ptrs = lambda t: (ctypes.c_void_p * len(t))(*t)  # noqa: E731
+        lengths = (ctypes.c_int64 * len(p))(*[n] * len(p))
+        return lib.experts_adamw_step(ptrs(p), ptrs(g), ptrs(c) if c else None, lengths, len(p), pt, gt, m, v, None,
+                                      None, 32, 1e-3, 0.9, 0.99, 1e-8, 0.0, 1, None, None)
+
+    assert step((A, B), (C, D)) == HIP and step((A, B), (C, C)) == HIP  # let through: no device
+    assert step((A, A + 1024), (C, D)) == HIP and step((A, A + 1020), (C, D)) == ALIAS
+    assert step((A, A), (C, D)) == ALIAS  # tied weights
+    assert step((A, B), (C, A)) == ALIAS and step((A, B), (B + 512, D)) == ALIAS
+    assert step((A, B), (C, D), (E, E)) == ALIAS and step((A, B), (C, D), (E, A)) == ALIAS
+    assert step((A, B), (C, D), (E, C)) == ALIAS
+    assert step((A, B), (C, D), (A, B), pt=BF16) == HIP  # its own copy
+    assert step((A, B), (C, D), (B, A), pt=BF16) == ALIAS
+    assert step((A, G + 512), (C, D)) == ALIAS and step((A, B), (C, H + 4)) == ALIAS
+    many = [A + 1024 * i for i in range(100)]
+    grads = [C + 1024 * (i // 2) for i in range(100)]
+    assert step(many, grads) == HIP
+    assert step(many[::-1] + [many[7]], grads + [D]) == ALIAS and step(many, [*grads[:-1], many[0] + 4]) == ALIAS
