@@ -132,6 +132,18 @@ def _side_stream(stream, device):
     return None
 
 
+def _check_workspace(workspace, device):
+    """The kernels write its bytes one after another from its first on."""
+    torch = _torch()
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 \
+            or workspace.device.type != "cuda":
+        raise TypeError("workspace must be a uint8 GPU tensor")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}, got {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+
+
 def _workspace(workspace, nbytes, device, stream=None):
     """The caller's workspace, or a new one. A new one is allocated on the
     stream the kernels run on, so the caching allocator does not hand its
@@ -144,8 +156,8 @@ def _workspace(workspace, nbytes, device, stream=None):
                 workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
         else:
             workspace = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or workspace.device.type != "cuda":
-        raise TypeError("workspace must be a uint8 GPU tensor")
+    else:
+        _check_workspace(workspace, device)
     return workspace
 
 

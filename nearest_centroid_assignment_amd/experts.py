@@ -26,7 +26,8 @@ from typing import NamedTuple
 
 import torch
 
-from .binding import HERE, KMeansError, _check, _record, _side_stream, _stream, lib as _kmeans_lib
+from .binding import (HERE, KMeansError, _check, _check_workspace, _record, _side_stream, _stream,
+                      lib as _kmeans_lib)
 
 ACTS = {"none": 0, "relu": 1, "gelu_tanh": 2, "silu": 3}
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
@@ -180,8 +181,8 @@ def _scratch(workspace, nbytes, like, side):
         if nbytes <= BLOCK:  # slack for alignment alone
             return None, None, 0
         workspace = _new(like, side, nbytes, torch.uint8)
-    elif workspace.dtype != torch.uint8 or not workspace.is_cuda:
-        raise TypeError("workspace must be a uint8 GPU tensor")
+    else:
+        _check_workspace(workspace, like.device)
     return workspace, workspace.data_ptr(), workspace.numel()
 
 

@@ -35,3 +35,21 @@ def test_adamw_tensors_overlap(lib):
     grads = [C + 1024 * (i // 2) for i in range(100)]
     assert step(many, grads) == HIP
     assert step(many[::-1] + [many[7]], grads + [D]) == ALIAS and step(many, [*grads[:-1], many[0] + 4]) == ALIAS
+
+
+def test_workspace_of_another_device(experts):
+    """A workspace on another GPU than the call's is refused."""
+    import torch
+
+    from nearest_centroid_assignment_amd import binding
+
+    class Bytes(torch.Tensor):
+        device = property(lambda self: torch.device("cuda", 1))
+
+    ws = torch.zeros(1000, dtype=torch.uint8).as_subclass(Bytes)
+    like = types.SimpleNamespace(device=torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="cuda:0"):
+        experts._scratch(ws, 300, like, None)
+    with pytest.raises(ValueError, match="cuda:0"):
+        binding._workspace(ws, 300, like.device)
+    assert experts._scratch(ws, 300, types.SimpleNamespace(device=ws.device), None)[2] == 1000

@@ -156,3 +156,26 @@ def test_slope_far_from_zero(dtype, act, rows):
     assert torch.equal(dx, want)
     z[0, 0] = float("nan")
     assert torch.isnan(experts.linear_backward(dy, dy, eye, pre=z, act=act)[0][0, 0])
+
+
+# ------------------------------------------------------------- memory and views
+
+
+def test_workspace_refusals():
+    """A workspace that is a strided view would be written between its elements."""
+    ids = torch.zeros(5000, 2, dtype=torch.int64, device="cuda")
+    x, w = randn(1, 64, 4096), randn(2, 64, 4096)
+    assert experts.lib().experts_linear_workspace_bytes(64, 64, 4096, 1, 0, 0, 0) > 256
+    room = torch.full((1 << 24, 2), 7, dtype=torch.uint8, device="cuda")
+    for bad in (room[:, 0], room.cpu()[:, 0].contiguous(), room[:, 0].contiguous().to(torch.int8), 5):
+        with pytest.raises((TypeError, ValueError)):
+            experts.plan(ids, 3, workspace=bad)
+        with pytest.raises((TypeError, ValueError)):
+            experts.linear(x, w, workspace=bad)
+        with pytest.raises((TypeError, ValueError)):
+            experts.linear_backward(randn(3, 64, 64), x, w, workspace=bad)
+    with pytest.raises((TypeError, ValueError)):
+        binding.kmeans_assign(x, w, torch.empty(64, dtype=torch.int64, device="cuda"), workspace=room[:, 0])
+    assert bool((room == 7).all())
+    flat = room.reshape(-1)
+    assert torch.equal(experts.linear(x, w, workspace=flat), experts.linear(x, w))
