@@ -129,6 +129,11 @@ PyObject *tuple_of(const at::Tensor &a, const at::Tensor &b, const at::Tensor &c
     return r;
 }
 
+// Autograd is told that t was written in place, as it is by torch's own operators.
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // What a status of the C ABI other than KM_OK becomes.
 PyObject *failed(int status, const char *name) {
     if (status == KM_ERR_HIP) {
@@ -435,6 +440,11 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t count) {
         code_of(pt), code_of(gt), pm, pv, ms, vs, bits, h[0], h[1], h[2], h[3], h[4], step, gs,
         queue(dev));
     if (status != KM_OK) return failed(status, "experts_adamw_step");
+    for (PyObject *list : {a[0], a[12]})
+        for (Py_ssize_t i = 0; list != Py_None && i < n; ++i)
+            written(THPVariable_Unpack(PyList_GET_ITEM(list, i)));
+    for (PyObject *o : {a[2], a[3], a[10], a[11]})
+        if (o != Py_None) written(THPVariable_Unpack(o));
     Py_RETURN_TRUE;
     END_HANDLE_TH_ERRORS
 }

@@ -190,6 +190,19 @@ def _mark(stream, dev, *tensors):
     _record(stream, torch.device("cuda", dev), *tensors)
 
 
+def _written(*tensors):
+    """Tell autograd that these were written in place (the native calls do too)."""
+    torch.autograd.graph.increment_version(
+        [t for t in tensors if t is not None and not t.is_inference()])
+
+
+def _given(out, dtype, rows, cols, dev):
+    """(pointer, row stride) of an output that the caller gives."""
+    got = _rows(out, dtype, rows, cols, dev, "out")
+    _written(out)
+    return got
+
+
 def _on_device(fn):
     """Run fn with its first tensor's device current: the library launches there."""
 
@@ -284,7 +297,7 @@ def _dispatch(x, plan, out, stream):
         out = _new(x, side, (pairs, width))
         po, ldo = out.data_ptr() or None, width
     else:
-        po, ldo = _rows(out, dtype, pairs, width, dev, "out")
+        po, ldo = _given(out, dtype, pairs, width, dev)
     _check(lib().experts_dispatch(px, ldx, code, tokens, top, width, order, place, po, ldo, queue),
            "experts_dispatch")
     if side is not None:
@@ -313,7 +326,7 @@ def _dispatch_backward(dxs, plan, out, stream):
         out = _new(dxs, side, (tokens, width))
         po, ldo = out.data_ptr() or None, width
     else:
-        po, ldo = _rows(out, dtype, tokens, width, dev, "out")
+        po, ldo = _given(out, dtype, tokens, width, dev)
     _check(lib().experts_dispatch_backward(pg, ldg, code, tokens, top, width, place, po, ldo,
                                            queue), "experts_dispatch_backward")
     if side is not None:
@@ -344,7 +357,7 @@ def _combine(ys, weights, plan, out, stream):
         out = _new(ys, side, (tokens, width))
         po, ldo = out.data_ptr() or None, width
     else:
-        po, ldo = _rows(out, dtype, tokens, width, dev, "out")
+        po, ldo = _given(out, dtype, tokens, width, dev)
     _check(lib().experts_combine(py, ldy, pw, code, tokens, top, width, place, po, ldo, queue),
            "experts_combine")
     if side is not None:
@@ -445,7 +458,7 @@ def _linear(x, w, bias, residual, act, offsets, save_pre, out, workspace, stream
         out = _new(x, side, (rows, outs))
         po, ldo = out.data_ptr() or None, outs
     else:
-        po, ldo = _rows(out, dtype, rows, outs, dev, "out")
+        po, ldo = _given(out, dtype, rows, outs, dev)
     pre = _new(x, side, (rows, outs)) if save_pre else None
     L = lib()
     nbytes = L.experts_linear_workspace_bytes(rows, outs, ins, experts, code, 0,
@@ -591,6 +604,7 @@ def _adamw_step(params, grads, m, v, lr, betas, eps, weight_decay, step, m_scale
     _check(lib().experts_adamw_step(pp, pg, pk, n, len(params), pc, gc, pm, pv, ms, vs, bits, lr,
                                     betas[0], betas[1], eps, weight_decay, step, gs, queue),
            "experts_adamw_step")
+    _written(*params, *(copies or ()), m, v, m_scale, v_scale)
     if side is not None:
         _mark(stream, dev, *params, *grads, *(copies or ()), m, v, m_scale, v_scale, grad_scale)
 

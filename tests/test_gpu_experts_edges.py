@@ -179,3 +179,35 @@ def test_workspace_refusals():
     assert bool((room == 7).all())
     flat = room.reshape(-1)
     assert torch.equal(experts.linear(x, w, workspace=flat), experts.linear(x, w))
+
+
+def test_versions():
+    """What a call writes in place counts as modified: autograd notices that a
+    tensor it saved has changed."""
+    side = torch.cuda.Stream()
+    for bits, stream in ((32, None), (8, None), (32, side)):
+        p = [torch.nn.Parameter(randn(i, 300)) for i in range(2)]
+        g = [randn(9, 300) for _ in p]
+        copies, state = [torch.zeros(300, dtype=torch.bfloat16, device="cuda") for _ in p], experts.adamw_state(p, bits)
+        written, read = [*p, *copies, *state.values()], [*g]
+        before = [t._version for t in written + read]
+        loss = (p[0] * p[0]).sum()
+        torch.cuda.synchronize()
+        experts.adamw_step(p, g, lr=0.1, copies=copies, stream=stream, **state)
+        torch.cuda.synchronize()
+        after = [t._version for t in written + read]
+        assert all(b > a for a, b in zip(before, after[:len(written)])) and after[len(written):] == before[len(written):]
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    plan = experts.plan(make_ids(1, 10, 2, 3).cuda(), 3)
+    xs, y, z = torch.empty(20, 16, device="cuda"), torch.empty(10, 16, device="cuda"), torch.empty(20, 24, device="cuda")
+    x, w, weights = randn(1, 10, 16), randn(2, 24, 16), randn(3, 10, 2)
+    for out, call in ((xs, lambda: experts.dispatch(x, plan, out=xs)), (y, lambda: experts.combine(xs, weights, plan, out=y)),
+                      (y, lambda: experts.dispatch_backward(xs, plan, out=y)), (z, lambda: experts.linear(xs, w, out=z))):
+        before = out._version
+        assert call() is out and out._version > before
+    with torch.inference_mode():
+        p = [randn(1, 300)]
+        state = experts.adamw_state(p)
+    experts.adamw_step(p, [randn(2, 300)], lr=0.1, **state)
+    assert not torch.equal(p[0], randn(1, 300))
