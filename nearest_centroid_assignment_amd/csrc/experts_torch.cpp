@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
 
@@ -134,6 +135,20 @@ void written(const at::Tensor &t) {
     if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
+// Warns where a graph is being recorded and one of these asks to be in it: the operator
+// is not. False if the warning has become an error.
+bool say_unrecorded(const char *name, at::ArrayRef<const at::Tensor *> inputs) {
+    if (!c10::GradMode::is_enabled()) return true;
+    for (const at::Tensor *t : inputs)
+        if (t && t->requires_grad())
+            return PyErr_WarnFormat(PyExc_UserWarning, 2,
+                                    "experts.%s is not recorded for autograd: an input requires grad, but "
+                                    "gradients are explicit calls (experts.%s_backward). Call it under "
+                                    "torch.no_grad(), or with detached tensors",
+                                    name, name) == 0;
+    return true;
+}
+
 // What a status of the C ABI other than KM_OK becomes.
 PyObject *failed(int status, const char *name) {
     if (status == KM_ERR_HIP) {
@@ -189,6 +204,7 @@ PyObject *dispatch(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (dev < 0 || code < 0 || !plan_of(a[1], dev, p) ||
         !rows_of(x, x->scalar_type(), p.tokens, x->size(1), dev, rx))
         NOT_HERE;
+    if (!say_unrecorded("dispatch", {x})) return nullptr;
     const int64_t width = x->size(1);
     at::Tensor xs = new_tensor({p.tokens * p.top, width}, x->scalar_type(), dev);
     const int status = dispatch_call(
@@ -234,6 +250,7 @@ PyObject *combine(PyObject *, PyObject *const *a, Py_ssize_t count) {
         NOT_HERE;
     const float *w = (const float *)dense(tensor(a[1]), at::kFloat, {p.tokens, p.top}, dev);
     if (!w) NOT_HERE;
+    if (!say_unrecorded("combine", {ys, tensor(a[1])})) return nullptr;
     const int64_t width = ys->size(1);
     at::Tensor y = new_tensor({p.tokens, width}, ys->scalar_type(), dev);
     const int status = combine_call(
@@ -316,6 +333,7 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t count) {
     const size_t bytes =
         linear_bytes(rows, w.outs, w.ins, w.experts, code, 0, misplaced(rx, w));
     if (bytes == 0) NOT_HERE;
+    if (!say_unrecorded("linear", {x, tensor(a[1]), tensor(a[2]), tensor(a[3])})) return nullptr;
     Scratch ws(bytes, dev);
     at::Tensor out = new_tensor({rows, w.outs}, type, dev), pre;
     const int save = PyObject_IsTrue(a[6]);
@@ -449,6 +467,18 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t count) {
     END_HANDLE_TH_ERRORS
 }
 
+// (name of the operator, inputs...) -> None: the warning for a call that Python takes
+PyObject *unrecorded(PyObject *, PyObject *const *a, Py_ssize_t count) {
+    HANDLE_TH_ERRORS
+    const char *name = count < 1 ? "" : PyUnicode_AsUTF8(a[0]);
+    if (!name) return nullptr;
+    std::vector<const at::Tensor *> inputs;
+    for (Py_ssize_t i = 1; i < count; ++i) inputs.push_back(tensor(a[i]));
+    if (!say_unrecorded(name, inputs)) return nullptr;
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
 // ({name: address of the C entry point}, check) -> None
 PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (count < 1 || !PyDict_Check(a[0])) {
@@ -500,6 +530,7 @@ PyMethodDef methods[] = {KX_METHOD(bind),
                          KX_METHOD(linear),
                          KX_METHOD(linear_backward),
                          KX_METHOD(adamw_step),
+                         KX_METHOD(unrecorded),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_experts_torch", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

@@ -14,7 +14,9 @@ Tensors supply pointers, strides and the stream; every step of the computation
 runs in the library's HIP kernels, and there is no CPU fallback. Matrices may
 have any row stride, with the elements of a row next to each other. As in
 ``binding``, a call enqueues on ``stream`` (the current one by default) and
-returns; gradients are explicit calls, given what the forward call returned.
+returns. Gradients are explicit calls, given what the forward call returned:
+autograd records none of this, and a forward call with an input that requires grad
+warns of it (not under ``torch.no_grad()``).
 """
 from __future__ import annotations
 
@@ -281,6 +283,7 @@ def dispatch(x, plan, out=None, stream=None):
         got = (_native or _module()).dispatch(x, plan)
         if got is not None:
             return got
+    _module().unrecorded("dispatch", x)
     return _dispatch(x, plan, out, stream)
 
 
@@ -341,6 +344,7 @@ def combine(ys, weights, plan, out=None, stream=None):
         got = (_native or _module()).combine(ys, weights, plan)
         if got is not None:
             return got
+    _module().unrecorded("combine", ys, weights)
     return _combine(ys, weights, plan, out, stream)
 
 
@@ -441,6 +445,7 @@ def linear(x, w, bias=None, residual=None, act="none", offsets=None, save_pre=Fa
                                             save_pre)
         if got is not None:
             return got
+    _module().unrecorded("linear", x, w, bias, residual)
     return _linear(x, w, bias, residual, act, offsets, save_pre, out, workspace, stream)
 
 

@@ -211,3 +211,28 @@ def test_versions():
         state = experts.adamw_state(p)
     experts.adamw_step(p, [randn(2, 300)], lr=0.1, **state)
     assert not torch.equal(p[0], randn(1, 300))
+
+
+def test_lost_gradients_are_said():
+    """The operators record no graph. An input that asks for one is answered, with
+    a warning; without gradients being recorded there is none."""
+    import warnings
+
+    plan = experts.plan(make_ids(1, 10, 2, 3).cuda(), 3)
+    x, xs, w, weights = randn(1, 10, 16), randn(2, 20, 16), randn(3, 24, 16), randn(4, 10, 2)
+    bias, res = randn(5, 24), randn(6, 20, 24)
+    calls = [(x, lambda **k: experts.dispatch(x, plan, **k)), (xs, lambda **k: experts.combine(xs, weights, plan, **k)),
+             (weights, lambda **k: experts.combine(xs, weights, plan, **k))]
+    calls += [(t, lambda **k: experts.linear(xs, w, bias, residual=res, **k)) for t in (xs, w, bias, res)]
+    for t, call in calls:
+        for stream in (None, torch.cuda.current_stream()):
+            with warnings.catch_warnings():
+                warnings.simplefilter("error")
+                want = call(stream=stream)
+                t.requires_grad_(True)
+                with torch.no_grad():
+                    call(stream=stream)
+            with pytest.warns(UserWarning, match="explicit calls"):
+                got = call(stream=stream)
+            assert torch.equal(got, want) and not got.requires_grad
+            t.requires_grad_(False)
