@@ -50,7 +50,15 @@ bool overlap(const Span &a, const Span &b) {
     const uintptr_t alo = (uintptr_t)a.p, blo = (uintptr_t)b.p;
     const uintptr_t ahi = alo + ((uintptr_t)(a.rows - 1) * a.ld + a.len) * a.elem;
     const uintptr_t bhi = blo + ((uintptr_t)(b.rows - 1) * b.ld + b.len) * b.elem;
-    return alo < bhi && blo < ahi;
+    if (alo >= bhi || blo >= ahi) return false;
+    // Rows equally far apart: b's start `at` bytes into a's, and where they lie past a's
+    // end and end before a's next row (columns of one buffer), no two rows meet.
+    const uintptr_t step = (uintptr_t)a.ld * a.elem;
+    if (a.rows > 1 && b.rows > 1 && step == (uintptr_t)b.ld * b.elem) {
+        const uintptr_t at = blo >= alo ? (blo - alo) % step : (step - (alo - blo) % step) % step;
+        if (at >= a.len * a.elem && at + b.len * b.elem <= step) return false;
+    }
+    return true;
 }
 int check_alias(const Span *outs, int n_outs, const Span *ins, int n_ins) {
     for (int i = 0; i < n_outs; ++i) {

@@ -53,3 +53,17 @@ def test_workspace_of_another_device(experts):
     with pytest.raises(ValueError, match="cuda:0"):
         binding._workspace(ws, 300, like.device)
     assert experts._scratch(ws, 300, types.SimpleNamespace(device=ws.device), None)[2] == 1000
+
+
+@no_gpu
+def test_columns_of_one_buffer(lib):
+    """Column ranges of the same rows overlap only where they share a column."""
+    def fwd(x, out, ld=40, ldo=40, rows=100, outs=16, ins=16):
+        return lib.experts_linear(x, ld, C, None, None, 0, None, F32, 0, rows, outs, ins, 1, out, ldo, None, 0, G,
+                                  1 << 24, None)
+
+    for x, out, want in ((A, A + 64, HIP), (A + 64, A, HIP), (A, A + 96, HIP), (A + 96, A, HIP), (A, A + 160 + 64, HIP),
+                         (A, A + 60, ALIAS), (A + 60, A, ALIAS), (A, A, ALIAS), (A, A + 100, ALIAS), (A + 100, A, ALIAS),
+                         (A, A + 160 * 99 + 60, ALIAS), (A, A + 160 * 99 + 64, HIP)):
+        assert fwd(x, out) == want, (x - A, out - A)
+    assert fwd(A, A + 64, ldo=44) == ALIAS and fwd(A, A + 64, rows=1) == HIP and fwd(A, A + 60, rows=1) == ALIAS

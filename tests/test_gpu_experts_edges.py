@@ -236,3 +236,24 @@ def test_lost_gradients_are_said():
                 got = call(stream=stream)
             assert torch.equal(got, want) and not got.requires_grad
             t.requires_grad_(False)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_halves_of_one_buffer(dtype):
+    """An input and an output that are column ranges of the same rows do not overlap."""
+    rows, k = 150, 70
+    buf, w = randn(1, rows, 2 * k + 2, dtype=dtype), randn(2, k, k, dtype=dtype, scale=0.1)
+    lo, hi = buf[:, :k], buf[:, k + 1:2 * k + 1]
+    want = experts.linear(lo.contiguous(), w, residual=lo.contiguous(), act="silu")
+    edge = buf[:, [k, 2 * k + 1]].clone()
+    experts.linear(lo, w, residual=lo, act="silu", out=hi)
+    assert torch.equal(hi, want) and torch.equal(buf[:, [k, 2 * k + 1]], edge)
+    plan = experts.plan(make_ids(1, rows, 1, 5).cuda(), 5)
+    experts.dispatch(hi, plan, out=lo)
+    assert torch.equal(lo, experts.dispatch(want, plan))
+    weights = randn(3, rows, 1)
+    experts.combine(lo, weights, plan, out=hi)
+    assert torch.equal(hi, experts.combine(lo.contiguous(), weights, plan))
+    for bad in (buf[:, k - 1:2 * k - 1], buf[:, :k]):
+        with pytest.raises(binding.KMeansError):
+            experts.linear(lo, w, out=bad)
