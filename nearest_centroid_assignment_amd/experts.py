@@ -546,12 +546,13 @@ def adamw_state(params, bits=32):
     params = list(params)
     total = _numels(params)[1]
     dev = params[0].device if params else "cuda"
+    f32 = dict(dtype=torch.float32, device=dev)
     if bits == 32:
-        return {"m": torch.zeros(total, device=dev), "v": torch.zeros(total, device=dev)}
+        return {"m": torch.zeros(total, **f32), "v": torch.zeros(total, **f32)}
     return {"m": torch.zeros(total, dtype=torch.int8, device=dev),
             "v": torch.zeros(total, dtype=torch.uint8, device=dev),
-            "m_scale": torch.zeros(total // BLOCK, device=dev),
-            "v_scale": torch.zeros(total // BLOCK, device=dev)}
+            "m_scale": torch.zeros(total // BLOCK, **f32),
+            "v_scale": torch.zeros(total // BLOCK, **f32)}
 
 
 def _pointers(tensors, dtype, params, dev, name):

@@ -67,3 +67,19 @@ def test_columns_of_one_buffer(lib):
                          (A, A + 160 * 99 + 60, ALIAS), (A, A + 160 * 99 + 64, HIP)):
         assert fwd(x, out) == want, (x - A, out - A)
     assert fwd(A, A + 64, ldo=44) == ALIAS and fwd(A, A + 64, rows=1) == HIP and fwd(A, A + 60, rows=1) == ALIAS
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_state_types(experts, bits):
+    """The moments are float32 whatever the process's default type is."""
+    import torch
+
+    kept = torch.get_default_dtype()
+    try:
+        torch.set_default_dtype(torch.float64)
+        state = experts.adamw_state([torch.zeros(300), torch.zeros(5)], bits)
+    finally:
+        torch.set_default_dtype(kept)
+    floats = ("m", "v") if bits == 32 else ("m_scale", "v_scale")
+    assert all(state[k].dtype == torch.float32 and not state[k].any() for k in floats)
+    assert state["m"].numel() == state["v"].numel() == 512 + 256
