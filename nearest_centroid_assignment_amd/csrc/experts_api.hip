@@ -315,11 +315,15 @@ size_t experts_linear_workspace_bytes(int64_t rows, int64_t outs, int64_t ins, i
     if (!linear_shape_ok(rows, outs, ins, experts) || !dtype_ok(dtype) || op < 0 || op > 1 ||
         !linear_grid_ok(dtype, op, rows, outs, ins, true, experts))
         return 0;
+    auto bytes = [&](bool grouped) {
+        // (The kernel for few rows reads any rows in place.)
+        const bool pads = dtype != EXPERTS_F32 && (unaligned || ins % 2 != 0) &&
+                          !(op == 0 && kx::rows_plan(dtype, rows, outs, ins, grouped, experts, false).thin);
+        return linear_layout(rows, outs, ins, experts, grouped, dtype, op, pads).total;
+    };
     // Without offsets a single expert may be cut differently; both fit.
-    const bool pads = dtype != EXPERTS_F32 && (unaligned || ins % 2 != 0);
-    const size_t grouped = linear_layout(rows, outs, ins, experts, true, dtype, op, pads).total;
-    const size_t dense = linear_layout(rows, outs, ins, experts, false, dtype, op, pads).total;
-    return experts == 1 && dense > grouped ? dense : grouped;
+    const size_t grouped = bytes(true), dense = experts == 1 ? bytes(false) : 0;
+    return dense > grouped ? dense : grouped;
 }
 
 int experts_linear(const void *x, int64_t ldx, const void *w, const void *bias,

@@ -83,3 +83,13 @@ def test_adamw_state_types(experts, bits):
     floats = ("m", "v") if bits == 32 else ("m_scale", "v_scale")
     assert all(state[k].dtype == torch.float32 and not state[k].any() for k in floats)
     assert state["m"].numel() == state["v"].numel() == 512 + 256
+
+
+def test_workspace_of_few_rows(lib):
+    """The kernel for few rows reads odd 16-bit rows in place: no room for copies."""
+    for rows, outs, ins, n in ((1, 8192, 2047, 1), (16, 4096, 2047, 1), (3, 500, 777, 2)):
+        for unaligned in (0, 1):
+            assert lib.experts_linear_workspace_bytes(rows, outs, ins, n, BF16, 0, unaligned) == 256
+    # Others still have it, and so have the gradients of few rows.
+    assert lib.experts_linear_workspace_bytes(1000, 8192, 2047, 1, BF16, 0, 0) >= 2 * 2048 * 9192
+    assert lib.experts_linear_workspace_bytes(1, 8192, 2047, 1, BF16, 1, 0) >= 2 * 2048 * 8193
