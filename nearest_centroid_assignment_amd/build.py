@@ -97,18 +97,50 @@ def _compile(sources, out_path, verbose: bool, save_temps: bool, extra_flags=Non
     return out_path
 
 
-def build_torch_module(verbose: bool = False) -> str:
-    """Compile the module that marshals torch tensors to the experts' entry
-    points (host code against torch's C++ headers; it links torch alone)."""
+def cxx() -> str | None:
+    """The C++ compiler of the torch module: the system's, or else ROCm's."""
+    for cand in (shutil.which("g++"), shutil.which("c++"), shutil.which("amdclang++"),
+                 "/opt/rocm/bin/amdclang++"):
+        if cand and os.path.exists(cand):
+            return cand
+    return None
+
+
+def torch_module_needs() -> str | None:
+    """What the torch module cannot be built without and is missing here."""
+    import importlib.util
     import sysconfig
 
+    if not cxx():
+        return "a C++ compiler"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python's C headers"
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return "torch"
+    if not os.path.isdir(os.path.join(os.path.dirname(spec.origin), "include", "torch")):
+        return "torch's C++ headers"
+    return None
+
+
+def build_torch_module(verbose: bool = False) -> str | None:
+    """Compile the module that marshals torch tensors to the experts' entry
+    points (host code against torch's C++ headers; it links torch alone). Where
+    something that only it needs is missing, says so and returns None: the libraries
+    are built all the same, and experts.py raises when it is used."""
+    import sysconfig
+
+    missing = torch_module_needs()
+    if missing:
+        print(f"{os.path.basename(TORCH_MODULE_PATH)} is not built (it takes torch tensors to the "
+              f"expert operators): {missing} not found", file=sys.stderr)
+        if os.path.exists(TORCH_MODULE_PATH):
+            os.remove(TORCH_MODULE_PATH)  # of other sources, for all that is known
+        return None
     from torch.utils.cpp_extension import include_paths, library_paths
 
-    cxx = shutil.which("g++") or shutil.which("c++")
-    if not cxx:
-        raise RuntimeError("g++ not found")
     out_tmp = TORCH_MODULE_PATH + ".tmp"
-    _run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+    _run([cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
           "-DUSE_ROCM=1", *(f"-isystem{p}" for p in include_paths()), "-isystem/opt/rocm/include",
           f"-isystem{sysconfig.get_paths()['include']}", os.path.join(CSRC, TORCH_MODULE_SOURCE),
           *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",

@@ -93,3 +93,35 @@ def test_workspace_of_few_rows(lib):
     # Others still have it, and so have the gradients of few rows.
     assert lib.experts_linear_workspace_bytes(1000, 8192, 2047, 1, BF16, 0, 0) >= 2 * 2048 * 9192
     assert lib.experts_linear_workspace_bytes(1, 8192, 2047, 1, BF16, 1, 0) >= 2 * 2048 * 8193
+
+
+@pytest.mark.parametrize("missing", ["compiler", "torch"])
+def test_build_without_torch_module(missing, monkeypatch, tmp_path, capsys):
+    """The libraries build where what only the torch module needs is missing; a
+    module of another build does not stay."""
+    import importlib.util
+
+    old = tmp_path / "_experts_torch.so"
+    old.write_text("")
+    made = []
+    monkeypatch.setattr(build, "TORCH_MODULE_PATH", str(old))
+    monkeypatch.setattr(build, "_compile", lambda sources, path, *a: made.append(path) or path)
+    monkeypatch.setattr(build, "_run", lambda *a, **k: pytest.fail("nothing is left to compile"))
+    if missing == "compiler":
+        exists = os.path.exists
+        monkeypatch.setattr(build.shutil, "which", lambda name: None)
+        monkeypatch.setattr(build.os.path, "exists", lambda p: "clang" not in str(p) and exists(p))
+    else:
+        find = importlib.util.find_spec
+        monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    assert build.build() == build.LIB_PATH
+    monkeypatch.undo()
+    assert made == [build.CALIB_PATH, build.LIB_PATH] and not old.exists()
+    assert f"{missing} not found" in capsys.readouterr().err
+
+
+def test_torch_module_compiler(monkeypatch):
+    """Without a system compiler the module is left to ROCm's."""
+    found = {"amdclang++": build.hipcc()}
+    monkeypatch.setattr(build.shutil, "which", found.get)
+    assert build.cxx() == found["amdclang++"] and build.torch_module_needs() is None
