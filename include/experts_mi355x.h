@@ -71,6 +71,8 @@ int experts_plan(const int64_t *ids, int64_t tokens, int64_t top, int64_t expert
 /*
  * xs[p] = x[order[p] / top]: the token rows in sorted order (tokens * top rows
  * of xs; rows at places without a pair become zero).
+ * Limits of this call, its gradient and experts_combine, tighter than the plan's:
+ * tokens < 2^24 (a workgroup of 256 a token is one dispatch), 1 <= width < 2^31.
  */
 int experts_dispatch(const void *x, int64_t ldx, int dtype, int64_t tokens, int64_t top,
                      int64_t width, const int32_t *order, const int32_t *place, void *xs,
@@ -91,7 +93,7 @@ int experts_combine(const void *ys, int64_t ldys, const float *weights, int dtyp
  * Gradients of experts_combine: dys[p] = weights[order[p]] * dy[token] (zero at
  * places without a pair) and dweights[t, s] = <dy[t], ys[place[t, s]]> (zero
  * for a dropped pair; float32, (tokens, top), dense). Either output may be
- * NULL; ys is read only for dweights.
+ * NULL; ys is read only for dweights. tokens * top < 2^26 - 4.
  */
 int experts_combine_backward(const void *dy, int64_t lddy, const void *ys, int64_t ldys,
                              const float *weights, int dtype, int64_t tokens, int64_t top,
@@ -109,7 +111,11 @@ int experts_combine_backward(const void *dy, int64_t lddy, const void *ys, int64
  *             (experts + 1) int32: expert e has the rows [offsets[e],
  *             offsets[e + 1]). Rows from offsets[experts] on become zero in
  *             out and pre.
- * 0 <= rows < 2^31; 1 <= outs, ins <= 2^20; 1 <= experts <= 65536; ld <= 2^20.
+ * 0 <= rows < 2^31; 1 <= outs, ins <= 2^20; 1 <= experts <= 65536; ld <= 2^20;
+ * and one dispatch has to hold the call: rows * outs < 2^35 - 2^12 (rows * ins too for
+ * the gradient and the 16-bit types, for these also experts * outs * ins; outs and ins
+ * rounded up to multiples of 8), and fewer than about 2^23 tiles of 64 x 64 to
+ * 256 x 256 outputs.
  * float32 uses the float32 matrix instructions, the 16-bit types theirs; both
  * accumulate in float32.
  * Workspace: partial sums where the depth is split; and where 16-bit rows of x

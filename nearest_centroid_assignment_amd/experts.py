@@ -12,9 +12,9 @@ include/experts_mi355x.h, in the same library as the k-means kernels).
 The labels of ``binding.assign`` are expert numbers as they are (one a token).
 Tensors supply pointers, strides and the stream; every step of the computation
 runs in the library's HIP kernels, and there is no CPU fallback. Matrices may
-have any row stride, with the elements of a row next to each other. As in
-``binding``, a call enqueues on ``stream`` (the current one by default) and
-returns. Gradients are explicit calls, given what the forward call returned:
+have any row stride, with the elements of a row next to each other; the header
+has the largest sizes. As in ``binding``, a call enqueues on ``stream`` (the current
+one by default) and returns. Gradients are explicit calls, given what the forward call returned:
 autograd records none of this, and a forward call with an input that requires grad
 warns of it (not under ``torch.no_grad()``).
 """

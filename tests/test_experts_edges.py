@@ -125,3 +125,26 @@ def test_torch_module_compiler(monkeypatch):
     found = {"amdclang++": build.hipcc()}
     monkeypatch.setattr(build.shutil, "which", found.get)
     assert build.cxx() == found["amdclang++"] and build.torch_module_needs() is None
+
+
+@no_gpu
+def test_limits(lib):
+    """The largest sizes that the header names are let through, the next are not."""
+    def dispatch(tokens, top=1):
+        return lib.experts_dispatch(A, 1, BF16, tokens, top, 1, B, C, D, 1, None)
+
+    def gather(tokens):
+        return lib.experts_dispatch_backward(A, 1, BF16, tokens, 1, 1, C, D, 1, None)
+
+    def combine(tokens):
+        return lib.experts_combine(A, 1, B, BF16, tokens, 1, 1, C, D, 1, None)
+
+    def back(tokens, top):
+        return lib.experts_combine_backward(A, 1, B, 1, C, BF16, tokens, top, 1, D, E, F, 1, G, None)
+
+    for call in (dispatch, gather, combine):
+        assert call(2**24 - 1) == HIP and call(2**24) == SHAPE
+    assert back(2**26 - 5, 1) == HIP and back(2**26 - 3, 1) == SHAPE and back(2**24, 4) == SHAPE
+    linear = lib.experts_linear_workspace_bytes
+    rows = (2**35 - 2**12) // 8192
+    assert linear(rows - 1, 8192, 64, 1, BF16, 0, 0) > 0 and linear(rows + 1, 8192, 64, 1, BF16, 0, 0) == 0
