@@ -257,3 +257,66 @@ def test_halves_of_one_buffer(dtype):
     for bad in (buf[:, k - 1:2 * k - 1], buf[:, :k]):
         with pytest.raises(binding.KMeansError):
             experts.linear(lo, w, out=bad)
+
+
+# ------------------------------------------- between the ways a call can be taken
+
+
+@pytest.mark.parametrize("tokens,top,n,drop", [
+    (64, 1, 65536, 0.1), (4096, 1, 1024, 0.1), (512, 8, 1024, 0), (4096, 1, 1025, 0), (131072, 1, 7, 0.1),
+    (131073, 1, 7, 0.1), (70000, 2, 1024, 0.05), (65536, 2, 4096, 0.05), (32768, 4, 4097, 0.05), (65536, 8, 33, 0.1),
+    (300000, 1, 5000, 0.02)])
+def test_plan_between_sorts(tokens, top, n, drop):
+    """The last size of each way to sort and the first of the next, against a stable sort."""
+    gu.announce(f"plan {tokens} x {top}, {n} experts, drop {drop}")
+    for lopsided in (False, True):
+        ids = make_ids(tokens + n, tokens, top, n, drop, lopsided)
+        p = experts.plan(ids.cuda(), n)
+        flat = ids.reshape(-1)
+        key = torch.where((flat >= 0) & (flat < n), flat, n)
+        live = int((key < n).sum())
+        order = key.sort(stable=True)[1].to(torch.int32)
+        order[live:] = -1
+        place = torch.full((tokens * top,), -1, dtype=torch.int32)
+        place[order[:live].long()] = torch.arange(live, dtype=torch.int32)
+        offsets = torch.cat([torch.zeros(1, dtype=torch.long), torch.bincount(key, minlength=n + 1)[:n].cumsum(0)])
+        assert torch.equal(p.order.cpu(), order)
+        assert torch.equal(p.place.cpu().reshape(-1), place)
+        assert torch.equal(p.offsets.cpu().long(), offsets)
+
+
+@pytest.mark.parametrize("dtype,tokens,width", [(torch.bfloat16, 40000, 2048), (torch.float16, 9000, 8192),
+                                                (torch.float32, 20000, 2048)])
+def test_rows_past_the_cache(dtype, tokens, width):
+    """Row sets of more than 256 MB in whole lines, which pass the caches by: every
+    row's outputs at sampled tokens in float64, and the places without a pair."""
+    top, n = 2, 65
+    gu.announce(f"rows past the cache: {dtype} {tokens} x {top} x {width}")
+    ids = make_ids(3, tokens, top, n, 0.1)
+    p = experts.plan(ids.cuda(), n)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x, dy, ys = (torch.randn(rows, width, generator=gen, device="cuda").to(dtype)
+                 for rows in (tokens, tokens, tokens * top))
+    weights = randn(4, tokens, top)
+    live = int(p.offsets[-1])
+    ys[live:] = float("nan")
+    xs, y = experts.dispatch(x, p), experts.combine(ys, weights, p)
+    dx = experts.dispatch_backward(ys, p)
+    dys, dweights = experts.combine_backward(dy, ys, weights, p)
+    assert not xs[live:].any() and not dys[live:].any()
+    assert torch.equal(xs[:live], x[p.order[:live].long() // top])
+    for t in [0, 1, tokens - 1, *np.random.default_rng(1).integers(0, tokens, 200).tolist()]:
+        places = p.place[t].tolist()
+        g, total, plain = f64(dy[t]), torch.zeros(width, dtype=torch.float64), torch.zeros(width, dtype=torch.float64)
+        size, plain_size = total.clone(), total.clone()
+        for s, at in enumerate(places):
+            if at < 0:
+                assert float(dweights[t, s]) == 0
+                continue
+            row, w = f64(ys[at]), float(weights[t, s])
+            total, size = total + w * row, size + abs(w) * row.abs()
+            plain, plain_size = plain + row, plain_size + row.abs()
+            close(dys[at], w * g, 2.0 ** -24 * (w * g).abs(), f"dys of {t}")
+            close(dweights[t, s], (g * row).sum(), summed(width) * (g * row).abs().sum(), f"dweights of {t}")
+        close(y[t], total, summed(top) * size, f"y of {t}")
+        close(dx[t], plain, summed(top) * plain_size, f"dx of {t}")
