@@ -4,10 +4,9 @@
 // The sort is a stable counting sort. A wave ranks its 64 pairs among themselves
 // by ballots over the bits of the expert numbers, leaves its count of each expert in
 // LDS, and the ranks of a whole block follow from a prefix over its waves; then a
-// prefix over blocks and experts gives the places. At most kSmallPairs pairs are
-// sorted by one block in one launch; up to kPlaceTiles blocks of 1024 pairs by two
-// launches (the second sums the blocks' counts in every block: 65536 x 2 pairs of
-// 1024 experts 23 us in four launches, 21 in two); more by four.
+// prefix over blocks and experts gives the places. One block in one launch, two
+// launches (the second sums the blocks' counts in every block) or four: see
+// plan_is_small and plan_in_two.
 //
 // The row kernels give one wave (or, with few tokens, one block) to a token: its
 // own row is read once, and the rows of its `top` pairs are reached through the
@@ -20,10 +19,10 @@ namespace kx {
 namespace {
 
 constexpr int kTile = (int)km::kSortTileRows;
-constexpr int kSmallTiles = 4;                     // tiles that the one-block sort takes
+constexpr int kSmallTiles = 2;                     // tiles that the one-block sort takes
 constexpr int kSmallPairs = kSmallTiles * 1024;
 constexpr int kWaveCounts = 65536;                 // counts of (wave, expert) in LDS: 128 KB
-constexpr int kPlaceTiles = 128, kPlaceExperts = 4096;
+constexpr int kPlaceTiles = 256, kPlaceExperts = 2048;  // most of the two-launch sort
 
 // Rank of the lane's expert among the wave's lanes with the same one and a lower
 // index, and how many have it; both 0 where expert < 0. `bits`: of the largest expert.
@@ -229,7 +228,7 @@ __global__ __launch_bounds__(1024) void plan_small_kernel(const int64_t *__restr
         int at = carry + block_scan(all, total);
         if (e < experts) {
             offsets[e] = at;
-            for (int w = 0; w < waves; ++w) {  // (places are below 4096)
+            for (int w = 0; w < waves; ++w) {  // (places are below 2048)
                 const int c = counts[w * experts + e];
                 counts[w * experts + e] = (unsigned short)at;
                 at += c;
@@ -506,8 +505,22 @@ struct Rows {
 
 }  // namespace
 
+// One block in one launch, as far as it is the fastest (its counts of (wave, expert) have
+// to fit LDS). us, one block / two launches: 2048 pairs of 8 experts 5.2 / 6.5, of 256
+// 6.3 / 7.0, of 1024 8.4 / 10.1; 2500 pairs 6.1 / 6.4, 7.6 / 7.1 and 10.3 / 10.4; 4096
+// pairs 7.8 / 6.5, 10.2 / 7.1, 14.5 / 10.3.
 bool plan_is_small(int64_t pairs, int64_t experts) {
     return pairs <= kSmallPairs && cdiv(pairs, 64) * experts <= kWaveCounts;
+}
+// In the two-launch sort every block sums the counts of all tiles, 1024 experts at a time.
+// us, two / four launches: 256 tiles of 17 experts 15.1 / 23.9, of 768 27.7 / 31.6, 293
+// tiles (blocks that no longer all run at once) 28.3 / 27.6 and 55.7 / 39.0; 1024 experts,
+// 128 tiles 20.5 / 22.6, 157 23.6 / 25.1, 196 29.8 / 28.0; 1100 experts, 64 tiles 16.3 /
+// 19.2, 128 24.9 / 23.4; 2048 experts, 32 tiles 15.5 / 17.4, 64 21.7 / 19.7; 2500
+// experts, 3 tiles 17.1 / 16.8.
+static bool plan_in_two(int64_t tiles, int64_t experts) {
+    return tiles <= kPlaceTiles && experts <= kPlaceExperts &&
+           tiles * experts * cdiv(experts, 1024) <= 160 * 1024;
 }
 
 hipError_t launch_plan(const int64_t *ids, int64_t pairs, int64_t experts, int *order, int *place,
@@ -517,7 +530,7 @@ hipError_t launch_plan(const int64_t *ids, int64_t pairs, int64_t experts, int *
         return launch(plan_small_kernel, 1, 1024, lds, s, ids, (int)pairs, (int)experts, order, place,
                       offsets);
     }
-    if (ws.tiles <= kPlaceTiles && experts <= kPlaceExperts) {
+    if (plan_in_two(ws.tiles, experts)) {
         const size_t lds = (size_t)16 * experts * sizeof(unsigned short);
         const hipError_t e = launch(plan_rank_kernel, ws.tiles, 1024, lds, s, ids, pairs, (int)experts,
                                     ws.tile_hist, ws.rank);

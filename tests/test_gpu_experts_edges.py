@@ -267,7 +267,7 @@ def test_halves_of_one_buffer(dtype):
     (131073, 1, 7, 0.1), (70000, 2, 1024, 0.05), (65536, 2, 4096, 0.05), (32768, 4, 4097, 0.05), (65536, 8, 33, 0.1),
     (300000, 1, 5000, 0.02)])
 def test_plan_between_sorts(tokens, top, n, drop):
-    """The last size of each way to sort and the first of the next, against a stable sort."""
+    """Sizes that each way to sort takes, and the largest counts in LDS, against a stable sort."""
     gu.announce(f"plan {tokens} x {top}, {n} experts, drop {drop}")
     for lopsided in (False, True):
         ids = make_ids(tokens + n, tokens, top, n, drop, lopsided)
@@ -320,3 +320,11 @@ def test_rows_past_the_cache(dtype, tokens, width):
             close(dweights[t, s], (g * row).sum(), summed(width) * (g * row).abs().sum(), f"dweights of {t}")
         close(y[t], total, summed(top) * size, f"y of {t}")
         close(dx[t], plain, summed(top) * plain_size, f"dx of {t}")
+
+
+@pytest.mark.parametrize("tokens,top,n", [
+    (2048, 1, 33), (2049, 1, 33), (1024, 2, 2048), (1025, 2, 2048), (163840, 1, 1024), (163841, 1, 1024),
+    (262144, 1, 300), (262145, 1, 300), (40960, 1, 2048), (40961, 1, 2048), (1100, 2, 2049)])
+def test_plan_at_thresholds(tokens, top, n):
+    """As above, at the sizes where the way to sort changes."""
+    test_plan_between_sorts(tokens, top, n, 0.1)
