@@ -8,10 +8,10 @@
 // launches (the second sums the blocks' counts in every block) or four: see
 // plan_is_small and plan_in_two.
 //
-// The row kernels give one wave (or, with few tokens, one block) to a token: its
-// own row is read once, and the rows of its `top` pairs are reached through the
-// inverse permutation, so every row is moved once and no sum needs an atomic. The
-// gradient of combine, whose rows are all the pairs', goes by place instead.
+// The row kernels give one wave or one block to a token (see how()): its own row is read
+// once, and the rows of its `top` pairs are reached through the inverse permutation, so
+// every row is moved once and no sum needs an atomic. The gradient of combine, whose rows
+// are all the pairs', goes by place instead.
 #include "experts.h"
 #include "kernels.h"
 
@@ -392,8 +392,8 @@ __device__ __forceinline__ float token_sum(float v) {
 
 // One place a wave (or block): its row of ys is read and its row of dys written in
 // sorted order, the token's row of dy gathered (a token's rows again, from the
-// caches). By token, with dys scattered: 131072 x 2048 bf16 rows from memory 281 us,
-// by place 251.
+// caches). By token, with dys scattered, a wave each: 131072 x 2048 bf16 rows 281 us, by
+// place 251.
 template <typename T, int NT, bool ONCE>
 __global__ __launch_bounds__(256) void combine_backward_kernel(
     const T *__restrict__ dy, int64_t lddy, const T *__restrict__ ys, int64_t ldys,
@@ -445,26 +445,43 @@ __global__ __launch_bounds__(256) void combine_backward_kernel(
     if (threadIdx.x % NT == 0) dweights[pair] = dot;
 }
 
-// A wave a token once the tokens fill the chip, a block before that. Rows of the
-// pairs that are more than the 256 MB of the memory-side cache pass the caches by,
-// where they are whole lines of 128 bytes: 131072 x 2048 bf16 rows, dispatch 159 ->
-// 123 us (its stores), combine 167 -> 138 (its loads), its gradient 280 -> 234 (both);
-// 15009 x 1001 f16 rows (30 MB), the gradient 18 -> 25.
+// `wave`: a wave or a block of four to each of `own` rows. A wave moves 1 KB of a row at a
+// time, so longer rows have more in flight with a block; short ones leave most of a block
+// idle, which counts once there are enough of them to fill the chip. us, wave / block, of
+// dispatch, combine (two slots a token; bf16 or float32) and combine's gradient:
+//   1024 rows of 1 KB  2.9 2.8 3.6 / 2.9 2.8 4.3     8192 of 1 KB  5.6 5.1 12 / 7.2 6.0 21
+//   1024 of 2 KB  3.5 3.3 4.2 / 3.2 3.1 4.5          8192 of 2 KB  9.8 9.0 18 / 11 10 22
+//   4096 of 3 KB  8.5 8.6 14 / 9.0 8.8 16            80000 of 3 KB  144 118 224 / 135 118 278
+//   4096 of 3.5 KB  9.5 10 18 / 9.9 9.8 17           80000 of 3.5 KB  168 154 308 / 157 154 295
+//   256 of 4 KB  4.1 4.9 4.9 / 2.8 2.8 3.6           65536 of 4 KB  171 143 246 / 149 124 252
+//   256 of 16 KB  10 14 12 / 4.9 5.4 5.8             20000 of 16 KB  201 206 320 / 193 184 305
+//
+// `once`: rows of the pairs that are more than the 256 MB of the memory-side cache pass
+// the caches by, where they are whole lines of 128 bytes. 65536 x 2 rows of 4 KB, all five
+// operators 770 -> 673 us: combine and dispatch's gradient 156 -> 124 (their loads),
+// combine's gradient 281 -> 252 (its stores); dispatch's stores are as fast either way
+// there (147, 149) and faster this way in shorter rows (360000 of 0.9 KB 73 -> 69). Smaller
+// sets are read from the cache: 15009 x 1001 f16 (30 MB), the gradient 18 -> 25.
 struct How {
     bool wave, once;
 };
+constexpr int64_t kMostBlocks = 1 << 24;  // of 256 threads: one dispatch
 template <typename T>
-How how(int64_t tokens, int64_t top, int64_t width, int64_t ld) {
-    const bool lines = width * (int64_t)sizeof(T) % 128 == 0 && ld * (int64_t)sizeof(T) % 128 == 0;
-    return {tokens >= 4096, lines && tokens * top * width * (int64_t)sizeof(T) > 256 << 20};
+How how(int64_t own, int64_t pairs, int64_t width, int64_t ld) {
+    const int64_t bytes = width * (int64_t)sizeof(T);
+    const bool lines = bytes % 128 == 0 && ld * (int64_t)sizeof(T) % 128 == 0;
+    return {own >= kMostBlocks || (own >= 2048 && bytes <= 3 << 10), lines && pairs * bytes > 256 << 20};
 }
 
-#define KX_ROWS(kernel, rows, ...)                                                              \
-    do {                                                                                        \
-        if (h.wave)                                                                             \
-            return launch(h.once ? kernel<T, 64, true __VA_ARGS__> : kernel<T, 64, false __VA_ARGS__>, \
-                          cdiv(rows, 4), 256, 0, s, KX_ARGS);                                   \
-        return launch(kernel<T, 256, false __VA_ARGS__>, rows, 256, 0, s, KX_ARGS);             \
+#define KX_ROWS(kernel, rows, ...)                                                             \
+    do {                                                                                       \
+        if (h.wave)                                                                            \
+            return launch(h.once ? kernel<T, 64, true __VA_ARGS__>                             \
+                                 : kernel<T, 64, false __VA_ARGS__>,                           \
+                          cdiv(rows, 4), 256, 0, s, KX_ARGS);                                  \
+        return launch(h.once ? kernel<T, 256, true __VA_ARGS__>                                \
+                             : kernel<T, 256, false __VA_ARGS__>,                              \
+                      rows, 256, 0, s, KX_ARGS);                                               \
     } while (0)
 
 template <typename T>
@@ -472,7 +489,7 @@ struct Rows {
     static hipError_t dispatch(const void *x, int64_t ldx, int64_t tokens, int64_t top,
                                int64_t width, const int *order, const int *place, void *xs,
                                int64_t ldxs, hipStream_t s) {
-        const How h = how<T>(tokens, top, width, ldxs);
+        const How h = how<T>(tokens, tokens * top, width, ldxs);
 #define KX_ARGS (const T *)x, ldx, tokens, top, width, order, place, (T *)xs, ldxs
         KX_ROWS(dispatch_kernel, tokens);
 #undef KX_ARGS
@@ -480,7 +497,7 @@ struct Rows {
     static hipError_t combine(const void *ys, int64_t ldys, const float *weights, int64_t tokens,
                               int64_t top, int64_t width, const int *place, void *y, int64_t ldy,
                               hipStream_t s) {
-        const How h = how<T>(tokens, top, width, ldys);
+        const How h = how<T>(tokens, tokens * top, width, ldys);
 #define KX_ARGS (const T *)ys, ldys, weights, tokens, top, width, place, (T *)y, ldy
         if (weights)
             KX_ROWS(combine_kernel, tokens, , true);
@@ -492,9 +509,8 @@ struct Rows {
                                const float *weights, int64_t tokens, int64_t top, int64_t width,
                                const int *order, const int *place, void *dys, int64_t lddys,
                                float *dweights, hipStream_t s) {
-        How h = how<T>(tokens, top, width, dys ? lddys : ldys);
         const int64_t pairs = tokens * top;
-        h.wave = pairs >= 4096;
+        const How h = how<T>(pairs, pairs, width, dys ? lddys : ldys);
 #define KX_ARGS                                                                                 \
     (const T *)dy, lddy, (const T *)ys, ldys, weights, pairs, top, width, order, place, (T *)dys, \
         lddys, dweights

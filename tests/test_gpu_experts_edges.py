@@ -328,3 +328,30 @@ def test_rows_past_the_cache(dtype, tokens, width):
 def test_plan_at_thresholds(tokens, top, n):
     """As above, at the sizes where the way to sort changes."""
     test_plan_between_sorts(tokens, top, n, 0.1)
+
+
+@pytest.mark.parametrize("dtype,width", [(torch.float16, 1536), (torch.float16, 1537), (torch.float32, 768)])
+@pytest.mark.parametrize("tokens", [1023, 1024, 2047, 2048])
+def test_rows_at_thresholds(dtype, width, tokens):
+    """Rows on both sides of where a wave or a block takes one, by length and number."""
+    top, n = 2, 9
+    p = experts.plan(make_ids(tokens, tokens, top, n, 0.1).cuda(), n)
+    x, dy, ys = (randn(s, r, width, dtype=dtype) for s, r in ((1, tokens), (2, tokens), (3, tokens * top)))
+    weights, live = randn(4, tokens, top), int(p.offsets[-1])
+    ys[live:] = float("nan")
+    at = p.place.long()
+    rows = torch.where((at >= 0)[:, :, None], ys[at.clamp(min=0)].float(), 0.0)
+    w = torch.where(at >= 0, weights, 0.0)
+    token = p.order[:live].long() // top
+    xs = experts.dispatch(x, p)
+    assert torch.equal(xs[:live], x[token]) and not xs[live:].any()
+    size = f64(rows).abs()
+    w = f64(w)[:, :, None]
+    close(experts.combine(ys, weights, p), (f64(rows) * w).sum(1), summed(top) * (size * w.abs()).sum(1), "y")
+    close(experts.dispatch_backward(ys, p), f64(rows).sum(1), summed(top) * size.sum(1), "dx")
+    dys, dweights = experts.combine_backward(dy, ys, weights, p)
+    want = f64(dy)[token.cpu()] * f64(weights).reshape(-1)[p.order[:live].long().cpu()][:, None]
+    close(dys[:live], want, 2.0 ** -24 * want.abs(), "dys")
+    terms = f64(rows) * f64(dy)[:, None]
+    close(dweights, terms.sum(2), summed(width) * terms.abs().sum(2), "dweights")
+    assert not dys[live:].any()
