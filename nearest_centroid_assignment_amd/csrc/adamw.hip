@@ -8,8 +8,9 @@
 // arguments (kTensors to a launch), so nothing is copied to the device and a
 // step can be captured in a graph.
 //
-// Bound by memory: everything is read and written once, past the caches (12
-// tensors of 67 million elements at most, float32 moments: 1000 -> 928 us, 5.7 TB/s).
+// Bound by memory: everything is read and written once, past the caches (12 tensors, 189
+// million elements, float32 moments: 1000 us through them, 909 to 935 past them, 5.7 to 5.8
+// TB/s).
 //
 // The arithmetic is float32 without contraction, in the order of the formulas:
 // a moment that lies between two codes gets the same one wherever these
@@ -19,7 +20,7 @@
 namespace kx {
 namespace {
 
-constexpr int kTensors = 64;        // per launch: 2.6 KB of kernel arguments
+constexpr int kTensors = 64;        // per launch: 2.9 KB of kernel arguments
 constexpr int kBlock = 256;         // elements that share a scale
 constexpr int kPerWave = 4;         // blocks per wave
 constexpr int kChunk = 4 * kPerWave * kBlock;
@@ -120,7 +121,7 @@ __device__ __forceinline__ int encode_v(float v, float scale) {
 // block of ten, the wave takes the exact form. Blocks whose quotients or reciprocal of
 // the scale may leave the normal range (the hardware's reciprocal is 0 there) take it
 // always: scales below 1e-30 or above 8e37, just under 2^126, and NaN.
-// (189 million elements: all exact 740 us, VALU bound; so 540 to 575.)
+// (189 million elements: all exact 740 us, VALU bound; so 540.)
 constexpr float kNearHalf = 0.4998f;
 __device__ __forceinline__ bool plain_scale(float scale) { return scale >= 1e-30f && scale <= 8e37f; }
 __device__ __forceinline__ void encode_m4(const float (&m)[4], float scale, int8_t (&q)[4]) {

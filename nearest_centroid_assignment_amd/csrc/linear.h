@@ -316,12 +316,13 @@ __device__ __forceinline__ void wait_loads() {
 // pause while the other reads, moves the stage three later in and waits for the next
 // one. A barrier ends each phase.
 // 8192^3 bf16, against `product` with two stages of 128 bytes: 9 % fewer cycles (the
-// matrix units busy 73 % of them, before 67 %), but 1.5 % less time, 813 us, since the
-// clock falls to 1.76 GHz from 1.87: at this rate the chip's power sets the pace (a
-// loop of nothing but these matrix instructions reaches 2.1 PFLOP/s). Shorter
-// products gain more (17 experts, 32768 x 4096 with depth 2048, 658 -> 625 us). dw,
-// both of whose operands are read by column, has 8192^3 2 % and 8192 x 2048 with depth
-// 8192 6 % slower this way, 17 experts 2 % faster: it keeps `product`.
+// matrix units busy 72 % of them, before 66 %), but 2 to 3 % less time (872 us under the
+// counters, before 901), since the clock falls to 1.66 GHz from 1.76: at this rate the
+// chip's power sets the pace (a loop of nothing but these matrix instructions reaches 2.1
+// PFLOP/s). Of 17 experts (32768 x 2048 with depth 4096, f16) the units are busy 51 % of
+// the cycles: there each tile's first loads and its epilogue, in rounds of 256 tiles, count
+// as much. dw, both of whose operands are read by column, has 8192^3 2 % and 8192 x 2048
+// with depth 8192 6 % slower this way, 17 experts 2 % faster: it keeps `product`.
 template <class S>
 __device__ __forceinline__ void product_in_turns(lds_char *smem, typename S::TileP &tp,
                                                  typename S::TileQ &tq, int depth, int wave,
@@ -529,8 +530,9 @@ __device__ __forceinline__ void store_whole(T *p, const float (&v)[8]) {
 // stages' memory), so that a wave's accesses to memory are whole rows of the tile,
 // 16 bytes a lane, where the matrix instruction leaves a lane four columns of one
 // row. (Stored as it leaves them, 8 bytes a lane: 8192 x 8192 x 2048 with gelu 318 us
-// against 287.) `load(row, col)` gives the aux of a place; it is asked for kAhead
-// blocks of 16 rows ahead, or its latency would be paid again for every block.
+// against 287, both before the epilogue chose its activation once.) `load(row, col)`
+// gives the aux of a place; it is asked for kAhead blocks of 16 rows ahead, or its latency
+// would be paid again for every block.
 template <class S, class Aux, class L, class F>
 __device__ __forceinline__ void by_rows(lds_char *smem, int wave, int lane,
                                         const f32x4 (&acc)[S::TM][S::TN], L load, F use) {

@@ -572,7 +572,9 @@ def adamw_step(params, grads, m, v, lr, betas=(0.9, 0.999), eps=1e-8, weight_dec
     parameters, one for the gradients; a tensor that is shared is given once). m, v (and the scales of 8-bit moments)
     as made by adamw_state. ``copies``: bfloat16 tensors that receive the new
     parameters. ``grad_scale``: a float32 GPU tensor of one element that
-    multiplies the gradients (clipping, loss scaling). step counts from 1."""
+    multiplies the gradients (clipping, loss scaling); the step is taken whatever
+    it holds, so an infinite or NaN gradient reaches the moments: with loss scaling,
+    look at the gradients before the call. step counts from 1."""
     if stream is None and (_native or _module()).adamw_step(
             params, grads, m, v, lr, betas[0], betas[1], eps, weight_decay, step, m_scale, v_scale,
             copies, grad_scale):
