@@ -108,9 +108,10 @@ int experts_combine_backward(const void *dy, int64_t lddy, const void *ys, int64
  *   bias      (outs) or (experts, outs), dense, or NULL.
  *   residual  or NULL. pre: output, or NULL.
  *   offsets   NULL (experts is then 1 and every row uses w), or the plan's
- *             (experts + 1) int32: expert e has the rows [offsets[e],
- *             offsets[e + 1]). Rows from offsets[experts] on become zero in
- *             out and pre.
+ *             (experts + 1) int32: offsets[0] is 0 and expert e has the rows
+ *             [offsets[e], offsets[e + 1]). Rows from offsets[experts] on become
+ *             zero in out and pre. (Other values leave rows unwritten, but make no
+ *             call read or write outside its matrices.)
  * 0 <= rows < 2^31; 1 <= outs, ins <= 2^20; 1 <= experts <= 65536; ld <= 2^20;
  * and one dispatch has to hold the call: rows * outs < 2^35 - 2^12 (rows * ins too for
  * the gradient and the 16-bit types, for these also experts * outs * ins; outs and ins

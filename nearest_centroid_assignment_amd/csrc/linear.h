@@ -506,6 +506,8 @@ struct Groups {
                 r.lo = __builtin_amdgcn_readlane(lo, l);
                 r.hi = __builtin_amdgcn_readlane(hi, l);
                 r.tile = mt - __builtin_amdgcn_readlane(incl - tiles, l);
+                // (Offsets that no plan makes can give more tiles than an int counts.)
+                if (r.tile < 0 || r.tile >= __builtin_amdgcn_readlane(tiles, l)) r.expert = -1;
                 return r;
             }
             before = __builtin_amdgcn_readlane(incl, 63);
@@ -611,7 +613,7 @@ __device__ __forceinline__ void rows_block(const RowsArgs &a, int block, lds_cha
     const int tiles_m = pr.offsets ? groups.total() : (rows + S::BM - 1) / S::BM;
     const int tiles = tiles_m * tiles_n;
     int id = xcd_tile(block, tiles * pr.splits, 0);
-    if (id < 0) return;
+    if (id < 0 || tiles_m < 1) return;  // (tiles_m < 1: an int did not hold them)
     const int part = __builtin_amdgcn_readfirstlane(id / tiles);
     id -= part * tiles;
     int mt, nt;

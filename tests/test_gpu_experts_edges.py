@@ -355,3 +355,44 @@ def test_rows_at_thresholds(dtype, width, tokens):
     terms = f64(rows) * f64(dy)[:, None]
     close(dweights, terms.sum(2), summed(width) * terms.abs().sum(2), "dweights")
     assert not dys[live:].any()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,outs,ins", [(5, 72, 40), (70, 16, 24), (3, 264, 1100)])
+def test_offsets_of_no_plan(dtype, n, outs, ins):
+    """Offsets that are out of order, negative or past the rows: nothing is written
+    outside the outputs, and the gradients of w read nothing around the inputs (NaN).
+    Rows of out that no expert has are left to chance."""
+    gu.announce(f"offsets of no plan: {dtype} {n} experts {outs} x {ins}")
+    rows, rng = 300, np.random.default_rng(n)
+    for kind in range(3):
+        offsets = rng.integers(-50, rows + 50, n + 1) if kind else np.arange(n + 1) % 2 * rows
+        if kind == 2:
+            offsets = np.where(rng.random(n + 1) < 0.5, 2**31 - 1, -2**31)
+        offsets = torch.from_numpy(offsets).to(torch.int32).cuda()
+        # A guard of a row and more on every side of x, dy and out.
+        full = [torch.full((rows + 4, k + 6), float("nan"), dtype=dtype, device="cuda") for k in (ins, outs, outs)]
+        x, dy, out = (t[2:-2, 2:2 + k] for t, k in zip(full, (ins, outs, outs)))
+        x.copy_(randn(1, rows, ins)), dy.copy_(randn(2, rows, outs)), out.zero_()
+        w = randn(3, n, outs, ins, dtype=dtype, scale=0.1)
+        experts.linear(x, w, offsets=offsets, act="silu", out=out)
+        dw, db = experts.linear_backward(dy, x, w, offsets=offsets, need_dx=False)[1:]
+        assert torch.isfinite(dw).all() and torch.isfinite(db).all()
+        guard = torch.ones_like(full[2], dtype=torch.bool)
+        guard[2:-2, 2:2 + outs] = False
+        assert torch.isnan(full[2][guard]).all()
+
+
+def test_more_tiles_than_an_int():
+    """As above, where the tiles that the offsets describe pass 2^31."""
+    rows, n, k = 1 << 23, 65536, 8
+    offsets = (torch.arange(n + 1, device="cuda") % 2 * rows).to(torch.int32)
+    x = torch.zeros(rows, k, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(n, k, k, dtype=torch.bfloat16, device="cuda")
+    assert (rows // 128) * (n // 2) >= 2**31  # (the tiles are of 64 to 256 rows)
+    full = torch.full((rows + 1024, k), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = full[512:-512]
+    gu.announce("more tiles than an int")
+    experts.linear(x, w, offsets=offsets, out=out)
+    assert bool((full[:512] == 7).all()) and bool((full[-512:] == 7).all())
+    assert bool(((out == 0) | (out == 7)).all())
