@@ -16,7 +16,8 @@ LIB_NAME = "libkmeans_mi355x.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.hip", "assign.hip", "update.hip", "fit.hip", "kmeanspp.hip",
            "experts_api.hip", "tokens.hip", "linear.hip", "linear_bf16.hip", "linear_f16.hip",
-           "linear_f32.hip", "adamw.hip"]
+           "linear_f32.hip", "adamw.hip", "layers_api.hip", "embed.hip", "norm.hip", "route.hip",
+           "entropy.hip", "entropy_bf16.hip", "entropy_f16.hip", "entropy_f32.hip"]
 # Calibration kernels for the measurements (copy, MFMA loop): a separate library.
 CALIB_NAME = "libkm_calib.so"
 CALIB_PATH = os.path.join(HERE, CALIB_NAME)

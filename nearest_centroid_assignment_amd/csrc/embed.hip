@@ -1,0 +1,329 @@
+// embed.hip - rows of a table by number, scaled, and the table's gradient.
+//
+//   y[t] = scale * w[ids[t]]          dw[v] = scale * sum over t with ids[t] = v of dy[t]
+//
+// Bound by memory: the lookup reads the rows that come up and writes y; the gradient
+// reads dy once and writes every row of dw once. The gradient sorts the tokens by number
+// (stable, so the sums have one order and no atomic), cuts the sorted places into chunks
+// of equal length, whatever the numbers' frequencies, and gives a wave or a block to each
+// chunk: a row whose tokens all lie in one chunk is written by it; of the others each
+// chunk leaves a float32 part, and a second kernel adds a row's parts in order and clears
+// the rows that no token has.
+#include "layers.h"
+#include "kernels.h"
+#include "rows.h"
+
+namespace kx {
+namespace {
+
+template <typename T, int NT, bool ONCE>
+__global__ __launch_bounds__(256) void embed_kernel(const int64_t *__restrict__ ids, int64_t tokens,
+                                                    const T *__restrict__ w, int64_t classes,
+                                                    int64_t width, float scale, T *__restrict__ out,
+                                                    int64_t ldo) {
+    constexpr int V = vec<T>();
+    const int64_t t = own_token<NT>();
+    if (t >= tokens) return;
+    const int64_t id = ids[t];
+    const bool live = id >= 0 && id < classes;
+    const T *p = w + (live ? id : 0) * width;
+#pragma unroll 4
+    for (int64_t c = (threadIdx.x % NT) * V; c < width; c += NT * V) {
+        const int64_t a = chunk_at<V>(c, width);
+        T v[V];
+        if (live) {
+            load_part<false, T, V>(p + a, width - a, v);
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = (T)(scale * (float)v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[j] = (T)0.0f;
+        }
+        store_part<ONCE, T, V>(out + t * ldo + a, width - a, v);
+    }
+}
+
+// The bucket of every token: its number modulo kEmbedBuckets, which spreads numbers that
+// lie together (frequent ones often do).
+__global__ __launch_bounds__(256) void bucket_kernel(const int64_t *__restrict__ ids,
+                                                     int64_t tokens, int64_t classes,
+                                                     int64_t *__restrict__ bucket) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= tokens) return;
+    const int64_t id = ids[t];
+    bucket[t] = id >= 0 && id < classes ? id & (kEmbedBuckets - 1) : -1;
+}
+
+// One block sorts one bucket's tokens by their number, stably: a count, a prefix over
+// the bucket's numbers (at most `locals`), and the tokens in rounds of 256.
+__global__ __launch_bounds__(256) void refine_kernel(const int64_t *__restrict__ ids,
+                                                     int64_t classes, const int *__restrict__ order,
+                                                     const int *__restrict__ offsets, int locals,
+                                                     int *__restrict__ sorted, int *__restrict__ lo,
+                                                     int *__restrict__ hi) {
+    extern __shared__ int base[];  // locals; then 4 x locals: counts of a round, by wave
+    int *count = base + locals;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int b = blockIdx.x;
+    const int first = offsets[b], members = offsets[b + 1] - first;
+    auto local = [&](int i) { return (int)(ids[order[first + i]] / kEmbedBuckets); };
+    for (int j = tid; j < 5 * locals; j += 256) base[j] = 0;
+    __syncthreads();
+    for (int i = tid; i < members; i += 256) atomicAdd(&base[local(i)], 1);
+    __syncthreads();
+    if (wave == 0) {
+        int run = first;
+        for (int l0 = 0; l0 < locals; l0 += 64) {
+            const int l = l0 + tid;
+            const int n = l < locals ? base[l] : 0;
+            const int incl = wave_incl_scan(n);
+            const int at = run + incl - n;
+            const int64_t v = (int64_t)l * kEmbedBuckets + b;
+            if (l < locals) {
+                base[l] = at;
+                if (v < classes) {
+                    lo[v] = at;
+                    hi[v] = at + n;
+                }
+            }
+            run += __builtin_amdgcn_readlane(incl, 63);
+        }
+    }
+    __syncthreads();
+    const int bits = 32 - __clz(locals);
+    for (int r = 0; r < members; r += 256) {
+        const int i = r + tid;
+        const int token = i < members ? order[first + i] : -1;
+        const int l = token >= 0 ? local(i) : -1;
+        int rank, same;
+        wave_rank(l, bits, rank, same);
+        if (l >= 0 && rank == 0) count[wave * locals + l] = same;
+        __syncthreads();
+        if (l >= 0) {
+            int at = base[l] + rank;
+            for (int w = 0; w < wave; ++w) at += count[w * locals + l];
+            sorted[at] = token;
+        }
+        __syncthreads();
+        if (l >= 0 && rank == 0) {  // the order of these integer sums does not matter
+            atomicAdd(&base[l], same);
+            count[wave * locals + l] = 0;
+        }
+        __syncthreads();
+    }
+}
+
+struct SumArgs {
+    int64_t lddy, width;
+    const int64_t *ids;
+    const int *order, *total, *lo, *hi;  // total: places with a token
+    int64_t classes;
+    int chunk, col_blocks;
+    float scale;
+    float *partial;
+};
+
+// Chunk c's part of a row whose tokens start at `lo`: a row that starts inside the chunk
+// has the second of its two slots, the one that starts before it, or with it, the first.
+__device__ __forceinline__ int64_t slot_of(int64_t c, int chunk, int lo) {
+    return 2 * c + (lo > c * chunk ? 1 : 0);
+}
+
+template <typename T, int V, int NT>
+__global__ __launch_bounds__(256) void sum_kernel(SumArgs a, const T *__restrict__ dy,
+                                                  T *__restrict__ dw) {
+    constexpr int kAhead = 8;
+    const int64_t unit = own_token<NT>();
+    const int64_t c = unit / a.col_blocks;
+    const int64_t col = ((unit - c * a.col_blocks) * NT + threadIdx.x % NT) * V;
+    const int64_t p0 = c * a.chunk, total = *a.total;
+    if (p0 >= total) return;
+    const int64_t p1 = p0 + a.chunk < total ? p0 + a.chunk : total;
+    const bool active = col < a.width;
+    const int64_t at = active ? chunk_at<V>(col, a.width) : 0;
+    const int64_t left = active ? a.width - at : 0;
+    float sum[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+    int64_t id = a.ids[a.order[p0]];
+    auto flush = [&]() {
+        const int lo = a.lo[id], hi = a.hi[id];
+        if (lo >= p0 && hi <= p1) {
+            T r[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) r[j] = (T)(a.scale * sum[j]);
+            store_part<false, T, V>(dw + id * a.width + at, left, r);
+        } else {
+            store_part<false, float, V>(a.partial + slot_of(c, a.chunk, lo) * a.width + at, left, sum);
+        }
+    };
+    for (int64_t p = p0; p < p1; p += kAhead) {
+        int64_t token[kAhead], next[kAhead];
+        T v[kAhead][V];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) token[u] = a.order[p + u < p1 ? p + u : p1 - 1];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            next[u] = a.ids[token[u]];
+            load_part<false, T, V>(dy + token[u] * a.lddy + at, left, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (p + u >= p1) break;
+            if (next[u] != id) {
+                flush();
+                id = next[u];
+#pragma unroll
+                for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] += (float)v[u][j];
+        }
+    }
+    flush();
+}
+
+// The first `joins` blocks: chunk c and 256 columns; the row that starts in chunk c and
+// goes on past it, if there is one, is the sum of its chunks' parts (four waves, each
+// every fourth part). The blocks after them clear the rows without a token, a wave each.
+template <typename T>
+__global__ __launch_bounds__(256) void finish_kernel(SumArgs a, int64_t joins, T *__restrict__ dw) {
+    constexpr int V = vec<T>();
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (blockIdx.x >= joins) {
+        const int64_t v = (int64_t)(blockIdx.x - joins) * 4 + wave;
+        if (v >= a.classes || a.lo[v] < a.hi[v]) return;
+        T zero[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) zero[j] = (T)0.0f;
+        for (int64_t col = lane * V; col < a.width; col += 64 * V) {
+            const int64_t at = chunk_at<V>(col, a.width);
+            store_part<false, T, V>(dw + v * a.width + at, a.width - at, zero);
+        }
+        return;
+    }
+    __shared__ float part[4][256];
+    const int64_t cols = (a.width + 255) / 256;
+    const int64_t c = blockIdx.x / cols;
+    const int64_t p0 = c * a.chunk, p1 = p0 + a.chunk;
+    if (p1 >= *a.total) return;  // the last chunk: nothing goes on
+    const int64_t id = a.ids[a.order[p1 - 1]];
+    const int lo = a.lo[id], hi = a.hi[id];
+    if (lo < p0 || hi <= p1) return;
+    const int64_t col = (blockIdx.x - c * cols) * 256 + lane * 4;
+    float sum[4] = {0, 0, 0, 0};
+    const int64_t left = a.width - col, last = (hi - 1) / a.chunk;
+    if (left > 0) {
+#pragma unroll 8
+        for (int64_t k = c + wave; k <= last; k += 4) {
+            float v[4];
+            load_part<false, float, 4>(a.partial + slot_of(k, a.chunk, lo) * a.width + col, left, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum[j] += v[j];
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[wave][lane * 4 + j] = sum[j];
+    __syncthreads();
+    const int64_t out = (blockIdx.x - c * cols) * 256 + threadIdx.x;
+    if (out < a.width) {
+        const int i = threadIdx.x;
+        dw[id * a.width + out] =
+            (T)(a.scale * ((part[0][i] + part[1][i]) + (part[2][i] + part[3][i])));
+    }
+}
+
+// A wave to a token's row where there are enough of them and they are short, else a block
+// (the rule of the token rows in tokens.hip).
+constexpr int64_t kMostBlocks = 1 << 24;
+bool by_wave(int64_t rows, int64_t bytes) {
+    return rows >= kMostBlocks || (rows >= 2048 && bytes <= 3 << 10);
+}
+
+template <typename T>
+hipError_t embed_t(const int64_t *ids, int64_t tokens, const void *w, int64_t classes, int64_t width,
+                   float scale, void *out, int64_t ldo, hipStream_t s) {
+    const int64_t bytes = width * (int64_t)sizeof(T);
+    const bool once = bytes % 128 == 0 && ldo * (int64_t)sizeof(T) % 128 == 0 && tokens * bytes > 256 << 20;
+    if (by_wave(tokens, bytes))
+        return launch(once ? embed_kernel<T, 64, true> : embed_kernel<T, 64, false>, cdiv(tokens, 4),
+                      256, 0, s, ids, tokens, (const T *)w, classes, width, scale, (T *)out, ldo);
+    return launch(once ? embed_kernel<T, 256, true> : embed_kernel<T, 256, false>, tokens, 256, 0, s,
+                  ids, tokens, (const T *)w, classes, width, scale, (T *)out, ldo);
+}
+
+// Threads and values a thread that a chunk's rows take: as many lanes busy as there are.
+template <typename T, class F>
+hipError_t with_rows(int64_t width, F f) {
+    constexpr int V = vec<T>();
+    if (width <= 64 * V / 4) return f(ActTag<V / 4>{}, ActTag<64>{});
+    if (width <= 64 * V) return f(ActTag<V>{}, ActTag<64>{});
+    return f(ActTag<V>{}, ActTag<256>{});
+}
+
+template <typename T>
+hipError_t backward_t(SumArgs a, int64_t tokens, const void *dy, void *dw, hipStream_t s) {
+    const int64_t chunks = cdiv(tokens, a.chunk);
+    hipError_t e = hipSuccess;
+    if (tokens > 0)
+        e = with_rows<T>(a.width, [&](auto v, auto nt) {
+            constexpr int V = decltype(v)::value, NT = decltype(nt)::value;
+            a.col_blocks = (int)cdiv(a.width, V * NT);
+            return launch(sum_kernel<T, V, NT>, cdiv(chunks * a.col_blocks, 256 / NT), 256, 0, s, a,
+                          (const T *)dy, (T *)dw);
+        });
+    if (e != hipSuccess) return e;
+    const int64_t joins = chunks * cdiv(a.width, 256);
+    return launch(finish_kernel<T>, joins + cdiv(a.classes, 4), 256, 0, s, a, joins, (T *)dw);
+}
+
+}  // namespace
+
+int64_t embed_chunk(int64_t tokens) { return tokens >= 65536 ? 64 : tokens >= 16384 ? 32 : 16; }
+
+bool embed_grid_ok(int dtype, int64_t tokens, int64_t classes, int64_t width) {
+    const int64_t chunks = cdiv(tokens, embed_chunk(tokens));
+    const int64_t v = dtype == 0 ? 4 : 8;
+    return chunks * cdiv(width, 64 * v) + 4 < kMostBlocks &&
+           chunks * cdiv(width, 256) + cdiv(classes, 4) < kMostBlocks;
+}
+
+hipError_t launch_embed(const int64_t *ids, int64_t tokens, const void *w, int dtype,
+                        int64_t classes, int64_t width, float scale, void *out, int64_t ldo,
+                        hipStream_t s) {
+    if (tokens == 0) return hipSuccess;
+    if (dtype == 0) return embed_t<float>(ids, tokens, w, classes, width, scale, out, ldo, s);
+    if (dtype == 1) return embed_t<bf16>(ids, tokens, w, classes, width, scale, out, ldo, s);
+    return embed_t<f16>(ids, tokens, w, classes, width, scale, out, ldo, s);
+}
+
+hipError_t launch_embed_backward(const void *dy, int64_t lddy, const int64_t *ids, int64_t tokens,
+                                 int dtype, int64_t classes, int64_t width, float scale, void *dw,
+                                 const EmbedScratch &ws, hipStream_t s) {
+    SumArgs a = {lddy, width, ids, ws.order, nullptr, ws.offsets, ws.offsets + 1, classes,
+                 (int)embed_chunk(tokens), 1, scale, ws.partial};
+    hipError_t e;
+    if (classes <= kEmbedDirect) {
+        e = launch_plan(ids, tokens, classes, ws.order, ws.place, ws.offsets, ws.plan, s);
+        a.total = ws.offsets + classes;
+    } else {
+        e = tokens ? launch(bucket_kernel, cdiv(tokens, 256), 256, 0, s, ids, tokens, classes, ws.bucket)
+                   : hipSuccess;
+        if (e == hipSuccess)
+            e = launch_plan(ws.bucket, tokens, kEmbedBuckets, ws.order, ws.place, ws.offsets, ws.plan, s);
+        const int locals = (int)cdiv(classes, kEmbedBuckets);
+        if (e == hipSuccess)
+            e = launch(refine_kernel, kEmbedBuckets, 256, (size_t)5 * locals * sizeof(int), s, ids,
+                       classes, ws.order, ws.offsets, locals, ws.sorted, ws.lo, ws.hi);
+        a.total = ws.offsets + kEmbedBuckets;
+        a.order = ws.sorted;
+        a.lo = ws.lo;
+        a.hi = ws.hi;
+    }
+    if (e != hipSuccess) return e;
+    if (dtype == 0) return backward_t<float>(a, tokens, dy, dw, s);
+    if (dtype == 1) return backward_t<bf16>(a, tokens, dy, dw, s);
+    return backward_t<f16>(a, tokens, dy, dw, s);
+}
+
+}  // namespace kx

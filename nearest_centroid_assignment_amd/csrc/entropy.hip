@@ -1,0 +1,175 @@
+// entropy.hip - what surrounds the products of entropy.h: the choice of the type, the
+// joins of the rows' sums and of split depths, and dz's scale.
+#include "layers.h"
+
+namespace kx {
+
+template <typename T>
+hipError_t launch_entropy_t(const EntropyProblem &pr, bool dz, hipStream_t s);
+template <typename T>
+hipError_t launch_entropy_dx_t(const EntropyGrad &e, hipStream_t s);
+template <typename T>
+hipError_t launch_entropy_dw_t(const EntropyGrad &e, hipStream_t s);
+
+namespace {
+
+// 16 rows a block, 16 threads to a row, each joining every 16th of the column tiles' sums
+// (the largest first, then the sums relative to it).
+__global__ __launch_bounds__(256) void entropy_join_kernel(EntropyProblem pr, int tiles) {
+    __shared__ float most[16][17], sums[16][17];
+    const int r = threadIdx.x & 15, slice = threadIdx.x >> 4;
+    const int64_t row = (int64_t)blockIdx.x * 16 + r;
+    const bool there = row < pr.rows;
+    const float2 *part = pr.part + (there ? row : pr.rows - 1);
+    constexpr float kLog2e = 1.44269504088896f;
+    auto finite_or_0 = [](float m) { return fabsf(m) < INFINITY ? m : 0.0f; };
+    float m = -INFINITY, s = 0.0f;
+    for (int k0 = slice; k0 < tiles; k0 += 16 * 8) {
+        float2 v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int k = k0 + 16 * u;
+            v[u] = part[(int64_t)(k < tiles ? k : k0) * pr.rows];
+            if (k >= tiles) v[u] = make_float2(-INFINITY, 0.0f);
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) top = fmaxf(top, v[u].x);
+        const float from = finite_or_0(top);
+        // (Nothing times an overflowing factor would be a NaN.)
+        s = s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f((finite_or_0(m) - from) * kLog2e);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            s += v[u].y == 0.0f ? 0.0f
+                                : v[u].y * __builtin_amdgcn_exp2f((finite_or_0(v[u].x) - from) * kLog2e);
+        m = top;
+    }
+    most[slice][r] = m;
+    sums[slice][r] = s;
+    __syncthreads();
+    if (slice != 0 || !there) return;
+    for (int k = 1; k < 16; ++k) m = fmaxf(m, most[k][r]);
+    const float from = finite_or_0(m);
+    float sum = 0.0f;
+    for (int k = 0; k < 16; ++k)
+        sum += sums[k][r] == 0.0f
+                   ? 0.0f
+                   : sums[k][r] * __builtin_amdgcn_exp2f((finite_or_0(most[k][r]) - from) * kLog2e);
+    const float lse = from + logf(sum);
+    const int64_t t = pr.targets[row];
+    pr.lse[row] = lse;
+    pr.loss[row] = t >= 0 && t < pr.classes ? lse - pr.hit[row] : 0.0f;
+}
+
+// float16 holds 2^-24 to 65504, and dz of a mean over many rows and classes lies below:
+// dz is kept times the power of two that brings the largest of its factors to 2^13 to
+// 2^14, and dx and dw are multiplied by its inverse, both exactly.
+__global__ __launch_bounds__(1024) void entropy_scale_kernel(EntropyProblem pr, float *scale) {
+    __shared__ float most[16];
+    float m = 0.0f;
+    bool odd = false;
+    for (int64_t r = threadIdx.x; r < pr.rows; r += 1024) {
+        const int64_t t = pr.targets[r];
+        const float b = t >= 0 && t < pr.classes ? pr.dloss[r] : 0.0f;
+        const float a = b + (pr.dlse ? pr.dlse[r] : 0.0f);
+        odd |= !(fabsf(a) < INFINITY);
+        m = fmaxf(m, fmaxf(fabsf(a), fabsf(b)));
+    }
+    if (__any(odd)) m = INFINITY;
+#pragma unroll
+    for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
+    if ((threadIdx.x & 63) == 0) most[threadIdx.x >> 6] = m;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int w = 1; w < 16; ++w) m = fmaxf(m, most[w]);
+    int e = 0;
+    if (m > 0.0f && m < INFINITY) {
+        frexpf(m, &e);
+        e = 14 - e;
+        e = e < -100 ? -100 : e > 100 ? 100 : e;
+    }
+    *scale = ldexpf(1.0f, e);
+}
+
+// A product whose depth was split: eight columns of a row a thread, the parts added in
+// order, then the piece before.
+template <typename T>
+__global__ __launch_bounds__(256) void entropy_parts_kernel(const float *__restrict__ partial,
+                                                            int splits, int64_t rows, int64_t cols,
+                                                            float *__restrict__ sum, bool first,
+                                                            bool last, const float *__restrict__ scale,
+                                                            T *__restrict__ out, int64_t ldo) {
+    const int64_t chunks = (cols + 7) / 8;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = id / chunks, n = (id - m * chunks) * 8;
+    if (m >= rows) return;
+    const int valid = (int)(cols - n < 8 ? cols - n : 8);
+    float z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (!first) load_row(sum + m * cols + n, valid, z);
+#pragma unroll 4
+    for (int k = 0; k < splits; ++k) {
+        float x[8];
+        load_row(partial + ((int64_t)k * rows + m) * cols + n, valid, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] += x[i];
+    }
+    if (!last) {
+        store_row(sum + m * cols + n, z, valid);
+        return;
+    }
+    const float alpha = scale ? 1.0f / *scale : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= alpha;
+    store_row(out + m * ldo + n, z, valid);
+}
+
+template <typename T>
+hipError_t grad_t(const EntropyGrad &g, hipStream_t s) {
+    hipError_t e = hipSuccess;
+    if (g.dx) {
+        e = launch_entropy_dx_t<T>(g, s);
+        if (e == hipSuccess && g.dx_cut.splits > 1)
+            e = launch(entropy_parts_kernel<T>, cdiv(g.rows * cdiv(g.width, 8), 256), 256, 0, s, g.partial,
+                       g.dx_cut.splits, g.rows, g.width, g.sum, g.first, g.last, g.scale, (T *)g.dx, g.lddx);
+    }
+    if (e != hipSuccess || !g.dw) return e;
+    e = launch_entropy_dw_t<T>(g, s);
+    if (e == hipSuccess && g.dw_cut.splits > 1)
+        e = launch(entropy_parts_kernel<T>, cdiv(g.count * cdiv(g.width, 8), 256), 256, 0, s, g.partial,
+                   g.dw_cut.splits, g.count, g.width, (float *)nullptr, true, true, g.scale, (T *)g.dw,
+                   g.width);
+    return e;
+}
+
+}  // namespace
+
+Cut entropy_plan(int dtype, int64_t rows, int64_t classes, int64_t width) {
+    return whole_plan(dtype, rows, classes, width);
+}
+int entropy_columns(int, const Cut &cut) { return cut.tile == 129 ? 128 : cut.tile == 32 ? 64 : cut.tile; }
+
+hipError_t launch_entropy(int dtype, const EntropyProblem &pr, hipStream_t s) {
+    hipError_t e;
+    if (dtype == 0)
+        e = launch_entropy_t<float>(pr, false, s);
+    else
+        e = dtype == 1 ? launch_entropy_t<bf16>(pr, false, s) : launch_entropy_t<f16>(pr, false, s);
+    if (e != hipSuccess) return e;
+    Cut cut = {};
+    cut.tile = pr.tile;
+    return launch(entropy_join_kernel, cdiv(pr.rows, 16), 256, 0, s, pr,
+                  (int)cdiv(pr.count, entropy_columns(dtype, cut)));
+}
+hipError_t launch_entropy_dz(int dtype, const EntropyProblem &pr, hipStream_t s) {
+    if (dtype == 0) return launch_entropy_t<float>(pr, true, s);
+    return dtype == 1 ? launch_entropy_t<bf16>(pr, true, s) : launch_entropy_t<f16>(pr, true, s);
+}
+hipError_t launch_entropy_scale(const EntropyProblem &pr, float *scale, hipStream_t s) {
+    return launch(entropy_scale_kernel, 1, 1024, 0, s, pr, scale);
+}
+hipError_t launch_entropy_grad(int dtype, const EntropyGrad &g, hipStream_t s) {
+    if (dtype == 0) return grad_t<float>(g, s);
+    return dtype == 1 ? grad_t<bf16>(g, s) : grad_t<f16>(g, s);
+}
+
+}  // namespace kx

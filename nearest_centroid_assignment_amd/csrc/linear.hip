@@ -303,12 +303,12 @@ bool lines(int64_t len, int64_t size) { return len * size % 128 == 0; }
 // sums: values to join.
 template <class F>
 Cut best_cut(int dtype, int64_t stages, int64_t bytes, int64_t sums, bool grouped,
-             bool on_lines, F tiles_of) {
+             bool on_lines, F tiles_of, int most_parts = 8) {
     Cut best = {64, 1, false, 0.0};
     double least = 1e300;
     for (const TileCost &c : dtype == 0 ? kFloat : kHalf) {
         const int64_t tiles = tiles_of(c.rows, c.cols);
-        for (int parts = 1; parts <= 8; parts *= 2) {
+        for (int parts = 1; parts <= most_parts; parts *= 2) {
             if (parts > 1 && (stages / parts < 4 || tiles * parts > 1024)) break;
             const double rounds = (double)cdiv(tiles * parts, 256);
             const double each = c.each * (on_lines ? 1.0 : c.apart);
@@ -358,6 +358,15 @@ Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped
     // experts, 25.7 / 27.8, of 6932 x 1068 x 3888, 4 experts, 82 / 134.
     const int64_t most = most_row_tiles(rows, 128, grouped, experts) * cdiv(cols, 128);
     if (c.tile == 128 && dtype != 0 && most <= 256) c.tile = 129;
+    return c;
+}
+
+Cut whole_plan(int dtype, int64_t rows, int64_t cols, int64_t depth) {
+    auto tiles = [&](int64_t m, int64_t n) { return cdiv(rows, m) * cdiv(cols, n); };
+    const int64_t size = dtype == 0 ? 4 : 2;
+    Cut c = best_cut(dtype, cdiv(depth * size, 128), (rows + cols) * depth * size, rows * cols, false,
+                     lines(depth, size), tiles, 1);
+    if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
     return c;
 }
 

@@ -14,6 +14,7 @@
 // are all the pairs', goes by place instead.
 #include "experts.h"
 #include "kernels.h"
+#include "rows.h"
 
 namespace kx {
 namespace {
@@ -24,19 +25,6 @@ constexpr int kSmallPairs = kSmallTiles * 1024;
 constexpr int kWaveCounts = 65536;                 // counts of (wave, expert) in LDS: 128 KB
 constexpr int kPlaceTiles = 256, kPlaceExperts = 2048;  // most of the two-launch sort
 
-// Rank of the lane's expert among the wave's lanes with the same one and a lower
-// index, and how many have it; both 0 where expert < 0. `bits`: of the largest expert.
-__device__ __forceinline__ void wave_rank(int expert, int bits, int &rank, int &count) {
-    const int lane = threadIdx.x & 63;
-    unsigned long long same = __ballot(expert >= 0);
-    for (int b = 0; b < bits; ++b) {
-        const bool set = (expert >> b) & 1;
-        const unsigned long long with = __ballot(set);
-        same &= set ? with : ~with;
-    }
-    rank = expert < 0 ? 0 : __popcll(same & ((1ull << lane) - 1ull));
-    count = expert < 0 ? 0 : __popcll(same);
-}
 __device__ __forceinline__ int bits_of(int64_t experts) { return 64 - __clzll((unsigned long long)experts); }
 
 __device__ __forceinline__ int expert_of(const int64_t *ids, int64_t i, int64_t pairs, int64_t experts) {
@@ -257,53 +245,6 @@ __global__ __launch_bounds__(1024) void plan_small_kernel(const int64_t *__restr
 // A row is moved 16 bytes a thread; NT threads (64 or 256) walk a token's row.
 // `width` need not be a multiple of the vector, nor the rows be aligned to it.
 
-template <typename T>
-constexpr int vec() {
-    return 16 / (int)sizeof(T);
-}
-
-template <bool ONCE, typename T, int V>
-__device__ __forceinline__ void load_part(const T *p, int64_t left, T (&v)[V]) {
-    if (left >= V) {
-        if (ONCE)
-            load_once(p, v);
-        else
-            load_vec(p, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = j < left ? p[j] : (T)0.0f;
-    }
-}
-template <bool ONCE, typename T, int V>
-__device__ __forceinline__ void store_part(T *p, int64_t left, const T (&v)[V]) {
-    if (left >= V) {
-        if (ONCE)
-            store_once(p, v);
-        else
-            store_vec(p, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            if (j < left) p[j] = v[j];
-    }
-}
-
-// Where the chunk of V values at c is read and written: the last one, where it would
-// leave the row, over the end of the one before (1001-wide rows, against one lane
-// going value by value: 15009 f16 rows, all five operators 65 us).
-template <int V>
-__device__ __forceinline__ int64_t chunk_at(int64_t c, int64_t width) {
-    return width >= V && c + V > width ? width - V : c;
-}
-
-// The token, or place, of this wave (NT = 64) or block.
-template <int NT>
-__device__ __forceinline__ int64_t own_token() {
-    const int64_t t = (int64_t)blockIdx.x * (256 / NT) + (NT == 64 ? threadIdx.x >> 6 : 0);
-    return ((int64_t)__builtin_amdgcn_readfirstlane((int)(t >> 32)) << 32) |
-           (uint32_t)__builtin_amdgcn_readfirstlane((int)t);
-}
-
 // Zero the rows among places [t * top, t * top + top) that hold no pair.
 template <typename T, int NT>
 __device__ __forceinline__ void clear_empty(const int *order, int64_t t, int64_t top, T *rows,
@@ -373,21 +314,6 @@ __global__ __launch_bounds__(256) void combine_kernel(const T *__restrict__ ys, 
         for (int j = 0; j < V; ++j) r[j] = (T)sum[j];
         store_part<false, T, V>(y + t * ldy + a, width - a, r);
     }
-}
-
-// Sum over the NT threads of a token, in a fixed order, to all of them.
-template <int NT>
-__device__ __forceinline__ float token_sum(float v) {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-    if (NT == 256) {
-        __shared__ float part[4];
-        __syncthreads();
-        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
-        __syncthreads();
-        v = (part[0] + part[1]) + (part[2] + part[3]);
-    }
-    return v;
 }
 
 // One place a wave (or block): its row of ys is read and its row of dys written in
