@@ -127,8 +127,8 @@ int layers_cross_entropy(const void *x, int64_t ldx, const void *w, const int64_
  * dlse makes any function of lse a part of the loss (for c lse^2: 2 c lse). dx or dw may be
  * NULL, not both. z is computed again, in pieces of the classes whose dz takes about 512 MiB
  * of the workspace; the products read dz rounded to dtype, which is what the 16-bit matrix
- * instructions take, for float16 times a power of two that keeps it in range. dx is summed
- * over the pieces in float32. An ignored row without dlse has dz 0 and dx 0; its x is read
+ * instructions take, divided by the largest |dloss + dlse| or |dloss| of a row (for float16
+ * times 2^14, which keeps it in range). dx is summed over the pieces in float32. An ignored row without dlse has dz 0 and dx 0; its x is read
  * by dw's product all the same and has to be finite.
  */
 size_t layers_cross_entropy_backward_workspace_bytes(int64_t rows, int64_t classes, int64_t width,

@@ -22,9 +22,10 @@ SOURCES = ["api.hip", "assign.hip", "update.hip", "fit.hip", "kmeanspp.hip",
 CALIB_NAME = "libkm_calib.so"
 CALIB_PATH = os.path.join(HERE, CALIB_NAME)
 CALIB_SOURCES = ["calib.hip"]
-# Marshalling of torch tensors for experts.py: a Python extension module.
+# Marshalling of torch tensors for experts.py and layers.py: Python extension modules.
 TORCH_MODULE_PATH = os.path.join(HERE, "_experts_torch.so")
 TORCH_MODULE_SOURCE = "experts_torch.cpp"
+LAYERS_MODULE_SOURCE = "layers_torch.cpp"  # _layers_torch.so, beside it
 
 # Per-source additional flags. The assignment kernel uses LLVM's iterative
 # occupancy-driven scheduler (measured, same-box A/B on the large shapes:
@@ -124,35 +125,48 @@ def torch_module_needs() -> str | None:
     return None
 
 
+def torch_modules() -> dict[str, str]:
+    """The sources of the torch modules, by the paths of the modules."""
+    layers = os.path.join(os.path.dirname(TORCH_MODULE_PATH), "_layers_torch.so")
+    return {TORCH_MODULE_PATH: TORCH_MODULE_SOURCE, layers: LAYERS_MODULE_SOURCE}
+
+
 def build_torch_module(verbose: bool = False) -> str | None:
-    """Compile the module that marshals torch tensors to the experts' entry
-    points (host code against torch's C++ headers; it links torch alone). Where
-    something that only it needs is missing, says so and returns None: the libraries
-    are built all the same, and experts.py raises when it is used."""
+    """Compile the modules that marshal torch tensors to the experts' and layers' entry
+    points (host code against torch's C++ headers; they link torch alone). Where
+    something that only they need is missing, says so and returns None: the libraries
+    are built all the same, and experts.py and layers.py raise when they are used."""
     import sysconfig
+    from concurrent.futures import ThreadPoolExecutor
 
     missing = torch_module_needs()
+    modules = torch_modules()
     if missing:
-        print(f"{os.path.basename(TORCH_MODULE_PATH)} is not built (it takes torch tensors to the "
-              f"expert operators): {missing} not found", file=sys.stderr)
-        if os.path.exists(TORCH_MODULE_PATH):
-            os.remove(TORCH_MODULE_PATH)  # of other sources, for all that is known
+        for path in modules:
+            print(f"{os.path.basename(path)} is not built (it takes torch tensors to the expert "
+                  f"operators and those around them): {missing} not found", file=sys.stderr)
+            if os.path.exists(path):
+                os.remove(path)  # of other sources, for all that is known
         return None
     from torch.utils.cpp_extension import include_paths, library_paths
 
-    out_tmp = TORCH_MODULE_PATH + ".tmp"
-    _run([cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
-          "-DUSE_ROCM=1", *(f"-isystem{p}" for p in include_paths()), "-isystem/opt/rocm/include",
-          f"-isystem{sysconfig.get_paths()['include']}", os.path.join(CSRC, TORCH_MODULE_SOURCE),
-          *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-          "-lc10_hip", "-o", out_tmp], verbose=verbose)
-    os.replace(out_tmp, TORCH_MODULE_PATH)
+    def one(path):
+        out_tmp = path + ".tmp"
+        _run([cxx(), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-D__HIP_PLATFORM_AMD__=1",
+              "-DUSE_ROCM=1", *(f"-isystem{p}" for p in include_paths()), "-isystem/opt/rocm/include",
+              f"-isystem{sysconfig.get_paths()['include']}", os.path.join(CSRC, modules[path]),
+              *(f"-L{p}" for p in library_paths()), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+              "-lc10_hip", "-o", out_tmp], verbose=verbose)
+        os.replace(out_tmp, path)
+
+    with ThreadPoolExecutor(max_workers=len(modules)) as pool:
+        list(pool.map(one, modules))
     return TORCH_MODULE_PATH
 
 
 def build(verbose: bool = False, save_temps: bool = False) -> str:
     """Compile the k-means library, the calibration library and the torch
-    module; returns the path of the k-means library."""
+    modules; returns the path of the k-means library."""
     from concurrent.futures import ThreadPoolExecutor
 
     with ThreadPoolExecutor(max_workers=1) as pool:

@@ -230,7 +230,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void entropy_dx_kernel(EntropyGrad e
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     const bool split = e.dx_cut.splits > 1, add = !split && !e.first, write = !split && e.last;
     float *to = split ? e.partial + (int64_t)part * rows * cols : e.sum;
-    const float alpha = e.scale ? 1.0f / *e.scale : 1.0f;
+    const float alpha = e.scale ? e.scale[1] : 1.0f;
     struct Aux {
         float v[8];
     };
@@ -298,7 +298,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void entropy_dw_kernel(EntropyGrad e
     const int wn = n0 + (wave % S::WN) * (S::BN / S::WN);
     const bool split = e.dw_cut.splits > 1;
     float *to = e.partial + (int64_t)part * mc * nc;
-    const float alpha = e.scale ? 1.0f / *e.scale : 1.0f;
+    const float alpha = e.scale ? e.scale[1] : 1.0f;
     struct None {};
     by_rows<S, None>(
         (lds_char *)memory, wave, lane, acc, [](int, int) { return None{}; },

@@ -82,7 +82,7 @@ struct EntropyProblem {
     float *loss, *lse;        // outputs; lse is read by the gradient
     // The gradient.
     const float *dloss, *dlse;
-    const float *scale;       // of dz (NULL: 1), a power of two
+    const float *scale;       // dz's factor and its inverse (NULL: 1)
     int64_t first, count;     // classes of this piece
     void *dz;                 // rows x lddz
     int64_t lddz;
@@ -91,8 +91,8 @@ Cut entropy_plan(int dtype, int64_t rows, int64_t classes, int64_t width);
 int entropy_columns(int dtype, const Cut &cut);  // of a tile
 hipError_t launch_entropy(int dtype, const EntropyProblem &pr, hipStream_t s);
 hipError_t launch_entropy_dz(int dtype, const EntropyProblem &pr, hipStream_t s);
-// The power of two that brings dz into float16's range.
-hipError_t launch_entropy_scale(const EntropyProblem &pr, float *scale, hipStream_t s);
+// The factor of a 16-bit dz and its inverse.
+hipError_t launch_entropy_scale(int dtype, const EntropyProblem &pr, float *scale, hipStream_t s);
 
 // dx (first and last piece, sums between them) and dw of a piece.
 struct EntropyGrad {

@@ -137,7 +137,7 @@ EntropyLayout entropy_layout(int64_t rows, int64_t classes, int64_t width, int d
             partial = b > partial ? b : partial;
         }
         L.partial = s.add(partial);
-        if (dtype == EXPERTS_F16) L.scale = s.add(4);
+        if (dtype != EXPERTS_F32) L.scale = s.add(8);
     }
     L.total = s.with_slack();
     return L;
@@ -456,9 +456,9 @@ int layers_cross_entropy_backward(const float *dloss, const float *dlse, const v
     pr.dloss = dloss;
     pr.dlse = dlse;
     pr.dz = base + L.dz;
-    if (dtype == EXPERTS_F16) {
+    if (dtype != EXPERTS_F32 && rows > 0) {
         float *scale = (float *)(base + L.scale);
-        if (kx::launch_entropy_scale(pr, scale, s) != hipSuccess) return KM_ERR_HIP;
+        if (kx::launch_entropy_scale(dtype, pr, scale, s) != hipSuccess) return KM_ERR_HIP;
         pr.scale = scale;
     }
     kx::EntropyGrad g = {};

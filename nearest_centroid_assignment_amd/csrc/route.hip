@@ -7,15 +7,20 @@
 //   weights = scale s / (sum of the chosen s), or scale s.
 //
 // Bound by memory at best (z read once, dz written once), in fact by the vector units: the
-// choice is a partial sort. L lanes (16 or 64) hold a token's choices, V each, as doubles
-// whose bits are 1.mantissa = (the float's bits in an order that integers have, then the
-// complement of the expert's number): every key is different, a tie goes to the lower
-// number, and one v_max_f64 and one v_min_f64 exchange two. Each lane sorts its V keys
-// with a network; then, `top` times, the largest head of the lanes is taken out.
-//
-// A choice between sums of float32 roundings can differ from the formula's where two
-// choices lie within those roundings. Where any two that follow each other, or two groups
-// at the border, come that near, the token's wave chooses again in float64.
+// choice is a partial sort. L lanes (16 or 64) hold a token's choices, V each, as keys in
+// which a tie goes to the lower number. Each lane sorts its V keys with a network of
+// maxima and minima; then, `top` times, the largest head of the lanes is taken out. Keys:
+//   kWide    float32 logits: a double 1.mantissa of the float's 32 bits, put in an order that
+//            integers have, and the complement of the expert's number.
+//   kNarrow  16-bit logits leave 13 bits of a float32 empty, which hold that complement.
+//   kScored  c is a float32 sum of roundings: 27 bits of it as an integer, of the largest |c|,
+//            and 4 for the place in the lane (26 and 5 with 32 keys). Where two choices that
+//            follow each other, or two groups at the border, lie within the roundings of each
+//            other, float64 tells: for choices each lane computes its own again and the lanes
+//            sort them (of 65536 tokens, 8 of 256 experts: 0.6 % of the waves), for groups
+//            the token's wave chooses again.
+// 65536 tokens, 8 of 256 from 4 of 8 groups, sigmoids and a bias, bf16: with wide keys for
+// everything 58 us and 1550 vector instructions a wave of four tokens, so 38 and 1000.
 #include "layers.h"
 #include "rows.h"
 
@@ -27,26 +32,76 @@ constexpr int kNumber = 20;  // bits of a key for the expert's number
 
 __device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// Larger for larger floats; -0 as 0. 0 is no float's that is not a NaN.
-__device__ __forceinline__ uint32_t ordered(float f) {
-    const uint32_t b = __float_as_uint(f + 0.0f);
-    return b & 0x80000000u ? ~b : b | 0x80000000u;
+enum { kWide, kNarrow, kScored };
+
+// float's bits in the order that integers have.
+__device__ __forceinline__ int ordered(float f) {
+    const int b = __float_as_int(f);
+    return b ^ ((b >> 31) & 0x7fffffff);
 }
-__device__ __forceinline__ double key_of(float choice, int expert) {
-    const uint64_t m = ((uint64_t)ordered(choice) << kNumber) | (((1u << kNumber) - 1) - (uint32_t)expert);
-    return __longlong_as_double((long long)(m | 0x3ff0000000000000ull));
+constexpr int kNone = (int)0x807fffff;  // ordered(-inf) with any low bits is at most this
+
+// (Without the canonicalising of fmax: a key is never a NaN.)
+__device__ __forceinline__ double key_max(double a, double b) {
+    double r;
+    asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
-__device__ __forceinline__ int number_of(double key) {
-    return (int)(((1u << kNumber) - 1) - ((uint32_t)__double_as_longlong(key) & ((1u << kNumber) - 1)));
+__device__ __forceinline__ double key_min(double a, double b) {
+    double r;
+    asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
-__device__ __forceinline__ float choice_of(double key) {
-    const uint32_t o = (uint32_t)((uint64_t)__double_as_longlong(key) >> kNumber);
-    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
-}
+__device__ __forceinline__ int key_max(int a, int b) { return a > b ? a : b; }
+__device__ __forceinline__ int key_min(int a, int b) { return a < b ? a : b; }
+
+template <int K, int V>
+struct Key {  // kNarrow
+    typedef int type;
+    static constexpr int kMask = (1 << 13) - 1;
+    static constexpr int kEmpty = INT32_MIN;
+    static __device__ __forceinline__ int of(float c, int expert, int) {
+        return (ordered(c) & ~kMask) | (kMask - expert);
+    }
+    static __device__ __forceinline__ bool live(int k) { return k > kNone; }
+    static __device__ __forceinline__ int number(int k) { return kMask - (k & kMask); }
+};
+template <int V>
+struct Key<kScored, V> {
+    typedef int type;
+    static constexpr int kBits = V <= 16 ? 4 : 5;
+    static constexpr int kMask = (1 << kBits) - 1;
+    static constexpr int kEmpty = INT32_MIN;
+    // c times the power of two that leaves it below 2^(30 - kBits) in magnitude, or -inf.
+    static __device__ __forceinline__ int of(float c, int, int place) {
+        return (int)((uint32_t)(int)fmaxf(c, -(float)(1 << (31 - kBits))) << kBits) | place;
+    }
+    static __device__ __forceinline__ bool live(int k) { return k >= -(1 << 30); }
+    static __device__ __forceinline__ int place(int k) { return k & kMask; }
+    static __device__ __forceinline__ int choice(int k) { return k >> kBits; }
+};
+template <int V>
+struct Key<kWide, V> {
+    typedef double type;
+    static constexpr double kEmpty = 0.0;
+    static __device__ __forceinline__ double of(float c, int expert, int) {
+        const uint32_t o = (uint32_t)ordered(c) ^ 0x80000000u;
+        const uint32_t hi = __builtin_amdgcn_alignbit(0x3ffu, o, 12);  // 0x3ff00000 | o >> 12
+        const uint32_t lo = o << kNumber | (((1u << kNumber) - 1) - (uint32_t)expert);
+        return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+    }
+    static __device__ __forceinline__ bool live(double k) {
+        const uint64_t m = (uint64_t)(((uint32_t)kNone ^ 0x80000000u) + 1) << kNumber;
+        return k >= __longlong_as_double((long long)(m | 0x3ff0000000000000ull));
+    }
+    static __device__ __forceinline__ int number(double k) {
+        return (int)(((1u << kNumber) - 1) - ((uint32_t)__double_as_longlong(k) & ((1u << kNumber) - 1)));
+    }
+};
 
 // Batcher's odd-even merge sort of V keys, largest first.
-template <int V>
-__device__ __forceinline__ void sort_keys(double (&k)[V]) {
+template <int V, typename K>
+__device__ __forceinline__ void sort_keys(K (&k)[V]) {
 #pragma unroll
     for (int p = 1; p < V; p *= 2)
 #pragma unroll
@@ -57,7 +112,7 @@ __device__ __forceinline__ void sort_keys(double (&k)[V]) {
                 for (int i = 0; i < q; ++i) {
                     const int a = i + j, b = a + q;
                     if (b < V && a / (2 * p) == b / (2 * p)) {
-                        const double hi = fmax(k[a], k[b]), lo = fmin(k[a], k[b]);
+                        const K hi = key_max(k[a], k[b]), lo = key_min(k[a], k[b]);
                         k[a] = hi;
                         k[b] = lo;
                     }
@@ -67,32 +122,58 @@ __device__ __forceinline__ void sort_keys(double (&k)[V]) {
 template <int CTRL>
 __device__ __forceinline__ double rotated(double x) {  // within 16 lanes
     const uint64_t b = (uint64_t)__double_as_longlong(x);
-    const int lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xf, 0xf, false);
-    const int hi = __builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, 0xf, 0xf, false);
+    const int lo = __builtin_amdgcn_mov_dpp((int)(uint32_t)b, CTRL, 0xf, 0xf, true);
+    const int hi = __builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xf, 0xf, true);
     return __longlong_as_double((long long)(((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo));
 }
-template <int L>
-__device__ __forceinline__ double lanes_max(double x) {
-    x = fmax(x, rotated<0x128>(x));  // row_ror:8, 4, 2, 1
-    x = fmax(x, rotated<0x124>(x));
-    x = fmax(x, rotated<0x122>(x));
-    x = fmax(x, rotated<0x121>(x));
+template <int CTRL>
+__device__ __forceinline__ int rotated(int x) {
+    return __builtin_amdgcn_mov_dpp(x, CTRL, 0xf, 0xf, true);
+}
+template <int L, typename K>
+__device__ __forceinline__ K lanes_most(K x) {  // of keys
+    x = key_max(x, rotated<0x128>(x));  // row_ror:8, 4, 2, 1
+    x = key_max(x, rotated<0x124>(x));
+    x = key_max(x, rotated<0x122>(x));
+    x = key_max(x, rotated<0x121>(x));
     if (L == 64) {
-        x = fmax(x, __shfl_xor(x, 16));
-        x = fmax(x, __shfl_xor(x, 32));
+        x = key_max(x, __shfl_xor(x, 16));
+        x = key_max(x, __shfl_xor(x, 32));
     }
     return x;
 }
 template <int L>
-__device__ __forceinline__ float lanes_max(float x) {
+__device__ __forceinline__ double lanes_max(double x) {
 #pragma unroll
-    for (int d = L / 2; d >= 1; d >>= 1) x = fmaxf(x, __shfl_xor(x, d));
+    for (int d = L / 2; d >= 1; d >>= 1) x = fmax(x, __shfl_xor(x, d));
+    return x;
+}
+template <int CTRL>
+__device__ __forceinline__ float rotated(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float x) {
+    x = fmaxf(x, rotated<0x128>(x));
+    x = fmaxf(x, rotated<0x124>(x));
+    x = fmaxf(x, rotated<0x122>(x));
+    x = fmaxf(x, rotated<0x121>(x));
+    if (L == 64) {
+        x = fmaxf(x, __shfl_xor(x, 16));
+        x = fmaxf(x, __shfl_xor(x, 32));
+    }
     return x;
 }
 template <int L>
-__device__ __forceinline__ float lanes_sum(float x) {
-#pragma unroll
-    for (int d = L / 2; d >= 1; d >>= 1) x += __shfl_xor(x, d);
+__device__ __forceinline__ float lanes_sum(float x) {  // to all lanes, of one order
+    x += rotated<0x128>(x);
+    x += rotated<0x124>(x);
+    x += rotated<0x122>(x);
+    x += rotated<0x121>(x);
+    if (L == 64) {
+        x += __shfl_xor(x, 16);
+        x += __shfl_xor(x, 32);
+    }
     return x;
 }
 template <int L>
@@ -102,9 +183,38 @@ __device__ __forceinline__ double lanes_sum(double x) {
     return x;
 }
 
+// (v_max and v_min: a NaN gives way to the other operand.)
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+
+// first >= second, with one more value.
+template <typename F>
+__device__ __forceinline__ void two_largest(F c, F &first, F &second) {
+    second = larger(second, smaller(first, c));
+    first = larger(first, c);
+}
+
+// x of the lane i places before, within the L lanes.
+template <int L, typename F>
+__device__ __forceinline__ F turned(F x, int i) {
+    const int lane = threadIdx.x & 63;
+    return __shfl(x, (lane & ~(L - 1)) | ((lane - i) & (L - 1)));
+}
+
+// Of every STEP-th of the 16 lanes, those before this one in the order of the keys.
+template <int STEP, int I = STEP>
+__device__ __forceinline__ int count_before(double key) {
+    if constexpr (I < 16)
+        return (int)(rotated<0x120 + I>(key) > key) + count_before<STEP, I + STEP>(key);
+    else
+        return 0;
+}
+
 // Of the lane's group: the sum of its one or two largest choices, and whether it is
 // among the `kept` best (ties to the lower group). `first` and `second`: the lane's two
-// largest (-inf: none). `least`: the least distance of a rank to one on the other side.
+// largest (-inf: none). `least`: how far the groups that stay lie from the others.
 template <int L, typename F>
 __device__ __forceinline__ bool group_kept(F first, F second, int groups, int kept, int best,
                                            int lanes, int group, F &least) {
@@ -116,28 +226,30 @@ __device__ __forceinline__ bool group_kept(F first, F second, int groups, int ke
         from -= from >= start + lanes ? lanes : 0;
         const int at = base + (from & (L - 1));
         const F c = __shfl(first, at), d = __shfl(second, at);
-        if (c > a) {
-            b = a > d ? a : d;
-            a = c;
-        } else {
-            b = b > c ? b : c;
-        }
+        two_largest(c, a, b);
+        b = larger(b, d);
     }
     const F none = -(F)INFINITY;
     const F rank = best == 2 && b > none ? a + b : a;
     int before = 0;
-    for (int g = 0; g < groups; ++g) {
-        const F other = __shfl(rank, base + g * lanes);
-        before += other > rank || (other == rank && g < group);
+    if constexpr (L == 16 && sizeof(F) == 4) {
+        // (A group's lanes hold the same key.)
+        const double key = Key<kWide, 1>::of(rank + 0.0f, group, 0);
+        if (lanes == 2)
+            before = 2 * count_before<2>(key);
+        else if (lanes == 4)
+            before = 4 * count_before<4>(key);
+        else
+            before = count_before<1>(key);
+    } else {
+        for (int i = 1; i < L; ++i) {
+            const F other = turned<L>(rank, i);
+            before += (int)(other > rank) | ((int)(other == rank) & (int)(((own - i) & (L - 1)) < start));
+        }
     }
-    const bool keep = group < groups && before < kept;
-    least = (F)INFINITY;
-    for (int g = 0; g < groups; ++g) {
-        const F other = __shfl(rank, base + g * lanes);
-        const bool there = __shfl((int)keep, base + g * lanes);
-        const F d = other > rank ? other - rank : rank - other;
-        if (group < groups && there != keep && d < least) least = d;
-    }
+    const bool keep = group < groups && before < kept * lanes;
+    const F worst = lanes_max<L>(keep ? -rank : none), other = lanes_max<L>(keep || group >= groups ? none : rank);
+    least = -worst - other;
     return keep;
 }
 
@@ -159,27 +271,24 @@ __device__ __forceinline__ Layout layout_of(int experts, int groups) {
 }
 
 template <typename T, int V>
-__device__ __forceinline__ void load_scores(const T *p, const Layout &l, float (&z)[V]) {
-    T v[V];
+__device__ __forceinline__ void load_own(const T *p, const Layout &l, T none, T (&v)[V]) {
     if (l.n == V) {
         load_vec(p + l.first, v);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) v[j] = j < l.n ? p[l.first + j] : (T)(-INFINITY);
+        for (int j = 0; j < V; ++j) v[j] = j < l.n ? p[l.first + j] : none;
     }
-#pragma unroll
-    for (int j = 0; j < V; ++j) z[j] = (float)v[j];
 }
-
-// The same choice in float64 (see the top): the t-th expert in lane t.
+// The same choice in float64 (see the top): the t-th expert in lane t. (As a function of
+// its own, or with rolled loops, it took 101 to 130 registers, which are every wave's, in
+// place of 90, and the size above 49 to 55 us in place of 46, before the lanes sorted.)
 template <int L, int V>
 __device__ __forceinline__ int choose_exactly(const float (&z)[V], const RouteProblem &pr, const Layout &l) {
     double c[V];
     double m = -INFINITY, sum = 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j) m = z[j] > m ? (double)z[j] : m;
-#pragma unroll
-    for (int d = L / 2; d >= 1; d >>= 1) m = fmax(m, __shfl_xor(m, d));
+    m = lanes_max<L>(m);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const bool live = z[j] > -INFINITY;
@@ -193,12 +302,7 @@ __device__ __forceinline__ int choose_exactly(const float (&z)[V], const RoutePr
         if (!pr.sigmoid) c[j] /= sum;
         if (pr.bias && j < l.n) c[j] += (double)pr.bias[l.first + j];
         if (!(z[j] > -INFINITY) || !(c[j] > -INFINITY)) c[j] = -INFINITY;
-        if (c[j] > first) {
-            second = first;
-            first = c[j];
-        } else if (c[j] > second) {
-            second = c[j];
-        }
+        two_largest(c[j], first, second);
     }
     bool keep = true;
     if (pr.groups > 1) {
@@ -232,20 +336,78 @@ __device__ __forceinline__ int choose_exactly(const float (&z)[V], const RoutePr
     return mine;
 }
 
-template <typename T, int L, int V>
-__global__ __launch_bounds__(256) void route_kernel(RouteProblem pr) {
+// The lane's candidate (`mine`, the t-th in lane t, -1: none) by its choice in float64: the
+// lanes up to `last` in order, ties to the lower number.
+template <int L, int V>
+__device__ __forceinline__ int resolve(const float (&z)[V], const RouteProblem &pr, float score, int mine,
+                                       int last) {
     const int own = threadIdx.x & (L - 1);
-    int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
-    const bool there = t < pr.tokens;
-    if (!there) t = pr.tokens - 1;  // its lanes go along, and store nothing
-    const Layout l = layout_of<L, V>(pr.experts, pr.groups);
-    const T *row = (const T *)pr.logits + t * pr.ld;
-    float z[V], c[V];
-    load_scores<T, V>(row, l, z);
-    const bool scored = pr.bias || (pr.groups > 1 && pr.best == 2);
+    double c = -INFINITY;
+    if (pr.sigmoid) {
+        c = 1.0 / (1.0 + exp(-(double)score));
+    } else {
+        double m = -INFINITY, sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) m = z[j] > m ? (double)z[j] : m;
+        m = lanes_max<L>(m);
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum += z[j] > -INFINITY ? exp((double)z[j] - m) : 0.0;
+        c = exp((double)score - m) / lanes_sum<L>(sum);
+    }
+    if (pr.bias && mine >= 0) c += (double)pr.bias[mine];
+    if (mine < 0) c = -INFINITY;
+    for (int pass = 0; pass <= last; ++pass) {  // odd-even transposition
+        const int with = ((own ^ pass) & 1) ? own - 1 : own + 1;
+        const int at = (threadIdx.x & 63 & ~(L - 1)) + (with & (L - 1));
+        const double other = __shfl(c, at);
+        const int number = __shfl(mine, at);
+        const bool before = other > c || (other == c && (uint32_t)number < (uint32_t)mine);
+        if (with >= 0 && with <= last && own <= last && (with > own) == before) {
+            c = other;
+            mine = number;
+        }
+    }
+    return mine;
+}
+
+// The `top` largest keys of the lanes that `keep` theirs, one after another: the t-th in lane t, and in kScored the lane that
+// had it. `twice`: whether two lanes had the same one. D keys of a lane can come up.
+template <int L, int K, int D, typename Keys>
+__device__ __forceinline__ void take(Keys &key, bool keep, int top, typename Keys::type &won, int &from,
+                                     bool &twice) {
+    const int own = threadIdx.x & (L - 1);
+    sort_keys(key.k);
+    key.k[0] = keep ? key.k[0] : Keys::kEmpty;
+    for (int i = 0; i < top; ++i) {
+        const auto best = lanes_most<L>(key.k[0]);
+        const bool had = keep & (key.k[0] == best);
+        if constexpr (K == kScored) {
+            const uint64_t all = __ballot(had);
+            const uint64_t lanes = L == 64 ? all : (all >> (threadIdx.x & 48)) & 0xffff;
+            twice |= (lanes & (lanes - 1)) != 0 && key.live(best);
+            from = own == i ? __ffsll((unsigned long long)lanes) - 1 : from;
+        }
+#pragma unroll
+        for (int j = 0; j + 1 < D; ++j) key.k[j] = had ? key.k[j + 1] : key.k[j];
+        if (D == Keys::kCount) key.k[D - 1] = had ? Keys::kEmpty : key.k[D - 1];
+        won = own == i ? best : won;
+    }
+}
+template <int K, int V>
+struct Keys : Key<K, V> {
+    static constexpr int kCount = V;
+    typename Key<K, V>::type k[V];
+};
+
+// The choice for the token of the L lanes, and its weights.
+template <typename T, int L, int V, int K, int B>
+__device__ __forceinline__ void route_token(const RouteProblem &pr, const Layout &l, const float (&bias)[B],
+                                            const float (&z)[V], bool there, const T *row, int64_t t) {
+    const int own = threadIdx.x & (L - 1);
+    float c[V];
     // The largest and the sum of e^(z - largest) where they are needed.
     float top = -INFINITY, total = 1.0f;
-    if (scored || (!pr.sigmoid && !pr.renormalize)) {
+    if (K == kScored || (!pr.sigmoid && !pr.renormalize)) {
 #pragma unroll
         for (int j = 0; j < V; ++j) top = fmaxf(top, z[j]);
         top = lanes_max<L>(top);
@@ -262,60 +424,88 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem pr) {
     }
     float far = 0.0f;   // what two choices may be off by together
     float most = 0.0f;  // the largest |c|
-    if (scored) {
+    if (K == kScored) {
+        const float each = 1.0f / total;
+        if (pr.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[j] = sigmoid(z[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[j] *= each;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) c[j] += bias[j];
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            c[j] = pr.sigmoid ? sigmoid(z[j]) : c[j] / total;
-            if (pr.bias && j < l.n) c[j] += pr.bias[l.first + j];
-            if (!(z[j] > -INFINITY) || !(c[j] > -INFINITY)) c[j] = -INFINITY;
-            if (c[j] > -INFINITY) most = fmaxf(most, fabsf(c[j]));
+            most = fmaxf(most, fabsf(c[j]));
+            c[j] = ((z[j] > -INFINITY) & (c[j] == c[j])) ? c[j] : -INFINITY;  // not a NaN
         }
         most = lanes_max<L>(most);
+        if (most == INFINITY) {  // a bias that takes experts out: of the others
+            most = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j) most = fmaxf(most, fabsf(c[j]) < INFINITY ? fabsf(c[j]) : 0.0f);
+            most = lanes_max<L>(most);
+        }
         // The scores' own errors (the argument's rounding times s'(z) |z|, the hardware's
         // 2^x and reciprocal; the softmax's sum), and that of adding the bias.
-        const float s = pr.sigmoid ? sigmoid(top) : 1.0f / total;
+        const float s = pr.sigmoid ? sigmoid(top) : each;
         const float slope = pr.sigmoid ? (top > -1.0f ? 0.25f : s * -top) : 0.0f;
         far = 2.0f * ((pr.sigmoid ? 0x1p-21f : 0x1p-18f) * s + 0x1p-23f * slope + 0x1p-24f * most);
     } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) c[j] = z[j];
+        for (int j = 0; j < V; ++j) c[j] = z[j] == z[j] ? z[j] + 0.0f : -INFINITY;  // not a NaN, nor -0
     }
     bool again = false;
     bool keep = true;
     if (pr.groups > 1) {
         float first = -INFINITY, second = -INFINITY, least;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            if (c[j] > first) {
-                second = first;
-                first = c[j];
-            } else if (c[j] > second) {
-                second = c[j];
-            }
-        }
+        for (int j = 0; j < V; ++j) two_largest(c[j], first, second);
         keep = group_kept<L, float>(first, second, pr.groups, pr.kept, pr.best, l.lanes, l.group, least);
-        again = scored && least <= 2.0f * far + 0x1p-22f * most;
+        again = K == kScored && least <= 2.0f * far + 0x1p-22f * most;
     }
-    double key[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) key[j] = keep && c[j] > -INFINITY ? key_of(c[j], l.first + j) : 0.0;
-    sort_keys<V>(key);
-    int mine = -1;  // the t-th chosen, in lane t
-    double before = 0.0;
-    for (int i = 0; i < pr.top + (scored ? 1 : 0); ++i) {
-        const double best = lanes_max<L>(key[0]);
-        if (key[0] == best) {
-#pragma unroll
-            for (int j = 0; j + 1 < V; ++j) key[j] = key[j + 1];
-            key[V - 1] = 0.0;
-        }
-        if (own == i && i < pr.top && best != 0.0) mine = number_of(best);
-        if (scored) {
-            if (i > 0 && best != 0.0) again |= choice_of(before) - choice_of(best) <= far;
-            before = best;
-        }
+    float unit = 1.0f;  // the power of two that makes integers of c
+    if constexpr (K == kScored) {
+        const int e = __builtin_amdgcn_frexp_expf(most);
+        const int up = 30 - Key<K, V>::kBits - e;
+        unit = ldexpf(1.0f, up < 120 ? up : 120);
     }
-    if (scored && __any(again)) mine = choose_exactly<L, V>(z, pr, l);
+    Keys<K, V> key;
+#pragma unroll
+    for (int j = 0; j < V; ++j) key.k[j] = key.of(K == kScored ? c[j] * unit : c[j], l.first + j, j);
+    typename Key<K, V>::type best = Keys<K, V>::kEmpty;
+    int from = 0;
+    // One more than is returned, where choices may have to be told apart. Of a lane's keys
+    // only as many can come up as are asked for, and the one after them.
+    const int asked = K == kScored && pr.top < L ? pr.top + 1 : pr.top;
+    if (V > 10 && asked <= 9)
+        take<L, K, V < 10 ? V : 10>(key, keep, asked, best, from, again);
+    else
+        take<L, K, V>(key, keep, asked, best, from, again);
+    int mine = -1;
+    if constexpr (K == kScored) {
+        const int first = __shfl(l.first, (threadIdx.x & 63 & ~(L - 1)) + from);
+        if (own < asked && key.live(best)) mine = first + key.place(best);
+        // Does any of them come near the one after it? (In units of the keys' choices, to
+        // which each is cut off.)
+        const int next = lanes_most<L>(keep ? key.k[0] : key.kEmpty);
+        int after = __shfl_down((int)best, 1, L);
+        after = own == asked - 1 ? next : after;
+        const bool near = mine >= 0 && key.live(after) &&
+                          (float)(key.choice(best) - key.choice(after)) <= far * unit + 2.0f;
+        const int last = asked - 1;
+        // The last asked for is not returned, unless there was no lane for one more.
+        const bool past = near && own == last;
+        const bool border = asked == pr.top ? past : __shfl((int)near, (threadIdx.x & 63 & ~(L - 1)) + last - 1) && past;
+        if (__any(again || border))
+            mine = choose_exactly<L, V>(z, pr, l);
+        else if (__any(near && own < last))
+            mine = resolve<L, V>(z, pr, mine >= 0 ? (float)row[mine] : -INFINITY, mine, last);
+        if (own >= pr.top) mine = -1;
+    } else if (own < pr.top && key.live(best)) {
+        mine = key.number(best);
+    }
 
     const bool chosen = mine >= 0;
     const float score = chosen ? (float)row[mine] : -INFINITY;
@@ -337,6 +527,27 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem pr) {
         pr.ids[t * pr.top + own] = mine;
         pr.weights[t * pr.top + own] = w;
     }
+}
+
+template <typename T, int L, int V, int K>
+__global__ __launch_bounds__(256) void route_kernel(RouteProblem pr) {
+    const Layout l = layout_of<L, V>(pr.experts, pr.groups);
+    float bias[K == kScored ? V : 1];
+    if constexpr (K == kScored) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) bias[j] = 0.0f;
+        if (pr.bias) load_own<float, V>(pr.bias, l, 0.0f, bias);
+    }
+    int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const bool there = t < pr.tokens;
+    if (!there) t = pr.tokens - 1;  // its lanes go along, and store nothing
+    const T *row = (const T *)pr.logits + t * pr.ld;
+    T raw[V];
+    load_own<T, V>(row, l, (T)(-INFINITY), raw);
+    float z[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) z[j] = (float)raw[j];
+    route_token<T, L, V, K>(pr, l, bias, z, there, row, t);
 }
 
 // With r the chosen's shares (their sum 1) and d = scale dweights:
@@ -422,18 +633,23 @@ Form form_of(int64_t experts, int64_t groups, int64_t top) {
     return {64, each <= 8 ? 8 : each <= 16 ? 16 : each <= 32 ? 32 : 0};
 }
 
-template <typename T>
-hipError_t route_t(const RouteProblem &pr, hipStream_t s) {
+template <typename T, int K>
+hipError_t route_k(const RouteProblem &pr, hipStream_t s) {
     const Form f = form_of(pr.experts, pr.groups, pr.top);
     const int64_t blocks = cdiv(pr.tokens, 256 / f.lanes);
     if (f.lanes == 16) {
-        if (f.each == 4) return launch(route_kernel<T, 16, 4>, blocks, 256, 0, s, pr);
-        if (f.each == 8) return launch(route_kernel<T, 16, 8>, blocks, 256, 0, s, pr);
-        return launch(route_kernel<T, 16, 16>, blocks, 256, 0, s, pr);
+        if (f.each == 4) return launch(route_kernel<T, 16, 4, K>, blocks, 256, 0, s, pr);
+        if (f.each == 8) return launch(route_kernel<T, 16, 8, K>, blocks, 256, 0, s, pr);
+        return launch(route_kernel<T, 16, 16, K>, blocks, 256, 0, s, pr);
     }
-    if (f.each == 8) return launch(route_kernel<T, 64, 8>, blocks, 256, 0, s, pr);
-    if (f.each == 16) return launch(route_kernel<T, 64, 16>, blocks, 256, 0, s, pr);
-    return launch(route_kernel<T, 64, 32>, blocks, 256, 0, s, pr);
+    if (f.each == 8) return launch(route_kernel<T, 64, 8, K>, blocks, 256, 0, s, pr);
+    if (f.each == 16) return launch(route_kernel<T, 64, 16, K>, blocks, 256, 0, s, pr);
+    return launch(route_kernel<T, 64, 32, K>, blocks, 256, 0, s, pr);
+}
+template <typename T>
+hipError_t route_t(const RouteProblem &pr, hipStream_t s) {
+    if (pr.bias || (pr.groups > 1 && pr.best == 2)) return route_k<T, kScored>(pr, s);
+    return route_k<T, sizeof(T) == 4 ? kWide : kNarrow>(pr, s);
 }
 template <typename T>
 hipError_t backward_t(const RouteProblem &pr, hipStream_t s) {

@@ -43,14 +43,14 @@ _lib = None
 _native = None  # the torch module, once lib() has loaded it
 
 
-def _load_native(L, names):
-    """The module that takes the ordinary calls natively (csrc/experts_torch.cpp),
-    bound to the library's entry points."""
-    path = os.path.join(HERE, "_experts_torch.so")
+def _load_native(L, names, name="_experts_torch"):
+    """The module that takes the ordinary calls natively (csrc/experts_torch.cpp,
+    csrc/layers_torch.cpp), bound to the library's entry points."""
+    path = os.path.join(HERE, f"{name}.so")
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with "
                            "`python -m nearest_centroid_assignment_amd.build`")
-    spec = importlib.util.spec_from_file_location("_experts_torch", path)
+    spec = importlib.util.spec_from_file_location(name, path)
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _check)

@@ -19,13 +19,12 @@ calls, and a forward call with an input that requires grad warns of it.
 from __future__ import annotations
 
 import ctypes
-import warnings
 
 import torch
 
 from .binding import KMeansError, _check
-from .experts import (_dense, _first, _given, _mark, _new, _on_device, _queue, _rows, _scratch,
-                      lib as _experts_lib)
+from .experts import (_dense, _first, _given, _load_native, _mark, _new, _on_device, _queue, _rows,
+                      _scratch, lib as _experts_lib)
 
 SCORES = {"softmax": 0, "sigmoid": 1}
 
@@ -33,13 +32,15 @@ __all__ = ["KMeansError", "embed", "embed_backward", "layer_norm", "layer_norm_b
            "route_backward", "cross_entropy", "cross_entropy_backward"]
 
 _lib = None
+_native = None  # the torch module (csrc/layers_torch.cpp), once lib() has loaded it
 
 
 def lib() -> ctypes.CDLL:
     """The HIP library with the layers' entry points declared."""
-    global _lib
+    global _lib, _native
     if _lib is None:
         L = _experts_lib()
+        names = []
         i64, vp, sz, i32, f64 = (ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int,
                                  ctypes.c_double)
         for name, res, args in (
@@ -64,16 +65,20 @@ def lib() -> ctypes.CDLL:
         ):
             f = getattr(L, name)
             f.restype, f.argtypes = res, args
+            names.append(name)
+        _native = _load_native(L, names, "_layers_torch")
         _lib = L
     return _lib
 
 
-def _unrecorded(name, *inputs):
-    """Warn where a graph is being recorded and one of these asks to be in it."""
-    if torch.is_grad_enabled() and any(isinstance(t, torch.Tensor) and t.requires_grad for t in inputs):
-        warnings.warn(f"layers.{name} is not recorded for autograd: an input requires grad, but gradients "
-                      f"are explicit calls (layers.{name}_backward). Call it under torch.no_grad(), or with "
-                      "detached tensors", UserWarning, stacklevel=3)
+def _module():
+    lib()
+    return _native
+
+
+# As in ``experts``, a call with fresh outputs on the current stream is first offered to the
+# native module, which takes it or, where anything about it is unusual, leaves it to the
+# Python below.
 
 
 def _numbers(t, name, count, dev=None):
@@ -118,7 +123,11 @@ def _misplaced(px, ldx, pw, width):
 def embed(ids, w, scale=1.0, out=None, stream=None):
     """scale * w[ids] for int64 numbers ids (tokens,) and a table w (classes, width):
     (tokens, width). Numbers outside [0, classes) give zero rows."""
-    _unrecorded("embed", w)
+    if out is None and stream is None:
+        got = (_native or _module()).embed(ids, w, scale)
+        if got is not None:
+            return got
+    _module().unrecorded("embed", w)
     return _embed(ids, w, scale, out, stream)
 
 
@@ -146,6 +155,10 @@ def _embed(ids, w, scale, out, stream):
 def embed_backward(dy, ids, classes, scale=1.0, workspace=None, stream=None):
     """Gradient of embed's table (classes, width), in dy's type: scale times the sum of each
     number's rows of dy (tokens, width)."""
+    if workspace is None and stream is None:
+        got = (_native or _module()).embed_backward(dy, ids, classes, scale)
+        if got is not None:
+            return got
     return _embed_backward(dy, ids, classes, scale, workspace, stream)
 
 
@@ -186,7 +199,11 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, save_stats=False, out=None, 
     rstd = 1 / sqrt(variance + eps); weight and bias (width,), of x's type or float32.
     With ``save_stats`` returns (out, mean, rstd), the latter (rows,) float32 for
     layer_norm_backward."""
-    _unrecorded("layer_norm", x, weight, bias)
+    if out is None and stream is None:
+        got = (_native or _module()).layer_norm(x, weight, bias, eps, save_stats)
+        if got is not None:
+            return got
+    _module().unrecorded("layer_norm", x, weight, bias)
     return _layer_norm(x, weight, bias, eps, save_stats, out, stream)
 
 
@@ -217,6 +234,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, need_dx=True, need_dweight=Tr
                         workspace=None, stream=None):
     """Gradients of layer_norm: (dx, dweight, dbias), None for those not needed; dweight and
     dbias of weight's type (x's without a weight)."""
+    if workspace is None and stream is None:
+        got = (_native or _module()).layer_norm_backward(dy, x, weight, mean, rstd, need_dx, need_dweight,
+                                                         need_dbias)
+        if got is not None:
+            return got
     return _layer_norm_backward(dy, x, weight, mean, rstd, need_dx, need_dweight, need_dbias, workspace,
                                 stream)
 
@@ -264,9 +286,15 @@ def route(logits, top, score="softmax", bias=None, groups=1, top_groups=None, gr
     ``top_groups`` groups with the largest sums of their ``group_best`` (1 or 2) largest
     score + bias. Weights are the scores, divided by their sum over the chosen with
     ``renormalize``, times ``scale``. Places for which no expert is left: id -1, weight 0."""
-    _unrecorded("route", logits)
-    return _route(logits, top, score, bias, groups, groups if top_groups is None else top_groups,
-                  group_best, renormalize, scale, stream)
+    if top_groups is None:
+        top_groups = groups
+    if stream is None:
+        got = (_native or _module()).route(logits, top, SCORES.get(score, -1), bias, groups, top_groups,
+                                           group_best, renormalize, scale)
+        if got is not None:
+            return got
+    _module().unrecorded("route", logits)
+    return _route(logits, top, score, bias, groups, top_groups, group_best, renormalize, scale, stream)
 
 
 @_on_device
@@ -291,6 +319,11 @@ def route_backward(dweights, logits, ids, score="softmax", renormalize=True, sca
     """Gradient of route's weights with respect to the logits, the choice fixed:
     (tokens, experts) in the logits' type, for dweights (tokens, top) float32 and the ids
     that route gave."""
+    if stream is None:
+        got = (_native or _module()).route_backward(dweights, logits, ids, SCORES.get(score, -1), renormalize,
+                                                    scale)
+        if got is not None:
+            return got
     return _route_backward(dweights, logits, ids, score, renormalize, scale, stream)
 
 
@@ -323,7 +356,11 @@ def cross_entropy(x, w, targets, workspace=None, stream=None):
     (rows,) float32, for x (rows, width), w (classes, width) and int64 targets (rows,).
     loss = lse - logit of the target, lse the log of the sum of e^logits. A target outside
     [0, classes) is ignored: its loss is 0."""
-    _unrecorded("cross_entropy", x, w)
+    if workspace is None and stream is None:
+        got = (_native or _module()).cross_entropy(x, w, targets)
+        if got is not None:
+            return got
+    _module().unrecorded("cross_entropy", x, w)
     return _cross_entropy(x, w, targets, workspace, stream)
 
 
@@ -353,6 +390,10 @@ def cross_entropy_backward(dloss, x, w, targets, lse, dlse=None, need_dx=True, n
     (rows,) float32 (1 / count for a mean) and, where lse is part of the loss too, dlse
     (rows,) float32. lse is what cross_entropy gave. The logits are computed again, in pieces of
     the classes."""
+    if workspace is None and stream is None:
+        got = (_native or _module()).cross_entropy_backward(dloss, x, w, targets, lse, dlse, need_dx, need_dw)
+        if got is not None:
+            return got
     return _cross_entropy_backward(dloss, x, w, targets, lse, dlse, need_dx, need_dw, workspace, stream)
 
 
