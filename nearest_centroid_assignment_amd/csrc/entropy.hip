@@ -10,6 +10,8 @@ template <typename T>
 hipError_t launch_entropy_dx_t(const EntropyGrad &e, hipStream_t s);
 template <typename T>
 hipError_t launch_entropy_dw_t(const EntropyGrad &e, hipStream_t s);
+template <typename T>
+hipError_t launch_entropy_both_t(const EntropyGrad &e, hipStream_t s);
 
 namespace {
 
@@ -130,6 +132,7 @@ __global__ __launch_bounds__(256) void entropy_parts_kernel(const float *__restr
 template <typename T>
 hipError_t grad_t(const EntropyGrad &g, hipStream_t s) {
     hipError_t e = hipSuccess;
+    if (g.together) return launch_entropy_both_t<T>(g, s);
     if (g.dx) {
         e = launch_entropy_dx_t<T>(g, s);
         if (e == hipSuccess && g.dx_cut.splits > 1)
@@ -147,10 +150,17 @@ hipError_t grad_t(const EntropyGrad &g, hipStream_t s) {
 
 }  // namespace
 
-Cut entropy_plan(int dtype, int64_t rows, int64_t classes, int64_t width) {
+Cut entropy_plan(int dtype, int64_t rows, int64_t classes, int64_t width, bool grad) {
+    if (!grad && rows <= 32) {
+        const int groups = classes >= 16384 ? 4 : classes >= 8192 ? 2 : 1;  // a block a compute unit
+        return {rows <= 16 ? 16 : 32, groups, true, 0.0};
+    }
     return whole_plan(dtype, rows, classes, width);
 }
-int entropy_columns(int, const Cut &cut) { return cut.tile == 129 ? 128 : cut.tile == 32 ? 64 : cut.tile; }
+int entropy_columns(int, const Cut &cut) {
+    if (cut.thin) return 16 * cut.splits;
+    return cut.tile == 129 ? 128 : cut.tile == 32 ? 64 : cut.tile;
+}
 
 hipError_t launch_entropy(int dtype, const EntropyProblem &pr, hipStream_t s) {
     hipError_t e;
@@ -159,8 +169,7 @@ hipError_t launch_entropy(int dtype, const EntropyProblem &pr, hipStream_t s) {
     else
         e = dtype == 1 ? launch_entropy_t<bf16>(pr, false, s) : launch_entropy_t<f16>(pr, false, s);
     if (e != hipSuccess) return e;
-    Cut cut = {};
-    cut.tile = pr.tile;
+    const Cut cut = {pr.tile, pr.thin, pr.thin != 0, 0.0};
     return launch(entropy_join_kernel, cdiv(pr.rows, 16), 256, 0, s, pr,
                   (int)cdiv(pr.count, entropy_columns(dtype, cut)));
 }

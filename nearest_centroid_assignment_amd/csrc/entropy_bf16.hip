@@ -15,5 +15,9 @@ template <>
 hipError_t launch_entropy_dw_t<bf16>(const EntropyGrad &e, hipStream_t s) {
     return pick_dw<bf16>(e, s);
 }
+template <>
+hipError_t launch_entropy_both_t<bf16>(const EntropyGrad &e, hipStream_t s) {
+    return pick_entropy_both<bf16>(e, s);
+}
 
 }  // namespace kx

@@ -15,5 +15,9 @@ template <>
 hipError_t launch_entropy_dw_t<f16>(const EntropyGrad &e, hipStream_t s) {
     return pick_dw<f16>(e, s);
 }
+template <>
+hipError_t launch_entropy_both_t<f16>(const EntropyGrad &e, hipStream_t s) {
+    return pick_entropy_both<f16>(e, s);
+}
 
 }  // namespace kx

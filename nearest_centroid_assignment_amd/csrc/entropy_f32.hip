@@ -15,5 +15,9 @@ template <>
 hipError_t launch_entropy_dw_t<float>(const EntropyGrad &e, hipStream_t s) {
     return pick_dw<float>(e, s);
 }
+template <>
+hipError_t launch_entropy_both_t<float>(const EntropyGrad &e, hipStream_t s) {
+    return pick_entropy_both<float>(e, s);
+}
 
 }  // namespace kx

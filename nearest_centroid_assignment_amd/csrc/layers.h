@@ -75,7 +75,7 @@ struct EntropyProblem {
     int64_t ldx, ldw, rows, classes, width;
     int64_t x_cols, w_cols;   // readable columns (a pad is zero)
     const int64_t *targets;
-    int tile;
+    int tile, thin;           // entropy_plan's tile, and with its `thin` its splits
     // The sums of each row over one column tile, and the target's logit.
     float2 *part;             // column tiles x rows
     float *hit;               // rows
@@ -87,7 +87,9 @@ struct EntropyProblem {
     void *dz;                 // rows x lddz
     int64_t lddz;
 };
-Cut entropy_plan(int dtype, int64_t rows, int64_t classes, int64_t width);
+// With `thin` (few rows, the forward call), tile rows and 16 * splits columns a block, and any
+// rows are read in place.
+Cut entropy_plan(int dtype, int64_t rows, int64_t classes, int64_t width, bool grad);
 int entropy_columns(int dtype, const Cut &cut);  // of a tile
 hipError_t launch_entropy(int dtype, const EntropyProblem &pr, hipStream_t s);
 hipError_t launch_entropy_dz(int dtype, const EntropyProblem &pr, hipStream_t s);
@@ -106,6 +108,7 @@ struct EntropyGrad {
     bool first, last;
     void *dw;                 // NULL: not computed
     Cut dx_cut, dw_cut;
+    bool together;            // one launch, both with dx_cut's tile and neither split
     float *partial;
 };
 hipError_t launch_entropy_grad(int dtype, const EntropyGrad &g, hipStream_t s);

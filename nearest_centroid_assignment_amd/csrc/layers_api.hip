@@ -81,9 +81,12 @@ bool entropy_shape_ok(int dtype, int64_t rows, int64_t classes, int64_t width) {
     if (dtype != EXPERTS_F32 && (rows * cdiv(width, 8) + 256 > kMaxGridThreads ||
                                  classes * cdiv(width, 8) + 256 > kMaxGridThreads))
         return false;
-    const kx::Cut cut = kx::entropy_plan(dtype, rows, classes, width);
-    const int64_t m = cut.tile == 129 ? 128 : cut.tile, n = kx::entropy_columns(dtype, cut);
-    return cdiv(rows, m) * cdiv(classes, n) + 8 <= kMaxGridThreads / 512;
+    for (bool grad : {false, true}) {
+        const kx::Cut cut = kx::entropy_plan(dtype, rows, classes, width, grad);
+        const int64_t m = cut.tile == 129 ? 128 : cut.tile, n = kx::entropy_columns(dtype, cut);
+        if (cdiv(rows, m) * cdiv(classes, n) + 8 > kMaxGridThreads / 512) return false;
+    }
+    return true;
 }
 // The classes of a piece: equal pieces, of whole tiles.
 int64_t piece_of(int64_t rows, int64_t classes, int dtype) {
@@ -119,7 +122,7 @@ EntropyLayout entropy_layout(int64_t rows, int64_t classes, int64_t width, int d
         L.w = s.add((size_t)classes * pad8(width) * 2);
     }
     if (!grad) {
-        const kx::Cut cut = kx::entropy_plan(dtype, rows, classes, width);
+        const kx::Cut cut = kx::entropy_plan(dtype, rows, classes, width, false);
         L.part = s.add((size_t)cdiv(classes, kx::entropy_columns(dtype, cut)) * rows * 8);
         L.hit = s.add((size_t)rows * 4);
     } else {
@@ -355,7 +358,8 @@ int layers_route_backward(const float *dweights, const void *logits, int64_t ld,
 size_t layers_cross_entropy_workspace_bytes(int64_t rows, int64_t classes, int64_t width,
                                             int dtype, int unaligned) {
     if (!dtype_ok(dtype) || !entropy_shape_ok(dtype, rows, classes, width)) return 0;
-    const bool pads = dtype != EXPERTS_F32 && (unaligned || width % 2 != 0);
+    const bool pads = dtype != EXPERTS_F32 && (unaligned || width % 2 != 0) &&
+                      !kx::entropy_plan(dtype, rows, classes, width, false).thin;
     return entropy_layout(rows, classes, width, dtype, false, pads).total;
 }
 
@@ -370,7 +374,9 @@ int layers_cross_entropy(const void *x, int64_t ldx, const void *w, const int64_
     const size_t b = size_of(dtype);
     if (!aligned(x, b) || !aligned(w, b) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4))
         return KM_ERR_ALIGN;
-    const bool pads = dtype != EXPERTS_F32 && !(in_place(x, ldx, width) && in_place(w, width, width));
+    const kx::Cut cut = kx::entropy_plan(dtype, rows, classes, width, false);
+    const bool pads = dtype != EXPERTS_F32 && !cut.thin &&
+                      !(in_place(x, ldx, width) && in_place(w, width, width));
     const EntropyLayout L = entropy_layout(rows, classes, width, dtype, false, pads);
     if (!ws_ok(workspace, workspace_bytes, L.total)) return KM_ERR_WORKSPACE;
     const Span outs[] = {{loss, 1, 0, rows, 4},
@@ -380,10 +386,13 @@ int layers_cross_entropy(const void *x, int64_t ldx, const void *w, const int64_
     if (int rc = check_alias(outs, 3, ins, 3)) return rc;
     const hipStream_t s = (hipStream_t)stream;
     char *base = ws_base(workspace);
-    const Operand xq = operand(x, ldx, rows, width, dtype, base + L.x, s);
-    if (xq.e != hipSuccess) return KM_ERR_HIP;
-    const Operand wp = operand(w, width, classes, width, dtype, base + L.w, s);
-    if (wp.e != hipSuccess) return KM_ERR_HIP;
+    Operand xq = {x, ldx, width, hipSuccess}, wp = {w, width, width, hipSuccess};
+    if (pads) {
+        xq = operand(x, ldx, rows, width, dtype, base + L.x, s);
+        if (xq.e != hipSuccess) return KM_ERR_HIP;
+        wp = operand(w, width, classes, width, dtype, base + L.w, s);
+        if (wp.e != hipSuccess) return KM_ERR_HIP;
+    }
     kx::EntropyProblem pr = {};
     pr.x = xq.p;
     pr.ldx = xq.ld;
@@ -393,7 +402,8 @@ int layers_cross_entropy(const void *x, int64_t ldx, const void *w, const int64_
     pr.classes = classes;
     pr.width = width;
     pr.targets = targets;
-    pr.tile = kx::entropy_plan(dtype, rows, classes, width).tile;
+    pr.tile = cut.tile;
+    pr.thin = cut.thin ? cut.splits : 0;
     pr.part = (float2 *)(base + L.part);
     pr.hit = (float *)(base + L.hit);
     pr.loss = loss;
@@ -481,7 +491,7 @@ int layers_cross_entropy_backward(const float *dloss, const float *dlse, const v
         pr.first = first;
         pr.count = count;
         pr.lddz = pad8(count);
-        pr.tile = kx::entropy_plan(dtype, rows, count, width).tile;
+        pr.tile = kx::entropy_plan(dtype, rows, count, width, true).tile;
         if (rows > 0 && kx::launch_entropy_dz(dtype, pr, s) != hipSuccess) return KM_ERR_HIP;
         g.w = (const char *)wp.p + (size_t)first * wp.ld * b;
         g.lddz = pr.lddz;
@@ -491,6 +501,12 @@ int layers_cross_entropy_backward(const float *dloss, const float *dlse, const v
         g.dw = dw ? (char *)dw + (size_t)first * width * b : nullptr;
         g.dx_cut = dx_cut(dtype, rows, count, width);
         g.dw_cut = kx::grad_plan(dtype, rows, count, width, 1);
+        const int tile = g.dx && g.dw ? kx::both_plan(dtype, rows, count, width, false, 1, g.dx_cut, g.dw_cut) : 0;
+        g.together = tile != 0;
+        if (tile) {
+            g.dx_cut.tile = g.dw_cut.tile = tile;
+            g.dx_cut.splits = g.dw_cut.splits = 1;
+        }
         if (kx::launch_entropy_grad(dtype, g, s) != hipSuccess) return KM_ERR_HIP;
     }
     return KM_OK;

@@ -38,72 +38,110 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[4][N], int
 // The thread's values of a row: C chunks of V, the last of the row moved back where it
 // would leave it. again(i): how many of chunk i's first values the chunk before holds too
 // (V: all, the chunk lies past the row).
-template <int V, int C, int NT>
+// EVEN: the row is whole chunks, so again is 0 or V.
+template <int V, int C, int NT, bool EVEN>
 struct Chunks {
     int64_t at[C];
     int again[C];
+    // Whether value j of chunk i counts here. (A comparison in the loop over rows: kept over
+    // all of it, the answers were more than the scalar registers.)
+    __device__ __forceinline__ bool counts(int i, int j) const {
+        int n = again[i];
+        if (!EVEN) asm volatile("" : "+v"(n));
+        return EVEN ? n != V : j >= n;
+    }
+    __device__ __forceinline__ bool there(int i) const { return again[i] != V; }
     __device__ __forceinline__ void init(int64_t width) {
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             const int64_t c = ((int64_t)i * NT + threadIdx.x % NT) * V;
-            at[i] = c < width ? chunk_at<V>(c, width) : 0;
+            at[i] = c < width ? chunk_at<V>(c, width) : 0;  // (width >= V)
             again[i] = c < width ? (int)(c - at[i]) : V;
         }
     }
 };
 
-template <typename T, typename W, int NT, int C>
-__global__ __launch_bounds__(256) void norm_kernel(NormProblem pr) {
-    constexpr int V = vec<T>();
-    __shared__ float part[2][4][1];
-    const int64_t r = own_token<NT>();
-    if (r >= pr.rows) return;
-    const int64_t width = pr.width;
-    Chunks<V, C, NT> ch;
-    ch.init(width);
-    const T *x = (const T *)pr.x + r * pr.ldx;
-    T v[C][V];
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-        load_part<false, T, V>(x + ch.at[i], ch.again[i] == V ? 0 : width - ch.at[i], v[i]);
-    float sum[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) sum[0] += j < ch.again[i] || j >= width ? 0.0f : (float)v[i][j];
-    row_sums<NT>(sum, part, 0);
-    const float mean = sum[0] / (float)width;
-    sum[0] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float d = (float)v[i][j] - mean;
-            sum[0] += j < ch.again[i] || j >= width ? 0.0f : d * d;
-        }
-    row_sums<NT>(sum, part, 1);
-    const float rstd = 1.0f / sqrtf(sum[0] / (float)width + pr.eps);
-    const W *weight = (const W *)pr.weight, *bias = (const W *)pr.bias;
-    T *out = (T *)pr.out + r * pr.ldo;
+template <bool ONCE, typename T, int V, int C, int NT, bool EVEN>
+__device__ __forceinline__ void load_chunks(const Chunks<V, C, NT, EVEN> &ch, const T *row, T (&v)[C][V]) {
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        if (ch.again[i] == V) continue;
-        const int64_t left = width - ch.at[i];
-        W w[V], b[V];
-        if (weight) load_part<false, W, V>(weight + ch.at[i], left, w);
-        if (bias) load_part<false, W, V>(bias + ch.at[i], left, b);
+        if (ch.there(i)) {
+            if (ONCE)
+                load_once(row + ch.at[i], v[i]);
+            else
+                load_vec(row + ch.at[i], v[i]);
+        } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float h = ((float)v[i][j] - mean) * rstd;
-            if (weight) h *= (float)w[j];
-            if (bias) h += (float)b[j];
-            v[i][j] = (T)h;
+            for (int j = 0; j < V; ++j) v[i][j] = (T)0.0f;
         }
-        store_part<false, T, V>(out + ch.at[i], left, v[i]);
     }
-    if (threadIdx.x % NT == 0 && pr.mean) {
-        pr.mean[r] = mean;
-        pr.rstd[r] = rstd;
+}
+template <bool ONCE, typename T, int V>
+__device__ __forceinline__ void store_chunk(T *p, const T (&v)[V]) {
+    if (ONCE)
+        store_once(p, v);
+    else
+        store_vec(p, v);
+}
+
+// Every `step`-th row a wave (NT = 64) or block, the next one on its way meanwhile. ONCE:
+// rows that no cache holds pass the caches by (see once_of).
+template <typename T, typename W, int NT, int C, bool ONCE, bool EVEN>
+__global__ __launch_bounds__(256) void norm_kernel(NormProblem pr, int64_t step) {
+    constexpr int V = vec<T>();
+    __shared__ float part[2][4][1];
+    int64_t r = own_token<NT>();
+    if (r >= pr.rows) return;
+    const int64_t width = pr.width;
+    Chunks<V, C, NT, EVEN> ch;
+    ch.init(width);
+    const W *weight = (const W *)pr.weight, *bias = (const W *)pr.bias;
+    T next[C][V];
+    load_chunks<ONCE>(ch, (const T *)pr.x + r * pr.ldx, next);
+    for (; r < pr.rows; r += step) {
+        T v[C][V];
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) v[i][j] = next[i][j];
+        if (r + step < pr.rows) load_chunks<ONCE>(ch, (const T *)pr.x + (r + step) * pr.ldx, next);
+        float sum[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[0] += ch.counts(i, j) ? (float)v[i][j] : 0.0f;
+        row_sums<NT>(sum, part, 0);
+        const float mean = sum[0] / (float)width;
+        sum[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float d = (float)v[i][j] - mean;
+                sum[0] += ch.counts(i, j) ? d * d : 0.0f;
+            }
+        row_sums<NT>(sum, part, 1);
+        const float rstd = 1.0f / sqrtf(sum[0] / (float)width + pr.eps);
+        T *out = (T *)pr.out + r * pr.ldo;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            if (!ch.there(i)) continue;
+            W w[V], b[V];
+            if (weight) load_vec(weight + ch.at[i], w);
+            if (bias) load_vec(bias + ch.at[i], b);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float h = ((float)v[i][j] - mean) * rstd;
+                if (weight) h *= (float)w[j];
+                if (bias) h += (float)b[j];
+                v[i][j] = (T)h;
+            }
+            store_chunk<ONCE>(out + ch.at[i], v[i]);
+        }
+        if (threadIdx.x % NT == 0 && pr.mean) {
+            pr.mean[r] = mean;
+            pr.rstd[r] = rstd;
+        }
     }
 }
 
@@ -161,45 +199,57 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormProblem pr) {
 
 // dx, and the columns' sums over the rows that the wave (NT = 64) or block takes: every
 // `step`-th. A block leaves one part of the sums.
-template <typename T, typename W, int NT, int C>
+template <typename T, typename W, int NT, int C, bool ONCE, bool EVEN>
 __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int64_t step) {
     constexpr int V = vec<T>();
     constexpr int kRows = 256 / NT;
     __shared__ float part[2][4][2];
     __shared__ float columns[NT == 64 ? C * 64 * V : 1];
     const int64_t width = pr.width;
-    Chunks<V, C, NT> ch;
+    Chunks<V, C, NT, EVEN> ch;
     ch.init(width);
     const W *weight = (const W *)pr.weight;
     W w[C][V];
     float dw[C][V], db[C][V];
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        if (weight) load_part<false, W, V>(weight + ch.at[i], ch.again[i] == V ? 0 : width - ch.at[i], w[i]);
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            if (!weight) w[i][j] = (W)1.0f;
+            w[i][j] = (W)1.0f;
             dw[i][j] = db[i][j] = 0.0f;
         }
+        if (weight && ch.there(i)) load_vec(weight + ch.at[i], w[i]);
     }
+    const float each = 1.0f / (float)width;
     int turn = 0;
-    for (int64_t r = own_token<NT>(); r < pr.rows; r += step, ++turn) {
-        const T *x = (const T *)pr.x + r * pr.ldx, *dy = (const T *)pr.dy + r * pr.lddy;
+    int64_t r = own_token<NT>();
+    T nv[C][V], nd[C][V];
+    float mean_of_next = 0.0f, rstd_of_next = 0.0f;
+    auto fetch = [&](int64_t r) {
+        load_chunks<ONCE>(ch, (const T *)pr.x + r * pr.ldx, nv);
+        load_chunks<ONCE>(ch, (const T *)pr.dy + r * pr.lddy, nd);
+        mean_of_next = pr.mean[r];
+        rstd_of_next = pr.rstd[r];
+    };
+    if (r < pr.rows) fetch(r);
+    for (; r < pr.rows; r += step, ++turn) {
         T v[C][V], d[C][V];
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int64_t left = ch.again[i] == V ? 0 : width - ch.at[i];
-            load_part<false, T, V>(x + ch.at[i], left, v[i]);
-            load_part<false, T, V>(dy + ch.at[i], left, d[i]);
-        }
-        const float mean = pr.mean[r], rstd = pr.rstd[r];
+        for (int i = 0; i < C; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                v[i][j] = nv[i][j];
+                d[i][j] = nd[i][j];
+            }
+        const float mean = mean_of_next, rstd = rstd_of_next;
+        if (r + step < pr.rows) fetch(r + step);
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < C; ++i)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float h = ((float)v[i][j] - mean) * rstd, y = (float)d[i][j];
-                const float g = j < ch.again[i] || j >= width ? 0.0f : y * (float)w[i][j];
+                const float g = ch.counts(i, j) ? y * (float)w[i][j] : 0.0f;
                 dw[i][j] += y * h;
                 db[i][j] += y;
                 sum[0] += g;
@@ -207,17 +257,17 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int6
             }
         if (!pr.out) continue;
         row_sums<NT>(sum, part, turn);
-        const float m = sum[0] / (float)width, mh = sum[1] / (float)width;
+        const float m = sum[0] * each, mh = sum[1] * each;
         T *out = (T *)pr.out + r * pr.ldo;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            if (ch.again[i] == V) continue;
+            if (!ch.there(i)) continue;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const float h = ((float)v[i][j] - mean) * rstd;
                 v[i][j] = (T)(rstd * ((float)d[i][j] * (float)w[i][j] - m - h * mh));
             }
-            store_part<false, T, V>(out + ch.at[i], width - ch.at[i], v[i]);
+            store_chunk<ONCE>(out + ch.at[i], v[i]);
         }
     }
     if (!pr.partial) return;
@@ -242,8 +292,7 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int6
         }
 #pragma unroll
         for (int i = 0; i < C; ++i)
-            if (ch.again[i] != V)
-                store_part<false, float, V>(to + k * width + ch.at[i], width - ch.at[i], own[i]);
+            if (ch.there(i)) store_vec(to + k * width + ch.at[i], own[i]);
     }
 }
 
@@ -340,15 +389,26 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormProblem pr, int64_t
 }
 
 // How rows are held: by a wave up to four chunks of 16 bytes a lane, by a block up to
-// four, else not.
+// four, else not (or of rows shorter than one access).
 enum { kWave, kBlock, kLong };
 template <typename T>
 int how_held(int64_t rows, int64_t width) {
     const int64_t wave = 64 * vec<T>();
+    if (width < vec<T>()) return kLong;  // less than one access
     if (width <= 4 * wave && (rows >= 1024 || width <= wave)) return kWave;
     return width <= 16 * wave ? kBlock : kLong;
 }
 constexpr int64_t kParts = 512;
+constexpr int64_t kBlocks = 1024;
+
+// Rows that are more than the 256 MB of the memory-side cache pass the caches by, where they
+// are whole lines of 128 bytes (the rule of the token rows in tokens.hip).
+template <typename T>
+bool once_of(const NormProblem &pr, int64_t tensors) {
+    const int64_t size = sizeof(T);
+    return tensors * pr.rows * pr.width * size > 256 << 20 && pr.width * size % 128 == 0 &&
+           pr.ldx * size % 128 == 0 && pr.ldo * size % 128 == 0;
+}
 
 template <typename T, class F>
 hipError_t by_size(int64_t rows, int64_t width, F f) {
@@ -369,7 +429,12 @@ hipError_t norm_t(const NormProblem &pr, hipStream_t s) {
         return launch(norm_long_kernel<T, W>, pr.rows, 256, 0, s, pr);
     return by_size<T>(pr.rows, pr.width, [&](auto nt, auto c) {
         constexpr int NT = decltype(nt)::value, C = decltype(c)::value;
-        return launch(norm_kernel<T, W, NT, C>, cdiv(pr.rows, 256 / NT), 256, 0, s, pr);
+        // As many blocks as run at once.
+        const int64_t all = cdiv(pr.rows, 256 / NT), blocks = all < kBlocks ? all : kBlocks;
+        const auto kernel = pr.width % vec<T>()  ? norm_kernel<T, W, NT, C, false, false>
+                            : once_of<T>(pr, 2) ? norm_kernel<T, W, NT, C, true, true>
+                                                : norm_kernel<T, W, NT, C, false, true>;
+        return launch(kernel, blocks, 256, 0, s, pr, blocks * (256 / NT));
     });
 }
 
@@ -386,7 +451,10 @@ hipError_t backward_t(NormProblem pr, int64_t parts, hipStream_t s) {
     } else {
         e = by_size<T>(pr.rows, pr.width, [&](auto nt, auto c) {
             constexpr int NT = decltype(nt)::value, C = decltype(c)::value;
-            return launch(norm_backward_kernel<T, W, NT, C>, parts, 256, 0, s, pr, parts * (256 / NT));
+            const auto kernel = pr.width % vec<T>()  ? norm_backward_kernel<T, W, NT, C, false, false>
+                                : once_of<T>(pr, 3) ? norm_backward_kernel<T, W, NT, C, true, true>
+                                                    : norm_backward_kernel<T, W, NT, C, false, true>;
+            return launch(kernel, parts, 256, 0, s, pr, parts * (256 / NT));
         });
     }
     if (e != hipSuccess || !sums) return e;

@@ -368,12 +368,18 @@ def check_entropy(dtype, rows, classes, width, skip=0.0, lse_grad=False, scale=1
     assert (loss[~live] == 0).all()
     if not lse_grad:
         assert (dx[~live] == 0).all()
-    if views:  # rows apart and off their boundaries; one output; the same bits
+    if views:  # rows apart and off their boundaries: the same bits; one output (cut otherwise)
         sx = strided(x)
         again = layers.cross_entropy(sx, w, targets)
         assert torch.equal(again[0], loss) and torch.equal(again[1], lse)
-        assert torch.equal(layers.cross_entropy_backward(dloss, sx, w, targets, lse, dlse, need_dw=False)[0], dx)
-        assert torch.equal(layers.cross_entropy_backward(dloss, sx, w, targets, lse, dlse, need_dx=False)[1], dw)
+        again = layers.cross_entropy_backward(dloss, sx, w, targets, lse, dlse)
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+        only = layers.cross_entropy_backward(dloss, sx, w, targets, lse, dlse, need_dw=False)
+        assert only[1] is None
+        close(only[0], *(t.cpu() for t in want["dx"]), "dx alone")
+        only = layers.cross_entropy_backward(dloss, sx, w, targets, lse, dlse, need_dx=False)
+        assert only[0] is None
+        close(only[1], *(t.cpu() for t in want["dw"]), "dw alone")
 
 
 @pytest.mark.parametrize("dtype", TYPES)
