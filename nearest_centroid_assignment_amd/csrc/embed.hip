@@ -22,7 +22,7 @@ __global__ __launch_bounds__(256) void embed_kernel(const int64_t *__restrict__ 
                                                     int64_t width, float scale, T *__restrict__ out,
                                                     int64_t ldo) {
     constexpr int V = vec<T>();
-    const int64_t t = own_token<NT>();
+    const int64_t t = NT == 16 ? (int64_t)blockIdx.x * 16 + threadIdx.x / 16 : own_token<NT>();
     if (t >= tokens) return;
     const int64_t id = ids[t];
     const bool live = id >= 0 && id < classes;
@@ -124,12 +124,19 @@ struct SumArgs {
 };
 
 // Chunk c's part of a row whose tokens start at `lo`: a row that starts inside the chunk
-// has the second of its two slots, the one that starts before it, or with it, the first.
+// has the second of its two slots, the one that starts before it, or with it, the first (as
+// sum_kernel leaves them).
 __device__ __forceinline__ int64_t slot_of(int64_t c, int chunk, int lo) {
     return 2 * c + (lo > c * chunk ? 1 : 0);
 }
 
-template <typename T, int V, int NT>
+// A chunk's tokens and their numbers lie in the lanes of the wave (kChunk at most), and its rows
+// come in groups of eight, the next group on its way while one is added. Which rows end
+// inside the chunk shows in the numbers themselves; only the first row may have begun before
+// it and the last go on after it.
+constexpr int kChunk = 64;
+
+template <typename T, int V, int NT, bool ONCE>
 __global__ __launch_bounds__(256) void sum_kernel(SumArgs a, const T *__restrict__ dy,
                                                   T *__restrict__ dw) {
     constexpr int kAhead = 8;
@@ -138,41 +145,54 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a, const T *__restrict
     const int64_t col = ((unit - c * a.col_blocks) * NT + threadIdx.x % NT) * V;
     const int64_t p0 = c * a.chunk, total = *a.total;
     if (p0 >= total) return;
-    const int64_t p1 = p0 + a.chunk < total ? p0 + a.chunk : total;
+    const int n = (int)(total - p0 < a.chunk ? total - p0 : a.chunk);
+    const int lane = threadIdx.x & 63;
+    const int token = a.order[p0 + (lane < n ? lane : n - 1)];
+    const int number = (int)a.ids[token];
+    const int first_lo = a.lo[__builtin_amdgcn_readlane(number, 0)];
+    const int last_hi = a.hi[__builtin_amdgcn_readlane(number, n - 1)];
     const bool active = col < a.width;
     const int64_t at = active ? chunk_at<V>(col, a.width) : 0;
     const int64_t left = active ? a.width - at : 0;
     float sum[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) sum[j] = 0.0f;
-    int64_t id = a.ids[a.order[p0]];
-    auto flush = [&]() {
-        const int lo = a.lo[id], hi = a.hi[id];
-        if (lo >= p0 && hi <= p1) {
+    T v[kAhead][V], next[kAhead][V];
+    auto fetch = [&](int p, T (&to)[kAhead][V]) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t t = __builtin_amdgcn_readlane(token, p + u < n ? p + u : n - 1);
+            load_part<ONCE, T, V>(dy + t * a.lddy + at, left, to[u]);
+        }
+    };
+    int id = __builtin_amdgcn_readlane(number, 0), start = 0;
+    auto flush = [&](int end) {
+        const bool whole = (start > 0 || first_lo >= p0) && (end < n || last_hi <= p0 + n);
+        if (whole) {
             T r[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) r[j] = (T)(a.scale * sum[j]);
-            store_part<false, T, V>(dw + id * a.width + at, left, r);
+            store_part<false, T, V>(dw + (int64_t)id * a.width + at, left, r);
         } else {
-            store_part<false, float, V>(a.partial + slot_of(c, a.chunk, lo) * a.width + at, left, sum);
+            float *to = a.partial + (2 * c + (start > 0 ? 1 : 0)) * a.width;
+            store_part<false, float, V>(to + at, left, sum);
         }
     };
-    for (int64_t p = p0; p < p1; p += kAhead) {
-        int64_t token[kAhead], next[kAhead];
-        T v[kAhead][V];
+    fetch(0, next);
+    for (int p = 0; p < n; p += kAhead) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) token[u] = a.order[p + u < p1 ? p + u : p1 - 1];
+        for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            next[u] = a.ids[token[u]];
-            load_part<false, T, V>(dy + token[u] * a.lddy + at, left, v[u]);
-        }
+            for (int j = 0; j < V; ++j) v[u][j] = next[u][j];
+        if (p + kAhead < n) fetch(p + kAhead, next);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            if (p + u >= p1) break;
-            if (next[u] != id) {
-                flush();
-                id = next[u];
+            if (p + u >= n) break;
+            const int now = __builtin_amdgcn_readlane(number, p + u);
+            if (now != id) {
+                flush(p + u);
+                id = now;
+                start = p + u;
 #pragma unroll
                 for (int j = 0; j < V; ++j) sum[j] = 0.0f;
             }
@@ -180,7 +200,7 @@ __global__ __launch_bounds__(256) void sum_kernel(SumArgs a, const T *__restrict
             for (int j = 0; j < V; ++j) sum[j] += (float)v[u][j];
         }
     }
-    flush();
+    flush(n);
 }
 
 // The first `joins` blocks: chunk c and 256 columns; the row that starts in chunk c and
@@ -198,7 +218,7 @@ __global__ __launch_bounds__(256) void finish_kernel(SumArgs a, int64_t joins, T
         for (int j = 0; j < V; ++j) zero[j] = (T)0.0f;
         for (int64_t col = lane * V; col < a.width; col += 64 * V) {
             const int64_t at = chunk_at<V>(col, a.width);
-            store_part<false, T, V>(dw + v * a.width + at, a.width - at, zero);
+            store_part<true, T, V>(dw + v * a.width + at, a.width - at, zero);
         }
         return;
     }
@@ -234,17 +254,30 @@ __global__ __launch_bounds__(256) void finish_kernel(SumArgs a, int64_t joins, T
 }
 
 // A wave to a token's row where there are enough of them and they are short, else a block
-// (the rule of the token rows in tokens.hip).
+// (the rule of the token rows in tokens.hip); 16 lanes where they hold it in one access each.
+// (Four rows a wave, their loads in flight together: 65536 x 4 KB of 50000 84 us, a block to
+// each 78.)
 constexpr int64_t kMostBlocks = 1 << 24;
 bool by_wave(int64_t rows, int64_t bytes) {
     return rows >= kMostBlocks || (rows >= 2048 && bytes <= 3 << 10);
+}
+
+// Rows that are more than the 256 MB of the memory-side cache pass the caches by, where they
+// are whole lines of 128 bytes (the same rule's other half).
+template <typename T>
+bool passes_by(int64_t rows, int64_t width, int64_t ld) {
+    const int64_t size = sizeof(T);
+    return width * size % 128 == 0 && ld * size % 128 == 0 && rows * width * size >= 256 << 20;
 }
 
 template <typename T>
 hipError_t embed_t(const int64_t *ids, int64_t tokens, const void *w, int64_t classes, int64_t width,
                    float scale, void *out, int64_t ldo, hipStream_t s) {
     const int64_t bytes = width * (int64_t)sizeof(T);
-    const bool once = bytes % 128 == 0 && ldo * (int64_t)sizeof(T) % 128 == 0 && tokens * bytes > 256 << 20;
+    const bool once = passes_by<T>(tokens, width, ldo);
+    if (width <= 16 * vec<T>() && tokens < kMostBlocks * 16)
+        return launch(once ? embed_kernel<T, 16, true> : embed_kernel<T, 16, false>, cdiv(tokens, 16), 256, 0,
+                      s, ids, tokens, (const T *)w, classes, width, scale, (T *)out, ldo);
     if (by_wave(tokens, bytes))
         return launch(once ? embed_kernel<T, 64, true> : embed_kernel<T, 64, false>, cdiv(tokens, 4),
                       256, 0, s, ids, tokens, (const T *)w, classes, width, scale, (T *)out, ldo);
@@ -264,13 +297,14 @@ hipError_t with_rows(int64_t width, F f) {
 template <typename T>
 hipError_t backward_t(SumArgs a, int64_t tokens, const void *dy, void *dw, hipStream_t s) {
     const int64_t chunks = cdiv(tokens, a.chunk);
+    const bool once = passes_by<T>(tokens, a.width, a.lddy);
     hipError_t e = hipSuccess;
     if (tokens > 0)
         e = with_rows<T>(a.width, [&](auto v, auto nt) {
             constexpr int V = decltype(v)::value, NT = decltype(nt)::value;
             a.col_blocks = (int)cdiv(a.width, V * NT);
-            return launch(sum_kernel<T, V, NT>, cdiv(chunks * a.col_blocks, 256 / NT), 256, 0, s, a,
-                          (const T *)dy, (T *)dw);
+            return launch(once ? sum_kernel<T, V, NT, true> : sum_kernel<T, V, NT, false>,
+                          cdiv(chunks * a.col_blocks, 256 / NT), 256, 0, s, a, (const T *)dy, (T *)dw);
         });
     if (e != hipSuccess) return e;
     const int64_t joins = chunks * cdiv(a.width, 256);
@@ -279,7 +313,7 @@ hipError_t backward_t(SumArgs a, int64_t tokens, const void *dy, void *dw, hipSt
 
 }  // namespace
 
-int64_t embed_chunk(int64_t tokens) { return tokens >= 65536 ? 64 : tokens >= 16384 ? 32 : 16; }
+int64_t embed_chunk(int64_t tokens) { return tokens >= 65536 ? kChunk : tokens >= 16384 ? kChunk / 2 : kChunk / 4; }
 
 bool embed_grid_ok(int dtype, int64_t tokens, int64_t classes, int64_t width) {
     const int64_t chunks = cdiv(tokens, embed_chunk(tokens));
