@@ -109,7 +109,8 @@ int layers_route_backward(const float *dweights, const void *logits, int64_t ld,
  * A target outside [0, classes) is ignored: its loss is 0 (lse is still given).
  * 0 <= rows < 2^31, 1 <= classes, width, ld <= 2^20, and fewer than about 2^23 tiles of
  * 64 x 64 to 256 x 256 logits. float32 uses the float32 matrix instructions, the 16-bit types
- * theirs; both accumulate in float32. Workspace: 8 bytes for 64 to 256 logits of a row, and
+ * theirs; both accumulate in float32. Workspace: 8 bytes for 64 to 256 logits of a row (small
+ * products of a long width: their logits' partial sums, at most 1024 tiles), and
  * where more than 32 16-bit rows do not lie on 4-byte boundaries (width odd, or, with
  * `unaligned` non-zero, an odd ld or a pointer off 4 bytes) room for their copies on padded
  * rows, w's too.

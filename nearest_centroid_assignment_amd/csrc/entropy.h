@@ -16,36 +16,11 @@
 // over the pieces in float32.
 #pragma once
 
-#include "layers.h"
+#include "entropy_rows.h"
 #include "linear.h"
 
 namespace kx {
 namespace {
-
-constexpr float kLog2e = 1.44269504088896f;
-
-__device__ __forceinline__ float finite_or_0(float m) {
-    return fabsf(m) < INFINITY ? m : 0.0f;
-}
-
-// A row's largest logit m and its sum of e^(z - m) (of e^z where m is not finite), and
-// another's added to it.
-struct RowSum {
-    float m, s;
-    __device__ __forceinline__ void add(float m2, float s2) {
-        const float most = fmaxf(m, m2), from = finite_or_0(most);
-        // (Nothing times an overflowing factor would be a NaN.)
-        const float own = s == 0.0f ? 0.0f : s * __builtin_amdgcn_exp2f((finite_or_0(m) - from) * kLog2e);
-        const float other = s2 == 0.0f ? 0.0f : s2 * __builtin_amdgcn_exp2f((finite_or_0(m2) - from) * kLog2e);
-        m = most;
-        s = own + other;
-    }
-};
-
-// Whether target t is a class, and its number.
-__device__ __forceinline__ int class_of(int64_t t, int64_t classes) {
-    return t >= 0 && t < classes ? (int)t : -1;
-}
 
 // acc = the tile (mt, nt) of x w^T over the piece's classes.
 template <class S>
@@ -257,12 +232,6 @@ __global__ __launch_bounds__(512) void entropy_thin_kernel(EntropyProblem pr) {
     if (threadIdx.x % kEach == 0 && row < rows) pr.part[(int64_t)blockIdx.x * rows + row] = make_float2(m, s);
 }
 
-// What dz of a row needs.
-struct RowTerms {
-    float lse, a, b;  // lse in units of log 2
-    int target;       // in the piece
-};
-
 template <class S>
 __global__ __launch_bounds__(S::NW * 64, 2) void entropy_dz_kernel(EntropyProblem pr) {
     typedef typename S::type T;
@@ -275,14 +244,9 @@ __global__ __launch_bounds__(S::NW * 64, 2) void entropy_dz_kernel(EntropyProble
     const int m0 = mt * S::BM, n0 = nt * S::BN;
     const int rows = (int)pr.rows, count = (int)pr.count;
     // Read before the product, which has barriers enough between this and their use.
-    if (threadIdx.x < S::BM) {
-        const float scale = pr.scale ? *pr.scale : 1.0f;
-        const int m = m0 + (int)threadIdx.x < rows ? m0 + (int)threadIdx.x : rows - 1;
-        const int t = class_of(pr.targets[m], pr.classes);
-        const float b = t >= 0 ? pr.dloss[m] * scale : 0.0f;
-        const float a = b + (pr.dlse ? pr.dlse[m] * scale : 0.0f);
-        terms[threadIdx.x] = {pr.lse[m] * kLog2e, a, b, t >= 0 ? t - (int)pr.first : -1};
-    }
+    const float scale = scale_of(pr, (float *)memory);
+    if (threadIdx.x < S::BM)
+        terms[threadIdx.x] = terms_of(pr, m0 + (int)threadIdx.x < rows ? m0 + threadIdx.x : rows - 1, scale);
     f32x4 acc[S::TM][S::TN];
     entropy_tile<S>(pr, m0, n0, (lds_char *)memory, wave, lane, acc);
     const int wm = (wave / S::WN) * (S::BM / S::WM);
@@ -296,18 +260,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void entropy_dz_kernel(EntropyProble
                 const int64_t m = wm + row;
                 const int n = wn + col;
                 if (!kWhole && (m0 + m >= rows || n >= pr.lddz)) return;
-                if (x.a == 0.0f) {  // nothing weighs an ignored row, whatever it holds
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[i] = 0.0f;
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        z[i] = x.a * __builtin_amdgcn_exp2f(fmaf(z[i], kLog2e, -x.lse));
-                }
-                if ((unsigned)(x.target - n) < 8u) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) z[i] -= n + i == x.target ? x.b : 0.0f;
-                }
+                dz_of(z, n, x);
                 if (!kWhole) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) z[i] = n + i < count ? z[i] : 0.0f;  // pads whole vectors

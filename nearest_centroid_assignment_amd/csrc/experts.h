@@ -220,8 +220,8 @@ struct Cut {
 Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped, int64_t experts,
               bool p_rows);
 Cut grad_plan(int dtype, int64_t rows, int64_t m_cols, int64_t n_cols, int64_t experts);
-// rows_plan's for a product of one group whose depth stays whole and whose tiles are full.
-Cut whole_plan(int dtype, int64_t rows, int64_t cols, int64_t depth);
+// rows_plan's for a product of one group, with the depth in `most_parts` parts at most.
+Cut plan_in_parts(int dtype, int64_t rows, int64_t cols, int64_t depth, int most_parts);
 // The tile of dx and dw in one launch, 0 where the two launches are better.
 int both_plan(int dtype, int64_t rows, int64_t outs, int64_t ins, bool grouped, int64_t experts,
               const Cut &dx, const Cut &dw);

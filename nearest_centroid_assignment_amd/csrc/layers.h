@@ -82,19 +82,25 @@ struct EntropyProblem {
     float *loss, *lse;        // outputs; lse is read by the gradient
     // The gradient.
     const float *dloss, *dlse;
-    const float *scale;       // dz's factor and its inverse (NULL: 1)
+    float *scale;             // dz's factor and its inverse (NULL: 1)
+    float most_dz;            // of scaled rows; 0: scale is given, else the dz kernel finds it
+    // A product cut in depth: float32 parts of the logits, rows x count each (parts 1: none).
+    int parts;
+    float *logits;
     int64_t first, count;     // classes of this piece
     void *dz;                 // rows x lddz
     int64_t lddz;
 };
 // With `thin` (few rows, the forward call), tile rows and 16 * splits columns a block, and any
-// rows are read in place.
+// rows are read in place; else in `splits` parts of the depth (logits, above).
 Cut entropy_plan(int dtype, int64_t rows, int64_t classes, int64_t width, bool grad);
-int entropy_columns(int dtype, const Cut &cut);  // of a tile
+int entropy_columns(const Cut &cut);  // of a tile
 hipError_t launch_entropy(int dtype, const EntropyProblem &pr, hipStream_t s);
 hipError_t launch_entropy_dz(int dtype, const EntropyProblem &pr, hipStream_t s);
-// The factor of a 16-bit dz and its inverse.
-hipError_t launch_entropy_scale(int dtype, const EntropyProblem &pr, float *scale, hipStream_t s);
+// The factor of a 16-bit dz and its inverse, where the rows are too many for every block of the
+// dz kernel to look at them.
+hipError_t launch_entropy_scale(const EntropyProblem &pr, hipStream_t s);
+constexpr int64_t kOwnScale = 1024;  // rows
 
 // dx (first and last piece, sums between them) and dw of a piece.
 struct EntropyGrad {

@@ -83,8 +83,8 @@ bool entropy_shape_ok(int dtype, int64_t rows, int64_t classes, int64_t width) {
         return false;
     for (bool grad : {false, true}) {
         const kx::Cut cut = kx::entropy_plan(dtype, rows, classes, width, grad);
-        const int64_t m = cut.tile == 129 ? 128 : cut.tile, n = kx::entropy_columns(dtype, cut);
-        if (cdiv(rows, m) * cdiv(classes, n) + 8 > kMaxGridThreads / 512) return false;
+        const int64_t m = cut.tile == 129 ? 128 : cut.tile, n = kx::entropy_columns(cut);
+        if (cdiv(rows, m) * cdiv(classes, n) * (cut.thin ? 1 : cut.splits) + 8 > kMaxGridThreads / 512) return false;
     }
     return true;
 }
@@ -96,22 +96,31 @@ int64_t piece_of(int64_t rows, int64_t classes, int dtype) {
     const int64_t pieces = cdiv(classes, most);
     return cdiv(cdiv(classes, pieces), 256) * 256;
 }
+// Few rows or classes leave few tiles of a deep product: up to 64 parts of it.
+constexpr int kMostParts = 64;
 kx::Cut dx_cut(int dtype, int64_t rows, int64_t count, int64_t width) {
-    return kx::rows_plan(dtype, rows, width, count, false, 1, true);
+    return kx::plan_in_parts(dtype, rows, width, count, kMostParts);
+}
+kx::Cut dw_cut(int dtype, int64_t rows, int64_t count, int64_t width) {
+    return kx::plan_in_parts(dtype, count, width, rows, kMostParts);
+}
+bool cut_fits(const kx::Cut &c, int64_t m, int64_t n) {
+    const int64_t tm = c.tile == 129 ? 128 : c.tile, tn = c.tile == 32 ? 64 : tm;
+    return cdiv(m, tm) * cdiv(n, tn) * c.splits + 8 <= kMaxGridThreads / 512 &&
+           cdiv(m * cdiv(n, 8), 256) <= kMaxGridThreads / 256;
 }
 bool entropy_grad_ok(int dtype, int64_t rows, int64_t classes, int64_t width) {
     const int64_t count = piece_of(rows, classes, dtype);
     const int64_t last = classes - (classes - 1) / count * count;
     for (int64_t n : {count, last})
-        if (!kx::rows_grid_ok(dtype, rows, width, n, false, 1, true) ||
-            !kx::grad_grid_ok(dtype, rows, n, width, 1) ||
-            cdiv(n * cdiv(width, 8), 256) > kMaxGridThreads / 256)
+        if (!cut_fits(dx_cut(dtype, rows, n, width), rows, width) ||
+            !cut_fits(dw_cut(dtype, rows, n, width), n, width))
             return false;
     return true;
 }
 
 struct EntropyLayout {
-    size_t x = 0, w = 0, part = 0, hit = 0, dz = 0, sum = 0, partial = 0, scale = 0, total = 0;
+    size_t x = 0, w = 0, part = 0, hit = 0, logits = 0, dz = 0, sum = 0, partial = 0, scale = 0, total = 0;
 };
 EntropyLayout entropy_layout(int64_t rows, int64_t classes, int64_t width, int dtype, bool grad,
                              bool pads) {
@@ -123,23 +132,31 @@ EntropyLayout entropy_layout(int64_t rows, int64_t classes, int64_t width, int d
     }
     if (!grad) {
         const kx::Cut cut = kx::entropy_plan(dtype, rows, classes, width, false);
-        L.part = s.add((size_t)cdiv(classes, kx::entropy_columns(dtype, cut)) * rows * 8);
-        L.hit = s.add((size_t)rows * 4);
+        if (cut.thin || cut.splits == 1) {
+            L.part = s.add((size_t)cdiv(classes, kx::entropy_columns(cut)) * rows * 8);
+            L.hit = s.add((size_t)rows * 4);
+        } else {
+            L.logits = s.add((size_t)cut.splits * rows * classes * 4);
+        }
     } else {
         const int64_t count = piece_of(rows, classes, dtype);
         const int64_t last = classes - (classes - 1) / count * count;
         L.dz = s.add((size_t)rows * pad8(count) * size_of(dtype));
         if (count < classes) L.sum = s.add((size_t)rows * width * 4);
-        size_t partial = 0;
+        size_t partial = 0, logits = 0;
         for (int64_t n : {count, last}) {
+            const int z = kx::entropy_plan(dtype, rows, n, width, true).splits;
+            const size_t c = z > 1 ? (size_t)z * rows * n * 4 : 0;
+            logits = c > logits ? c : logits;
             const int dx = dx_cut(dtype, rows, n, width).splits;
-            const int dw = kx::grad_plan(dtype, rows, n, width, 1).splits;
+            const int dw = dw_cut(dtype, rows, n, width).splits;
             const size_t a = dx > 1 ? (size_t)dx * rows * width * 4 : 0;
             const size_t b = dw > 1 ? (size_t)dw * n * width * 4 : 0;
             partial = a > partial ? a : partial;
             partial = b > partial ? b : partial;
         }
-        L.partial = s.add(partial);
+        // (The logits' parts are done with before the products' parts are made.)
+        L.partial = L.logits = s.add(partial > logits ? partial : logits);
         if (dtype != EXPERTS_F32) L.scale = s.add(8);
     }
     L.total = s.with_slack();
@@ -404,6 +421,8 @@ int layers_cross_entropy(const void *x, int64_t ldx, const void *w, const int64_
     pr.targets = targets;
     pr.tile = cut.tile;
     pr.thin = cut.thin ? cut.splits : 0;
+    pr.parts = cut.thin ? 1 : cut.splits;
+    pr.logits = (float *)(base + L.logits);
     pr.part = (float2 *)(base + L.part);
     pr.hit = (float *)(base + L.hit);
     pr.loss = loss;
@@ -466,10 +485,14 @@ int layers_cross_entropy_backward(const float *dloss, const float *dlse, const v
     pr.dloss = dloss;
     pr.dlse = dlse;
     pr.dz = base + L.dz;
+    pr.logits = (float *)(base + L.logits);
     if (dtype != EXPERTS_F32 && rows > 0) {
-        float *scale = (float *)(base + L.scale);
-        if (kx::launch_entropy_scale(dtype, pr, scale, s) != hipSuccess) return KM_ERR_HIP;
-        pr.scale = scale;
+        pr.scale = (float *)(base + L.scale);
+        pr.most_dz = dtype == EXPERTS_F16 ? 16384.0f : 1.0f;
+        if (rows > kx::kOwnScale) {
+            if (kx::launch_entropy_scale(pr, s) != hipSuccess) return KM_ERR_HIP;
+            pr.most_dz = 0.0f;
+        }
     }
     kx::EntropyGrad g = {};
     g.dz = pr.dz;
@@ -491,7 +514,9 @@ int layers_cross_entropy_backward(const float *dloss, const float *dlse, const v
         pr.first = first;
         pr.count = count;
         pr.lddz = pad8(count);
-        pr.tile = kx::entropy_plan(dtype, rows, count, width, true).tile;
+        const kx::Cut cut = kx::entropy_plan(dtype, rows, count, width, true);
+        pr.tile = cut.tile;
+        pr.parts = cut.splits;
         if (rows > 0 && kx::launch_entropy_dz(dtype, pr, s) != hipSuccess) return KM_ERR_HIP;
         g.w = (const char *)wp.p + (size_t)first * wp.ld * b;
         g.lddz = pr.lddz;
@@ -500,7 +525,7 @@ int layers_cross_entropy_backward(const float *dloss, const float *dlse, const v
         g.last = first + count == classes;
         g.dw = dw ? (char *)dw + (size_t)first * width * b : nullptr;
         g.dx_cut = dx_cut(dtype, rows, count, width);
-        g.dw_cut = kx::grad_plan(dtype, rows, count, width, 1);
+        g.dw_cut = dw_cut(dtype, rows, count, width);
         const int tile = g.dx && g.dw ? kx::both_plan(dtype, rows, count, width, false, 1, g.dx_cut, g.dw_cut) : 0;
         g.together = tile != 0;
         if (tile) {

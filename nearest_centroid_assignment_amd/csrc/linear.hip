@@ -361,11 +361,11 @@ Cut rows_plan(int dtype, int64_t rows, int64_t cols, int64_t depth, bool grouped
     return c;
 }
 
-Cut whole_plan(int dtype, int64_t rows, int64_t cols, int64_t depth) {
+Cut plan_in_parts(int dtype, int64_t rows, int64_t cols, int64_t depth, int most_parts) {
     auto tiles = [&](int64_t m, int64_t n) { return cdiv(rows, m) * cdiv(cols, n); };
     const int64_t size = dtype == 0 ? 4 : 2;
     Cut c = best_cut(dtype, cdiv(depth * size, 128), (rows + cols) * depth * size, rows * cols, false,
-                     lines(depth, size), tiles, 1);
+                     lines(depth, size), tiles, most_parts);
     if (c.tile == 128 && dtype != 0 && tiles(128, 128) <= 256) c.tile = 129;
     return c;
 }

@@ -272,6 +272,7 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int6
     }
     if (!pr.partial) return;
     float *to = pr.partial + (int64_t)blockIdx.x * 2 * width;
+    const bool only = gridDim.x == 1;  // then there is nothing to join
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         auto &own = k == 0 ? dw : db;
@@ -292,7 +293,17 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int6
         }
 #pragma unroll
         for (int i = 0; i < C; ++i)
-            if (ch.there(i)) store_vec(to + k * width + ch.at[i], own[i]);
+            if (ch.there(i)) {
+                W *out = (W *)(k == 0 ? pr.dweight : pr.dbias);
+                if (!only) {
+                    store_vec(to + k * width + ch.at[i], own[i]);
+                } else if (out) {
+                    W r[V];
+#pragma unroll
+                    for (int j = 0; j < V; ++j) r[j] = (W)own[i][j];
+                    store_vec(out + ch.at[i], r);
+                }
+            }
     }
 }
 
@@ -457,14 +468,16 @@ hipError_t backward_t(NormProblem pr, int64_t parts, hipStream_t s) {
             return launch(kernel, parts, 256, 0, s, pr, parts * (256 / NT));
         });
     }
-    if (e != hipSuccess || !sums) return e;
+    if (e != hipSuccess || !sums || (parts == 1 && how_held<T>(pr.rows, pr.width) != kLong)) return e;
     return launch(norm_join_kernel<W>, cdiv(2 * pr.width, 64), 1024, 0, s, pr, parts);
 }
 
 template <typename T>
 int64_t parts_of(int64_t rows, int64_t width) {
     const int how = how_held<T>(rows, width);
-    const int64_t most = how == kLong ? cdiv(rows, 16) : how == kWave ? cdiv(rows, 4) : rows;
+    // A few rows in one block save the launch that joins the parts: 12 x 56 bf16 4.8 us against
+    // 3.8 + 2.0; but 64 x 512 13.7 against 4.0 + 3.7.
+    const int64_t most = how == kLong ? cdiv(rows, 16) : how == kWave ? cdiv(rows, rows <= 16 ? 16 : 4) : rows;
     const int64_t parts = how == kLong ? 64 : kParts;
     return most < 1 ? 1 : most < parts ? most : parts;
 }

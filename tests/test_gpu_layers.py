@@ -386,7 +386,8 @@ def check_entropy(dtype, rows, classes, width, skip=0.0, lse_grad=False, scale=1
 @pytest.mark.parametrize("rows,classes,width,skip", [
     (1, 1, 1, 0), (1, 5, 7, 0), (3, 64, 64, 0.5), (16, 1000, 129, 0.2), (65, 257, 40, 0), (100, 3000, 72, 0.1),
     (300, 513, 1001, 0.3), (1000, 1111, 777, 0.1), (2, 20000, 64, 0), (16, 70001, 96, 0.1), (513, 130, 2048, 0),
-    (2100, 2304, 256, 0.05), (5000, 7, 24, 0.1), (40, 900, 33, 2.0), (128, 4096, 3000, 0)])
+    (2100, 2304, 256, 0.05), (5000, 7, 24, 0.1), (40, 900, 33, 2.0), (128, 4096, 3000, 0), (658, 119, 2944, 0.1),
+    (100, 33, 4097, 0.1), (1100, 17, 2050, 0.1), (203, 24640, 192, 0), (33, 8191, 520, 0)])
 def test_cross_entropy(dtype, rows, classes, width, skip):
     check_entropy(dtype, rows, classes, width, skip, lse_grad=rows % 2 == 0, views=rows in (16, 65, 1000))
 
