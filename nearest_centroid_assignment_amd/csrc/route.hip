@@ -13,14 +13,15 @@
 //   kWide    float32 logits: a double 1.mantissa of the float's 32 bits, put in an order that
 //            integers have, and the complement of the expert's number.
 //   kNarrow  16-bit logits leave 13 bits of a float32 empty, which hold that complement.
-//   kScored  c is a float32 sum of roundings: 27 bits of it as an integer, of the largest |c|,
-//            and 4 for the place in the lane (26 and 5 with 32 keys). Where two choices that
-//            follow each other, or two groups at the border, lie within the roundings of each
-//            other, float64 tells: for choices each lane computes its own again and the lanes
-//            sort them (of 65536 tokens, 8 of 256 experts: 0.6 % of the waves), for groups
-//            the token's wave chooses again.
+//   kScored  c is a float32 sum of roundings: 23 bits of it as an integer, of the largest |c|,
+//            and 8 for the lane and the place in it (with 64 lanes 20 or 21, and 10 or 11), so
+//            that no two are the same. Where two choices that follow each other, or two groups
+//            at the border, lie within the roundings of each other, float64 tells: for choices
+//            each lane computes its own again and the lanes sort them (at the size below in
+//            0.3 to 1.2 % of the waves, by the logits' spread), for groups the token's wave
+//            chooses again.
 // 65536 tokens, 8 of 256 from 4 of 8 groups, sigmoids and a bias, bf16: with wide keys for
-// everything 58 us and 1550 vector instructions a wave of four tokens, so 38 and 1000.
+// everything 58 us and 1550 vector instructions a wave of four tokens, so 37 and 900.
 #include "layers.h"
 #include "rows.h"
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ double key_min(double a, double b) {
 __device__ __forceinline__ int key_max(int a, int b) { return a > b ? a : b; }
 __device__ __forceinline__ int key_min(int a, int b) { return a < b ? a : b; }
 
-template <int K, int V>
+template <int K, int L, int V>
 struct Key {  // kNarrow
     typedef int type;
     static constexpr int kMask = (1 << 13) - 1;
@@ -66,22 +67,24 @@ struct Key {  // kNarrow
     static __device__ __forceinline__ bool live(int k) { return k > kNone; }
     static __device__ __forceinline__ int number(int k) { return kMask - (k & kMask); }
 };
-template <int V>
-struct Key<kScored, V> {
+template <int L, int V>
+struct Key<kScored, L, V> {
     typedef int type;
-    static constexpr int kBits = V <= 16 ? 4 : 5;
-    static constexpr int kMask = (1 << kBits) - 1;
+    static constexpr int kPlace = V <= 16 ? 4 : 5, kBits = kPlace + (L == 16 ? 4 : 6);
     static constexpr int kEmpty = INT32_MIN;
-    // c times the power of two that leaves it below 2^(30 - kBits) in magnitude, or -inf.
-    static __device__ __forceinline__ int of(float c, int, int place) {
-        return (int)((uint32_t)(int)fmaxf(c, -(float)(1 << (31 - kBits))) << kBits) | place;
+    // c times the power of two that leaves it below 2^(30 - kBits) in magnitude, or an
+    // infinity. `at`: the lane, and the place in it.
+    static __device__ __forceinline__ int of(float c, int, int at) {
+        const float held = __builtin_amdgcn_fmed3f(c, -(float)(1 << (31 - kBits)), (float)(1 << (30 - kBits)));
+        return (int)((uint32_t)(int)held << kBits) | at;
     }
     static __device__ __forceinline__ bool live(int k) { return k >= -(1 << 30); }
-    static __device__ __forceinline__ int place(int k) { return k & kMask; }
+    static __device__ __forceinline__ int place(int k) { return k & ((1 << kPlace) - 1); }
+    static __device__ __forceinline__ int lane(int k) { return (k >> kPlace) & (L - 1); }
     static __device__ __forceinline__ int choice(int k) { return k >> kBits; }
 };
-template <int V>
-struct Key<kWide, V> {
+template <int L, int V>
+struct Key<kWide, L, V> {
     typedef double type;
     static constexpr double kEmpty = 0.0;
     static __device__ __forceinline__ double of(float c, int expert, int) {
@@ -234,7 +237,7 @@ __device__ __forceinline__ bool group_kept(F first, F second, int groups, int ke
     int before = 0;
     if constexpr (L == 16 && sizeof(F) == 4) {
         // (A group's lanes hold the same key.)
-        const double key = Key<kWide, 1>::of(rank + 0.0f, group, 0);
+        const double key = Key<kWide, 16, 1>::of(rank + 0.0f, group, 0);
         if (lanes == 2)
             before = 2 * count_before<2>(key);
         else if (lanes == 4)
@@ -370,33 +373,26 @@ __device__ __forceinline__ int resolve(const float (&z)[V], const RouteProblem &
     return mine;
 }
 
-// The `top` largest keys of the lanes that `keep` theirs, one after another: the t-th in lane t, and in kScored the lane that
-// had it. `twice`: whether two lanes had the same one. D keys of a lane can come up.
-template <int L, int K, int D, typename Keys>
-__device__ __forceinline__ void take(Keys &key, bool keep, int top, typename Keys::type &won, int &from,
-                                     bool &twice) {
+// The `top` largest keys of the lanes that `keep` theirs, one after another: the t-th in lane
+// t. D keys of a lane can come up.
+template <int L, int D, typename Keys>
+__device__ __forceinline__ void take(Keys &key, bool keep, int top, typename Keys::type &won) {
     const int own = threadIdx.x & (L - 1);
     sort_keys(key.k);
     key.k[0] = keep ? key.k[0] : Keys::kEmpty;
     for (int i = 0; i < top; ++i) {
         const auto best = lanes_most<L>(key.k[0]);
         const bool had = keep & (key.k[0] == best);
-        if constexpr (K == kScored) {
-            const uint64_t all = __ballot(had);
-            const uint64_t lanes = L == 64 ? all : (all >> (threadIdx.x & 48)) & 0xffff;
-            twice |= (lanes & (lanes - 1)) != 0 && key.live(best);
-            from = own == i ? __ffsll((unsigned long long)lanes) - 1 : from;
-        }
 #pragma unroll
         for (int j = 0; j + 1 < D; ++j) key.k[j] = had ? key.k[j + 1] : key.k[j];
         if (D == Keys::kCount) key.k[D - 1] = had ? Keys::kEmpty : key.k[D - 1];
         won = own == i ? best : won;
     }
 }
-template <int K, int V>
-struct Keys : Key<K, V> {
+template <int K, int L, int V>
+struct Keys : Key<K, L, V> {
     static constexpr int kCount = V;
-    typename Key<K, V>::type k[V];
+    typename Key<K, L, V>::type k[V];
 };
 
 // The choice for the token of the L lanes, and its weights.
@@ -426,6 +422,7 @@ __device__ __forceinline__ void route_token(const RouteProblem &pr, const Layout
     float most = 0.0f;  // the largest |c|
     if (K == kScored) {
         const float each = 1.0f / total;
+        const bool sound = total == total;
         if (pr.sigmoid) {
 #pragma unroll
             for (int j = 0; j < V; ++j) c[j] = sigmoid(z[j]);
@@ -438,7 +435,10 @@ __device__ __forceinline__ void route_token(const RouteProblem &pr, const Layout
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             most = fmaxf(most, fabsf(c[j]));
-            c[j] = ((z[j] > -INFINITY) & (c[j] == c[j])) ? c[j] : -INFINITY;  // not a NaN
+            // A NaN, or -inf. (The bias holds no NaN, and the sum none but for a NaN or an
+            // infinite logit, which leave a softmax nothing to choose by.)
+            const bool out = __builtin_amdgcn_classf(z[j], 0x007);
+            c[j] = (out | !sound) ? -INFINITY : c[j];
         }
         most = lanes_max<L>(most);
         if (most == INFINITY) {  // a bias that takes experts out: of the others
@@ -468,24 +468,23 @@ __device__ __forceinline__ void route_token(const RouteProblem &pr, const Layout
     float unit = 1.0f;  // the power of two that makes integers of c
     if constexpr (K == kScored) {
         const int e = __builtin_amdgcn_frexp_expf(most);
-        const int up = 30 - Key<K, V>::kBits - e;
+        const int up = 30 - Key<K, L, V>::kBits - e;
         unit = ldexpf(1.0f, up < 120 ? up : 120);
     }
-    Keys<K, V> key;
+    Keys<K, L, V> key;
 #pragma unroll
-    for (int j = 0; j < V; ++j) key.k[j] = key.of(K == kScored ? c[j] * unit : c[j], l.first + j, j);
-    typename Key<K, V>::type best = Keys<K, V>::kEmpty;
-    int from = 0;
+    for (int j = 0; j < V; ++j) key.k[j] = key.of(K == kScored ? c[j] * unit : c[j], l.first + j, own * (V <= 16 ? 16 : 32) + j);
+    typename Key<K, L, V>::type best = Keys<K, L, V>::kEmpty;
     // One more than is returned, where choices may have to be told apart. Of a lane's keys
     // only as many can come up as are asked for, and the one after them.
     const int asked = K == kScored && pr.top < L ? pr.top + 1 : pr.top;
     if (V > 10 && asked <= 9)
-        take<L, K, V < 10 ? V : 10>(key, keep, asked, best, from, again);
+        take<L, V < 10 ? V : 10>(key, keep, asked, best);
     else
-        take<L, K, V>(key, keep, asked, best, from, again);
+        take<L, V>(key, keep, asked, best);
     int mine = -1;
     if constexpr (K == kScored) {
-        const int first = __shfl(l.first, (threadIdx.x & 63 & ~(L - 1)) + from);
+        const int first = __shfl(l.first, (threadIdx.x & 63 & ~(L - 1)) + key.lane(best));
         if (own < asked && key.live(best)) mine = first + key.place(best);
         // Does any of them come near the one after it? (In units of the keys' choices, to
         // which each is cut off.)
@@ -537,6 +536,8 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem pr) {
 #pragma unroll
         for (int j = 0; j < V; ++j) bias[j] = 0.0f;
         if (pr.bias) load_own<float, V>(pr.bias, l, 0.0f, bias);
+#pragma unroll
+        for (int j = 0; j < V; ++j) bias[j] = bias[j] == bias[j] ? bias[j] : -INFINITY;
     }
     int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
     const bool there = t < pr.tokens;

@@ -317,6 +317,22 @@ def test_route_extremes():
     assert layers.route(z, 4, bias=bias)[0].tolist() == [[0, 3, -1, -1]]
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_infinite_bias(score):
+    """A bias of +inf takes its experts first, one of -inf takes them out, in any groups."""
+    z = randn(77, 50, 40)
+    bias = 0.1 * randn(78, 40)
+    bias[[7, 23]], bias[[2, 30, 31]] = math.inf, -math.inf
+    for groups, kept, best in ((1, 1, 1), (4, 2, 1), (4, 2, 2)):
+        ids, w = layers.route(z, 5, score=score, bias=bias, groups=groups, top_groups=kept, group_best=best)
+        assert (ids[:, :2] == torch.tensor([7, 23], device="cuda")).all() and w.isfinite().all()
+        s = (torch.softmax(z.double(), 1) if score == "softmax" else torch.sigmoid(z.double())) + bias.double()
+        if groups > 1:  # those of 7 and 23
+            s[:, 10:20], s[:, 30:] = -math.inf, -math.inf
+        s[:, [7, 23]] = -math.inf
+        assert (ids[:, 2:] == s.topk(3, 1).indices).all()
+
+
 # ----------------------------------------------------------- cross entropy
 
 
