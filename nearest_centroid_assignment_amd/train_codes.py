@@ -1,0 +1,136 @@
+"""Train a model of cluster codes, end to end on the GPU:
+
+    python -m nearest_centroid_assignment_amd.train_codes [--steps 200] [--bits 8]
+
+The data are walks over Gaussian blobs (``datagen``): which blob comes next depends on the
+one before. ``kmeans_fit`` finds the centroids, ``assign`` makes codes of the samples, and the
+model learns to tell the next code from the present one. One step:
+
+    embed -> layer_norm -> linear (router) -> route -> plan -> dispatch -> linear (silu)
+    -> linear -> combine -> added to the embedding -> layer_norm -> cross_entropy
+    the gradients of each, in the other direction -> adamw_step
+
+The experts are chosen by sigmoid scores under a bias that is moved after every step
+towards equal loads, as ``plan``'s offsets count them. The loss is compared at the end with
+the entropy of the walk itself.
+"""
+from __future__ import annotations
+
+import argparse
+import math
+
+import torch
+
+from . import binding, datagen, experts, layers
+
+SCORE = dict(score="sigmoid", renormalize=True)
+NAMES = ("table", "norm1", "shift1", "router", "w1", "b1", "w2", "b2", "norm2", "shift2", "head")
+
+
+class Model:
+    """float32 masters, the bfloat16 copies that the operators read, AdamW's moments and
+    the experts' bias."""
+
+    def __init__(self, classes, count, width, hidden, bits, gen):
+        def draw(*shape, scale):
+            return torch.randn(shape, generator=gen, device="cuda") * scale
+
+        one, zero = (lambda: torch.ones(width, device="cuda")), (lambda *s: torch.zeros(s, device="cuda"))
+        self.masters = [draw(classes, width, scale=1.0), one(), zero(width),
+                        draw(count, width, scale=width ** -0.5),
+                        draw(count, hidden, width, scale=width ** -0.5), zero(count, hidden),
+                        draw(count, width, hidden, scale=hidden ** -0.5), zero(count, width), one(), zero(width),
+                        draw(classes, width, scale=width ** -0.5)]
+        self.copies = [p.to(torch.bfloat16) for p in self.masters]
+        self.balance = torch.zeros(count, device="cuda")
+        self.state = experts.adamw_state(self.masters, bits)
+        self.step = 0
+
+    def update(self, grads, offsets, lr, rate=1e-3, clip=1.0):
+        norm = torch.stack(torch._foreach_norm(grads)).norm()
+        scale = (clip / (norm + 1e-6)).clamp(max=1.0).reshape(1).float()
+        self.step += 1
+        experts.adamw_step(self.masters, grads, lr=lr, betas=(0.9, 0.99), weight_decay=0.01,
+                           step=self.step, copies=self.copies, grad_scale=scale, **self.state)
+        load = offsets.diff().float()
+        self.balance += rate * torch.sign(load.mean() - load)
+
+
+def forward(model, codes, targets, top=2):
+    """(loss (tokens,), what the gradients need)."""
+    table, n1, s1, router, w1, b1, w2, b2, n2, s2, head = model.copies
+    e = layers.embed(codes, table)
+    y, *stats1 = layers.layer_norm(e, n1, s1, save_stats=True)
+    logits = experts.linear(y, router)
+    ids, weights = layers.route(logits, top, bias=model.balance, **SCORE)
+    plan = experts.plan(ids, router.shape[0])
+    xs = experts.dispatch(y, plan)
+    hidden, pre = experts.linear(xs, w1, b1, act="silu", offsets=plan.offsets, save_pre=True)
+    ys = experts.linear(hidden, w2, b2, offsets=plan.offsets)
+    h = e + experts.combine(ys, weights, plan)
+    out, *stats2 = layers.layer_norm(h, n2, s2, save_stats=True)
+    loss, lse = layers.cross_entropy(out, head, targets)
+    return loss, (codes, targets, e, y, stats1, logits, ids, weights, plan, xs, hidden, pre, ys, h, out, stats2, lse)
+
+
+def backward(model, dloss, saved):
+    """Gradients of the parameters for dloss (tokens,)."""
+    codes, targets, e, y, stats1, logits, ids, weights, plan, xs, hidden, pre, ys, h, out, stats2, lse = saved
+    table, n1, _, router, w1, _, w2, _, n2, _, head = model.copies
+    dout, dhead = layers.cross_entropy_backward(dloss, out, head, targets, lse)
+    dh, dn2, ds2 = layers.layer_norm_backward(dout, h, n2, *stats2)
+    dys, dweights = experts.combine_backward(dh, ys, weights, plan)
+    dz, dw2, db2 = experts.linear_backward(dys, hidden, w2, offsets=plan.offsets, in_pre=pre, in_act="silu")
+    dxs, dw1, db1 = experts.linear_backward(dz, xs, w1, offsets=plan.offsets)
+    dlogits = layers.route_backward(dweights, logits, ids, **SCORE)
+    dy, drouter, _ = experts.linear_backward(dlogits, y, router, need_dbias=False)
+    dy += experts.dispatch_backward(dxs, plan)
+    de, dn1, ds1 = layers.layer_norm_backward(dy, e, n1, *stats1)
+    dtable = layers.embed_backward(dh + de, codes, table.shape[0])
+    return [dtable, dn1, ds1, drouter, dw1, db1, dw2, db2, dn2, ds2, dhead]
+
+
+def train(steps=200, samples=16384, width=128, hidden=256, clusters=64, count=8, batch=4096, bits=32, lr=3e-3,
+          seed=0, log=print):
+    """Returns (first loss, last loss, entropy of the walk)."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    X, C0 = datagen.make_blobs(samples, clusters, 64, kb=clusters, sigma_c=1.0, sigma=0.25, seed=seed)
+    X, C0 = torch.from_numpy(X).cuda(), torch.from_numpy(C0).cuda()
+    fit = binding.fit(X, C0, max_iter=20, tol=1e-3)
+    codes, _ = binding.assign(X, fit["centres"], min_dist=False)
+    log(f"{clusters} centroids in {fit['n_iter']} iterations, inertia {fit['inertia']:.4g}")
+    # The walk: from each code to every other with its own frequencies; a sample of each code.
+    ways = torch.softmax(2.5 * torch.randn(clusters, clusters, generator=gen, device="cuda"), 1)
+    entropy = -(ways * ways.log()).sum(1).mean()
+    model = Model(clusters, count, width, hidden, bits, gen)
+    losses = []
+    for step in range(steps):
+        now = codes[torch.randint(samples, (batch,), generator=gen, device="cuda")]
+        after = torch.multinomial(ways[now], 1, generator=gen)[:, 0]
+        loss, saved = forward(model, now, after)
+        losses.append(loss.mean())
+        grads = backward(model, torch.full((batch,), 1.0 / batch, device="cuda"), saved)
+        model.update(grads, saved[8].offsets, lr)
+        if step % 50 == 0 or step == steps - 1:
+            log(f"step {step}: loss {float(losses[-1]):.4f}")
+    return float(losses[0]), float(torch.stack(losses[-5:]).mean()), float(entropy)
+
+
+def main(argv=None):
+    ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
+    ap.add_argument("--steps", type=int, default=200)
+    ap.add_argument("--batch", type=int, default=4096)
+    ap.add_argument("--clusters", type=int, default=64)
+    ap.add_argument("--experts", type=int, default=8)
+    ap.add_argument("--width", type=int, default=128)
+    ap.add_argument("--hidden", type=int, default=256)
+    ap.add_argument("--bits", type=int, choices=(8, 32), default=32)
+    ap.add_argument("--seed", type=int, default=0)
+    a = ap.parse_args(argv)
+    first, last, walk = train(steps=a.steps, batch=a.batch, clusters=a.clusters, count=a.experts, width=a.width,
+                              hidden=a.hidden, bits=a.bits, seed=a.seed)
+    print(f"loss {first:.4f} -> {last:.4f}; log of the codes {math.log(a.clusters):.4f}, entropy of the walk {walk:.4f}")
+
+
+if __name__ == "__main__":
+    main()
