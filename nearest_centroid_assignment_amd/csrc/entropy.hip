@@ -249,6 +249,8 @@ hipError_t join_parts(const float *partial, int splits, int64_t rows, int64_t co
 template <typename T>
 hipError_t grad_t(const EntropyGrad &g, hipStream_t s) {
     hipError_t e = hipSuccess;
+    if (g.rows == 0)  // a sum of no parts
+        return join_parts<T>(nullptr, 0, g.count, g.width, nullptr, true, true, nullptr, g.dw, g.width, s);
     if (g.together) return launch_entropy_both_t<T>(g, s);
     if (g.dx) {
         e = launch_entropy_dx_t<T>(g, s);

@@ -468,9 +468,10 @@ int layers_cross_entropy_backward(const float *dloss, const float *dlse, const v
     if (rows == 0 && !dw) return KM_OK;
     const hipStream_t s = (hipStream_t)stream;
     char *base = ws_base(workspace);
-    const Operand xq = operand(x, ldx, rows, width, dtype, base + L.x, s);
+    Operand xq = {x, ldx, width, hipSuccess}, wp = {w, width, width, hipSuccess};
+    if (rows > 0) xq = operand(x, ldx, rows, width, dtype, base + L.x, s);  // (else w may be NULL)
     if (xq.e != hipSuccess) return KM_ERR_HIP;
-    const Operand wp = operand(w, width, classes, width, dtype, base + L.w, s);
+    if (rows > 0) wp = operand(w, width, classes, width, dtype, base + L.w, s);
     if (wp.e != hipSuccess) return KM_ERR_HIP;
     kx::EntropyProblem pr = {};
     pr.x = xq.p;

@@ -52,7 +52,8 @@ def strided(t, extra=3, shift=1):
 @pytest.mark.parametrize("tokens,classes,width,skip,hot", [
     (0, 5, 8, 0, 0), (1, 1, 1, 0, 0), (3, 7, 5, 0.5, 0), (8, 300, 2048, 0, 0), (100, 17, 1001, 0.2, 0),
     (5000, 33, 64, 0, 0.3), (1000, 1, 24, 0.1, 0), (4097, 3000, 40, 0.1, 0.5), (2100, 2048, 33, 0, 0),
-    (70000, 50000, 24, 0.05, 0.2), (20000, 2049, 130, 0, 0.9), (300, 5000, 8, 2.0, 0), (40, 9, 9000, 0.1, 0.5)])
+    (70000, 50000, 24, 0.05, 0.2), (20000, 2049, 130, 0, 0.9), (300, 5000, 8, 2.0, 0), (40, 9, 9000, 0.1, 0.5),
+    (8192, 2048, 16, 0.1, 0.1), (8193, 2048, 16, 0.1, 0.1), (30000, 700, 24, 0.1, 0.3), (1025, 200, 16, 0, 0.5)])
 def test_embed(dtype, tokens, classes, width, skip, hot):
     """The products with the scale are rounded once in float32 and once to the type; a
     gradient sums up to as many rows as a number comes up, and is scaled once."""
@@ -422,6 +423,9 @@ def test_cross_entropy_no_rows():
     assert loss.shape == lse.shape == (0,)
     dx, dw = layers.cross_entropy_backward(loss, x, w, none, lse)
     assert dx.shape == (0, 24) and dw.shape == w.shape and (dw == 0).all()
+    x, w = x[:, :23].bfloat16(), w[:, :23].bfloat16()  # of rows that a product would copy
+    dx, dw = layers.cross_entropy_backward(loss, x, w.contiguous(), none, lse)
+    assert dx.shape == (0, 23) and dw.shape == w.shape and (dw == 0).all()
 
 
 def test_cross_entropy_large_logits():
