@@ -5,10 +5,10 @@
 //   dweight = sum over rows of dy h,  dbias = sum over rows of dy
 //
 // Bound by memory: x is read and y written once; the gradient reads x and dy and
-// writes dx once. A row lives in the registers of a wave or of a block, so that the
+// writes dx once. A row lives in the registers of a few lanes, a wave or a block, so that the
 // variance is the mean square of what is left after the mean is taken off (two passes
 // over registers: no cancellation), and the columns' sums of the gradient stay in
-// registers over all rows that a wave or block takes; the blocks' sums are added in order
+// registers over all rows that they take; the blocks' sums are added in order
 // by a second kernel. Rows that no registers hold are read again from the caches.
 #include "layers.h"
 #include "rows.h"
@@ -16,22 +16,44 @@
 namespace kx {
 namespace {
 
+// A row's threads: 16 or 32 lanes, a wave, or a block of 128, 256 or 512.
+template <int NT>
+constexpr int kThreads = NT > 64 ? NT : 256;
+template <int NT>
+constexpr int kRowWaves = NT > 64 ? NT / 64 : 1;
+template <int NT>
+__device__ __forceinline__ int64_t own_row() {
+    if (NT > 64) return blockIdx.x;
+    return NT < 64 ? (int64_t)blockIdx.x * (256 / NT) + threadIdx.x / NT : own_token<NT>();
+}
+
 // Sum of each of v over the NT threads of a row, in a fixed order, to all of them.
 // `turn`: two calls in a row use the two halves of the memory, so one barrier is enough.
 template <int NT, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[4][N], int turn) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*part)[kRowWaves<NT>][N], int turn) {
 #pragma unroll
-    for (int d = 32; d >= 1; d >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d);
-    if (NT == 256) {
+    for (int i = 0; i < N; ++i) {
+        v[i] += rotated<0x128>(v[i]);
+        v[i] += rotated<0x124>(v[i]);
+        v[i] += rotated<0x122>(v[i]);
+        v[i] += rotated<0x121>(v[i]);
+        if (NT > 16) v[i] += __shfl_xor(v[i], 16);
+        if (NT > 32) v[i] += __shfl_xor(v[i], 32);
+    }
+    if constexpr (NT > 64) {
         float(*p)[N] = part[turn & 1];
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
             for (int i = 0; i < N; ++i) p[threadIdx.x >> 6][i] = v[i];
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = (p[0][i] + p[1][i]) + (p[2][i] + p[3][i]);
+        for (int i = 0; i < N; ++i) {
+            v[i] = p[0][i] + p[1][i];
+            if (NT > 128) v[i] += p[2][i] + p[3][i];
+#pragma unroll
+            for (int w = 4; w < kRowWaves<NT>; w += 4)
+                v[i] += (p[w][i] + p[w + 1][i]) + (p[w + 2][i] + p[w + 3][i]);
+        }
     }
 }
 
@@ -84,13 +106,13 @@ __device__ __forceinline__ void store_chunk(T *p, const T (&v)[V]) {
         store_vec(p, v);
 }
 
-// Every `step`-th row a wave (NT = 64) or block, the next one on its way meanwhile. ONCE:
+// Every `step`-th row a few lanes, a wave or a block, the next one on its way meanwhile. ONCE:
 // rows that no cache holds pass the caches by (see once_of).
 template <typename T, typename W, int NT, int C, bool ONCE, bool EVEN>
-__global__ __launch_bounds__(256) void norm_kernel(NormProblem pr, int64_t step) {
+__global__ __launch_bounds__(kThreads<NT>) void norm_kernel(NormProblem pr, int64_t step) {
     constexpr int V = vec<T>();
-    __shared__ float part[2][4][1];
-    int64_t r = own_token<NT>();
+    __shared__ float part[2][kRowWaves<NT>][1];
+    int64_t r = own_row<NT>();
     if (r >= pr.rows) return;
     const int64_t width = pr.width;
     Chunks<V, C, NT, EVEN> ch;
@@ -197,14 +219,13 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormProblem pr) {
     }
 }
 
-// dx, and the columns' sums over the rows that the wave (NT = 64) or block takes: every
+// dx, and the columns' sums over the rows that the lanes, the wave or the block take: every
 // `step`-th. A block leaves one part of the sums.
 template <typename T, typename W, int NT, int C, bool ONCE, bool EVEN>
-__global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int64_t step) {
+__global__ __launch_bounds__(kThreads<NT>) void norm_backward_kernel(NormProblem pr, int64_t step) {
     constexpr int V = vec<T>();
-    constexpr int kRows = 256 / NT;
-    __shared__ float part[2][4][2];
-    __shared__ float columns[NT == 64 ? C * 64 * V : 1];
+    __shared__ float part[2][kRowWaves<NT>][2];
+    __shared__ float columns[NT <= 64 ? C * 64 * V : 1];
     const int64_t width = pr.width;
     Chunks<V, C, NT, EVEN> ch;
     ch.init(width);
@@ -222,7 +243,7 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int6
     }
     const float each = 1.0f / (float)width;
     int turn = 0;
-    int64_t r = own_token<NT>();
+    int64_t r = own_row<NT>();
     T nv[C][V], nd[C][V];
     float mean_of_next = 0.0f, rstd_of_next = 0.0f;
     auto fetch = [&](int64_t r) {
@@ -276,8 +297,17 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int6
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         auto &own = k == 0 ? dw : db;
-        if (NT == 64) {  // the four waves' sums, one after another
-            for (int q = 0; q < kRows; ++q) {
+        if (NT < 64) {  // the wave's rows
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    if (NT == 16) own[i][j] += __shfl_xor(own[i][j], 16);
+                    own[i][j] += __shfl_xor(own[i][j], 32);
+                }
+        }
+        if (NT <= 64) {  // the four waves' sums, one after another
+            for (int q = 0; q < 4; ++q) {
                 __syncthreads();
                 if ((int)(threadIdx.x >> 6) != q) continue;
 #pragma unroll
@@ -286,10 +316,10 @@ __global__ __launch_bounds__(256) void norm_backward_kernel(NormProblem pr, int6
                     for (int j = 0; j < V; ++j) {
                         const int at = (i * V + j) * 64 + (threadIdx.x & 63);
                         if (q > 0) own[i][j] += columns[at];
-                        if (q < kRows - 1) columns[at] = own[i][j];
+                        if (q < 3) columns[at] = own[i][j];
                     }
             }
-            if (threadIdx.x < 192) continue;
+            if (threadIdx.x < 192 || threadIdx.x >= 192 + NT) continue;
         }
 #pragma unroll
         for (int i = 0; i < C; ++i)
@@ -399,15 +429,23 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormProblem pr, int64_t
     if (to) to[i < pr.width ? i : i - pr.width] = (W)v;
 }
 
-// How rows are held: by a wave up to four chunks of 16 bytes a lane, by a block up to
-// four, else not (or of rows shorter than one access).
-enum { kWave, kBlock, kLong };
+// How rows are held, in chunks of 16 bytes a thread: by 16 lanes up to two, by 32 up to four (a
+// quarter of them idle), by a wave up to four, by two waves up to four where a block of 256 would
+// leave more idle, by a block of 256 or 512 up to four; else not (nor are rows shorter than
+// one access). The fewer threads, the more rows share a reduction; few rows want more threads.
+// bf16, forward and backward, us: 262144 x 64 by a wave 86 and 113, by 16 lanes 24 and 28; 65536 x
+// 257 by a wave 31 and 39, by 32 lanes 25 and 31, x 520 47 and 65, 36 and 57, but 16384 x 1001 18
+// and 26, 16 and 34; 16384 x 2051 by a block 48 and 73, by two waves 42 and 66 (1100 rows: 7 and
+// 16, 6 and 21). float32: 16384 x 4097 not held 147 and 413, by 512 threads 116 and 165.
+enum { kLanes, kWave, kPair, kBlock, kWide, kLong };
 template <typename T>
 int how_held(int64_t rows, int64_t width) {
     const int64_t wave = 64 * vec<T>();
-    if (width < vec<T>()) return kLong;  // less than one access
+    if (width < vec<T>()) return kLong;
+    if (2 * width <= wave || (2 * width <= 3 * wave && rows >= 1024)) return kLanes;
     if (width <= 4 * wave && (rows >= 1024 || width <= wave)) return kWave;
-    return width <= 16 * wave ? kBlock : kLong;
+    if (width > 4 * wave && width <= 6 * wave && rows >= 4096) return kPair;
+    return width <= 16 * wave ? kBlock : width <= 32 * wave ? kWide : kLong;
 }
 constexpr int64_t kParts = 512;
 constexpr int64_t kBlocks = 1024;
@@ -424,10 +462,17 @@ bool once_of(const NormProblem &pr, int64_t tensors) {
 template <typename T, class F>
 hipError_t by_size(int64_t rows, int64_t width, F f) {
     constexpr int V = vec<T>();
-    if (how_held<T>(rows, width) == kWave) {
+    const int how = how_held<T>(rows, width);
+    if (how == kLanes) {
+        if (width <= 16 * V) return f(ActTag<16>{}, ActTag<1>{});
+        if (width <= 32 * V) return f(ActTag<16>{}, ActTag<2>{});
+        return width <= 64 * V ? f(ActTag<32>{}, ActTag<2>{}) : f(ActTag<32>{}, ActTag<4>{});
+    }
+    if (how == kPair) return f(ActTag<128>{}, ActTag<4>{});
+    if (how == kWide) return f(ActTag<512>{}, ActTag<4>{});
+    if (how == kWave) {
         if (width <= 64 * V) return f(ActTag<64>{}, ActTag<1>{});
-        if (width <= 128 * V) return f(ActTag<64>{}, ActTag<2>{});
-        return f(ActTag<64>{}, ActTag<4>{});
+        return width <= 128 * V ? f(ActTag<64>{}, ActTag<2>{}) : f(ActTag<64>{}, ActTag<4>{});
     }
     if (width <= 256 * V) return f(ActTag<256>{}, ActTag<1>{});
     if (width <= 512 * V) return f(ActTag<256>{}, ActTag<2>{});
@@ -441,11 +486,13 @@ hipError_t norm_t(const NormProblem &pr, hipStream_t s) {
     return by_size<T>(pr.rows, pr.width, [&](auto nt, auto c) {
         constexpr int NT = decltype(nt)::value, C = decltype(c)::value;
         // As many blocks as run at once.
-        const int64_t all = cdiv(pr.rows, 256 / NT), blocks = all < kBlocks ? all : kBlocks;
+        constexpr int kRows = kThreads<NT> / NT;
+        const int64_t all = cdiv(pr.rows, kRows), most = NT == 128 ? 2 * kBlocks : kBlocks;
+        const int64_t blocks = all < most ? all : most;
         const auto kernel = pr.width % vec<T>()  ? norm_kernel<T, W, NT, C, false, false>
                             : once_of<T>(pr, 2) ? norm_kernel<T, W, NT, C, true, true>
                                                 : norm_kernel<T, W, NT, C, false, true>;
-        return launch(kernel, blocks, 256, 0, s, pr, blocks * (256 / NT));
+        return launch(kernel, blocks, kThreads<NT>, 0, s, pr, blocks * kRows);
     });
 }
 
@@ -465,7 +512,7 @@ hipError_t backward_t(NormProblem pr, int64_t parts, hipStream_t s) {
             const auto kernel = pr.width % vec<T>()  ? norm_backward_kernel<T, W, NT, C, false, false>
                                 : once_of<T>(pr, 3) ? norm_backward_kernel<T, W, NT, C, true, true>
                                                     : norm_backward_kernel<T, W, NT, C, false, true>;
-            return launch(kernel, parts, 256, 0, s, pr, parts * (256 / NT));
+            return launch(kernel, parts, kThreads<NT>, 0, s, pr, parts * (kThreads<NT> / NT));
         });
     }
     if (e != hipSuccess || !sums || (parts == 1 && how_held<T>(pr.rows, pr.width) != kLong)) return e;
@@ -477,8 +524,10 @@ int64_t parts_of(int64_t rows, int64_t width) {
     const int how = how_held<T>(rows, width);
     // A few rows in one block save the launch that joins the parts: 12 x 56 bf16 4.8 us against
     // 3.8 + 2.0; but 64 x 512 13.7 against 4.0 + 3.7.
-    const int64_t most = how == kLong ? cdiv(rows, 16) : how == kWave ? cdiv(rows, rows <= 16 ? 16 : 4) : rows;
-    const int64_t parts = how == kLong ? 64 : kParts;
+    const int64_t most = how == kLong || how == kLanes ? cdiv(rows, width <= 32 * vec<T>() ? 16 : 8)
+                         : how == kWave                ? cdiv(rows, rows <= 16 ? 16 : 4)
+                                                       : rows;
+    const int64_t parts = how == kLong ? 64 : how == kPair ? 2 * kParts : kParts;
     return most < 1 ? 1 : most < parts ? most : parts;
 }
 

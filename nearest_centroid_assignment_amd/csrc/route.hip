@@ -151,10 +151,6 @@ __device__ __forceinline__ double lanes_max(double x) {
     for (int d = L / 2; d >= 1; d >>= 1) x = fmax(x, __shfl_xor(x, d));
     return x;
 }
-template <int CTRL>
-__device__ __forceinline__ float rotated(float x) {
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
-}
 template <int L>
 __device__ __forceinline__ float lanes_max(float x) {
     x = fmaxf(x, rotated<0x128>(x));

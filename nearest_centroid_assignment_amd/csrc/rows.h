@@ -1,5 +1,5 @@
 // rows.h - device helpers of the kernels that give a wave or a block to a row
-// (tokens.hip, embed.hip, norm.hip).
+// (tokens.hip, embed.hip, norm.hip, route.hip).
 #pragma once
 
 #include "experts.h"
@@ -19,6 +19,11 @@ __device__ __forceinline__ void wave_rank(int expert, int bits, int &rank, int &
     }
     rank = expert < 0 ? 0 : __popcll(same & ((1ull << lane) - 1ull));
     count = expert < 0 ? 0 : __popcll(same);
+}
+// x of another of the 16 lanes (CTRL 0x120 + n: n places on).
+template <int CTRL>
+__device__ __forceinline__ float rotated(float x) {
+    return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(x), CTRL, 0xf, 0xf, true));
 }
 template <typename T>
 constexpr int vec() {

@@ -109,7 +109,9 @@ def test_embed_of_centroids():
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,width", [
     (0, 9), (1, 1), (3, 5), (1, 2048), (7, 64), (2000, 129), (1030, 512), (33, 1001), (1100, 2048),
-    (1500, 1025), (5, 4096), (70, 8192), (3, 8195), (2, 20000), (40, 17001), (4100, 24)])
+    (1500, 1025), (5, 4096), (70, 8192), (3, 8195), (2, 20000), (40, 17001), (4100, 24), (70, 128), (37, 130),
+    (2000, 256), (600, 16384), (1, 7000), (20000, 72), (4100, 2055),
+    (1030, 760), (500, 260)])
 def test_layer_norm(dtype, rows, width):
     """mean is a float32 sum; d = x - mean is off by what the mean is and one rounding; the
     variance (its sum's roundings, twice d's) enters h by half. With e the error of d
