@@ -54,63 +54,91 @@ __global__ __launch_bounds__(256) void bucket_kernel(const int64_t *__restrict__
     bucket[t] = id >= 0 && id < classes ? id & (kEmbedBuckets - 1) : -1;
 }
 
-// One block sorts one bucket's tokens by their number, stably: a count, a prefix over
-// the bucket's numbers (at most `locals`), and the tokens in rounds of 256.
-__global__ __launch_bounds__(256) void refine_kernel(const int64_t *__restrict__ ids,
-                                                     int64_t classes, const int *__restrict__ order,
-                                                     const int *__restrict__ offsets, int locals,
-                                                     int *__restrict__ sorted, int *__restrict__ lo,
-                                                     int *__restrict__ hi) {
-    extern __shared__ int base[];  // locals; then 4 x locals: counts of a round, by wave
-    int *count = base + locals;
-    const int tid = threadIdx.x, wave = tid >> 6;
+// The wave's accesses to LDS before this one, by any of its lanes, come before those after it.
+__device__ __forceinline__ void in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// One block sorts one bucket's tokens by their number, stably: each wave counts a run of them,
+// a prefix over the bucket's numbers (at most `locals`) and the waves, and each wave places its
+// run. (A frequent number's bucket holds a good part of all tokens, and no barrier is in its
+// way. us of the gradient of 64 columns, 65536 tokens of 50000 numbers, frequent as 1 / number,
+// and as often as each other: eight waves 59 and 46, sixteen 54 and 49; four in rounds of 256
+// tokens with three barriers each 75 and 45.)
+constexpr int kRefineWaves = 8;
+
+__global__ __launch_bounds__(kRefineWaves * 64) void refine_kernel(
+    const int64_t *__restrict__ ids, int64_t classes, const int *__restrict__ order,
+    const int *__restrict__ offsets, int locals, int *__restrict__ sorted, int *__restrict__ lo,
+    int *__restrict__ hi) {
+    constexpr int kAhead = 4;
+    extern __shared__ int count[];  // kRefineWaves x locals
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int b = blockIdx.x;
     const int first = offsets[b], members = offsets[b + 1] - first;
-    auto local = [&](int i) { return (int)(ids[order[first + i]] / kEmbedBuckets); };
-    for (int j = tid; j < 5 * locals; j += 256) base[j] = 0;
+    const int bits = 32 - __clz(locals);
+    const int run = (members + kRefineWaves * 64 - 1) / (kRefineWaves * 64) * 64;
+    const int from = wave * run, to = from + run < members ? from + run : members;
+    int *own = count + wave * locals;
+    for (int j = tid; j < kRefineWaves * locals; j += kRefineWaves * 64) count[j] = 0;
     __syncthreads();
-    for (int i = tid; i < members; i += 256) atomicAdd(&base[local(i)], 1);
+    // `place`: where they go; else they are counted.
+    auto sweep = [&](bool place) {
+        for (int r = from; r < to; r += kAhead * 64) {
+            int token[kAhead], l[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = r + u * 64 + lane;
+                token[u] = i < to ? order[first + i] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                l[u] = token[u] >= 0 ? (int)(ids[token[u]] / kEmbedBuckets) : -1;
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                if (r + u * 64 >= to) break;
+                int rank, same;
+                wave_rank(l[u], bits, rank, same);
+                in_order();
+                const int before = l[u] >= 0 ? own[l[u]] : 0;
+                in_order();
+                if (l[u] >= 0 && rank == 0) own[l[u]] = before + same;
+                if (place && l[u] >= 0) sorted[before + rank] = token[u];
+            }
+        }
+    };
+    sweep(false);
     __syncthreads();
     if (wave == 0) {
-        int run = first;
+        int start = first;
         for (int l0 = 0; l0 < locals; l0 += 64) {
-            const int l = l0 + tid;
-            const int n = l < locals ? base[l] : 0;
-            const int incl = wave_incl_scan(n);
-            const int at = run + incl - n;
+            const int l = l0 + lane;
+            int n[kRefineWaves], all = 0;
+#pragma unroll
+            for (int w = 0; w < kRefineWaves; ++w) {
+                n[w] = l < locals ? count[w * locals + l] : 0;
+                all += n[w];
+            }
+            const int incl = wave_incl_scan(all);
+            int at = start + incl - all;
             const int64_t v = (int64_t)l * kEmbedBuckets + b;
             if (l < locals) {
-                base[l] = at;
                 if (v < classes) {
                     lo[v] = at;
-                    hi[v] = at + n;
+                    hi[v] = at + all;
+                }
+#pragma unroll
+                for (int w = 0; w < kRefineWaves; ++w) {
+                    count[w * locals + l] = at;
+                    at += n[w];
                 }
             }
-            run += __builtin_amdgcn_readlane(incl, 63);
+            start += __builtin_amdgcn_readlane(incl, 63);
         }
     }
     __syncthreads();
-    const int bits = 32 - __clz(locals);
-    for (int r = 0; r < members; r += 256) {
-        const int i = r + tid;
-        const int token = i < members ? order[first + i] : -1;
-        const int l = token >= 0 ? local(i) : -1;
-        int rank, same;
-        wave_rank(l, bits, rank, same);
-        if (l >= 0 && rank == 0) count[wave * locals + l] = same;
-        __syncthreads();
-        if (l >= 0) {
-            int at = base[l] + rank;
-            for (int w = 0; w < wave; ++w) at += count[w * locals + l];
-            sorted[at] = token;
-        }
-        __syncthreads();
-        if (l >= 0 && rank == 0) {  // the order of these integer sums does not matter
-            atomicAdd(&base[l], same);
-            count[wave * locals + l] = 0;
-        }
-        __syncthreads();
-    }
+    sweep(true);
 }
 
 struct SumArgs {
@@ -285,7 +313,8 @@ hipError_t embed_t(const int64_t *ids, int64_t tokens, const void *w, int64_t cl
                   ids, tokens, (const T *)w, classes, width, scale, (T *)out, ldo);
 }
 
-// Threads and values a thread that a chunk's rows take: as many lanes busy as there are.
+// Threads and values a thread that a chunk's rows take: as many lanes busy as there are (65536 x 64
+// bf16 of 1000: by 8 values 59 us, by 2 36).
 template <typename T, class F>
 hipError_t with_rows(int64_t width, F f) {
     constexpr int V = vec<T>();
@@ -313,6 +342,9 @@ hipError_t backward_t(SumArgs a, int64_t tokens, const void *dy, void *dw, hipSt
 
 }  // namespace
 
+// Long chunks leave few parts to join, short ones more blocks. us of the gradient with chunks of
+// 16 / 32 / 64: 5000 x 777 float32 of 1111 27 / 28 / 34, 20000 x 1024 bf16 of 500 43 / 37 / 45,
+// 65536 x 2048 bf16 of 50000 185 / 166 / 158.
 int64_t embed_chunk(int64_t tokens) { return tokens >= 65536 ? kChunk : tokens >= 16384 ? kChunk / 2 : kChunk / 4; }
 
 bool embed_grid_ok(int dtype, int64_t tokens, int64_t classes, int64_t width) {
@@ -347,8 +379,9 @@ hipError_t launch_embed_backward(const void *dy, int64_t lddy, const int64_t *id
             e = launch_plan(ws.bucket, tokens, kEmbedBuckets, ws.order, ws.place, ws.offsets, ws.plan, s);
         const int locals = (int)cdiv(classes, kEmbedBuckets);
         if (e == hipSuccess)
-            e = launch(refine_kernel, kEmbedBuckets, 256, (size_t)5 * locals * sizeof(int), s, ids,
-                       classes, ws.order, ws.offsets, locals, ws.sorted, ws.lo, ws.hi);
+            e = launch(refine_kernel, kEmbedBuckets, kRefineWaves * 64,
+                       (size_t)kRefineWaves * locals * sizeof(int), s, ids, classes, ws.order,
+                       ws.offsets, locals, ws.sorted, ws.lo, ws.hi);
         a.total = ws.offsets + kEmbedBuckets;
         a.order = ws.sorted;
         a.lo = ws.lo;

@@ -13,7 +13,9 @@ hipError_t launch_embed(const int64_t *ids, int64_t tokens, const void *w, int d
                         hipStream_t s);
 
 // Classes up to this many are sorted by the plan; more of them first by their
-// number modulo kEmbedBuckets.
+// number modulo kEmbedBuckets. (us of the gradient, plan / buckets: 65536 x 512 bf16 of 2000 62 /
+// 100, of 500 x 128 33 / 86 before the buckets' sort had no barriers; 65536 x 64 of 2500 36 / 35,
+// frequent as 1 / number 44 / 56, of 10000 45 / 37 and 52 / 57, of 50000 94 / 46 and 96 / 59.)
 constexpr int64_t kEmbedDirect = 2048;
 constexpr int64_t kEmbedBuckets = 1024;
 struct EmbedScratch {
@@ -100,6 +102,8 @@ hipError_t launch_entropy_dz(int dtype, const EntropyProblem &pr, hipStream_t s)
 // The factor of a 16-bit dz and its inverse, where the rows are too many for every block of the
 // dz kernel to look at them.
 hipError_t launch_entropy_scale(const EntropyProblem &pr, hipStream_t s);
+// (dx and dw of 64 x 8192 x 512 bf16 21.5 us, with a launch for the scale 23.0; 2048 x 2048 x 512
+// 37.5 and 39; 8192 x 8192 x 512 253 and 240.)
 constexpr int64_t kOwnScale = 1024;  // rows
 
 // dx (first and last piece, sums between them) and dw of a piece.
