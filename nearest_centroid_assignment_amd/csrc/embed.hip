@@ -54,12 +54,6 @@ __global__ __launch_bounds__(256) void bucket_kernel(const int64_t *__restrict__
     bucket[t] = id >= 0 && id < classes ? id & (kEmbedBuckets - 1) : -1;
 }
 
-// The wave's accesses to LDS before this one, by any of its lanes, come before those after it.
-__device__ __forceinline__ void in_order() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // One block sorts one bucket's tokens by their number, stably: each wave counts a run of them,
 // a prefix over the bucket's numbers (at most `locals`) and the waves, and each wave places its
 // run. (A frequent number's bucket holds a good part of all tokens, and no barrier is in its

@@ -21,7 +21,7 @@
 //            0.3 to 1.2 % of the waves, by the logits' spread), for groups the token's wave
 //            chooses again.
 // 65536 tokens, 8 of 256 from 4 of 8 groups, sigmoids and a bias, bf16: with wide keys for
-// everything 58 us and 1550 vector instructions a wave of four tokens, so 37 and 900.
+// everything 58 us and 1550 vector instructions a wave of four tokens, so 36 to 38 and 950.
 #include "layers.h"
 #include "rows.h"
 
@@ -551,15 +551,22 @@ __global__ __launch_bounds__(256) void route_kernel(RouteProblem pr) {
 //   renormalised  dz = r (d - sum r d), for sigmoids times 1 - s
 //   sigmoid       dz = s (1 - s) d
 //   softmax       dz = p (d - sum p d), of the others -p sum p d
-// One row for L lanes: lane i has the i-th chosen, then every lane looks through the
-// chosen for its V of the row's places.
+// One row for L lanes: lane i has the i-th chosen and puts its dz into the row in LDS, which the
+// lanes then store, V places each. (65536 tokens, 8 of 256, bf16: 15.9 us, 4.6 TB/s with every logit's
+// line read; every lane looking through the chosen for its places 18.2, 630 vector
+// instructions a wave.)
 template <typename T, int L>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem pr) {
     constexpr int V = vec<T>();
+    extern __shared__ __align__(16) float rows[];  // 256 / L, each a whole number of V
+    float *sums = rows + threadIdx.x / L * ((pr.experts + V - 1) / V * V);
     const int own = threadIdx.x & (L - 1), base = threadIdx.x & 63 & ~(L - 1);
     int64_t t = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
     const bool there = t < pr.tokens;
     if (!there) t = pr.tokens - 1;
+    for (int c = own * V; c < pr.experts; c += L * V)
+#pragma unroll
+        for (int j = 0; j < V; ++j) sums[c + j] = 0.0f;
     const T *row = (const T *)pr.logits + t * pr.ld;
     int64_t id = own < pr.top ? pr.chosen[t * pr.top + own] : -1;
     const bool live = id >= 0 && id < pr.experts;
@@ -590,26 +597,35 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteProblem pr) {
         dz = p * d;
         inner = lanes_sum<L>(dz);
     }
-    if (!live) dz = 0.0f;
+    // Is one chosen twice? (Not by route.) Then its first lane adds them.
+    bool first = live;
+    in_order();
+    if (live) ((int *)sums)[at] = own;
+    in_order();
+    if (__any(live && ((int *)sums)[at] != own)) {
+        for (int i = 0; i < pr.top; ++i) {
+            const int e = __shfl(at, base + i);
+            const float v = __shfl(dz, base + i);
+            if (live && e == at && i < own) first = false;
+            if (live && e == at && i > own) dz += v;
+        }
+    }
+    in_order();
+    if (first) sums[at] = dz;
+    in_order();
     T *out = (T *)pr.dlogits + t * pr.lddl;
     for (int c0 = 0; c0 < pr.experts; c0 += L * V) {
         const int c = c0 + own * V;
         float g[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) g[j] = 0.0f;
+        for (int j = 0; j < V; ++j) g[j] = c < pr.experts ? sums[c + j] : 0.0f;
         if (dense) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 if (c + j >= pr.experts) continue;
                 const float z = (float)row[c + j];
-                if (z > -INFINITY) g[j] = -inner * (exp_of(z - top) / total);
+                if (z > -INFINITY) g[j] -= inner * (exp_of(z - top) / total);
             }
-        }
-        for (int i = 0; i < pr.top; ++i) {
-            const int e = __shfl(at, base + i) - c;
-            const float v = __shfl(dz, base + i);
-#pragma unroll
-            for (int j = 0; j < V; ++j) g[j] += e == j ? v : 0.0f;
         }
         if (there && c < pr.experts) store_row(out + c, g, pr.experts - c);
     }
@@ -650,9 +666,10 @@ hipError_t route_t(const RouteProblem &pr, hipStream_t s) {
 }
 template <typename T>
 hipError_t backward_t(const RouteProblem &pr, hipStream_t s) {
+    const size_t row = (size_t)cdiv(pr.experts, vec<T>()) * vec<T>() * sizeof(float);  // at most 8 KB
     if (pr.top <= 16 && pr.experts <= 16 * 2 * vec<T>())
-        return launch(route_backward_kernel<T, 16>, cdiv(pr.tokens, 16), 256, 0, s, pr);
-    return launch(route_backward_kernel<T, 64>, cdiv(pr.tokens, 4), 256, 0, s, pr);
+        return launch(route_backward_kernel<T, 16>, cdiv(pr.tokens, 16), 256, 16 * row, s, pr);
+    return launch(route_backward_kernel<T, 64>, cdiv(pr.tokens, 4), 256, 4 * row, s, pr);
 }
 
 }  // namespace

@@ -20,6 +20,11 @@ __device__ __forceinline__ void wave_rank(int expert, int bits, int &rank, int &
     rank = expert < 0 ? 0 : __popcll(same & ((1ull << lane) - 1ull));
     count = expert < 0 ? 0 : __popcll(same);
 }
+// The wave's accesses to LDS before this one, by any of its lanes, come before those after it.
+__device__ __forceinline__ void in_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
 // x of another of the 16 lanes (CTRL 0x120 + n: n places on).
 template <int CTRL>
 __device__ __forceinline__ float rotated(float x) {

@@ -320,6 +320,32 @@ def test_route_extremes():
     assert layers.route(z, 4, bias=bias)[0].tolist() == [[0, 3, -1, -1]]
 
 
+@pytest.mark.parametrize("experts", [40, 700])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_route_backward_of_repeated_experts(experts, score, renormalize):
+    """Ids that no route gives, an expert more than once: its gradients add up. The terms of a
+    sum of k values d r, |r| <= 1, are each off by a dozen float32 roundings (exponentials,
+    division, inner sum), so all are by 16 of them at most of the largest."""
+    z = randn(5, 9, experts)
+    ids = numbers(6, 9 * 5, experts).reshape(9, 5)
+    ids[0], ids[1] = 3, torch.tensor([4, 2, 4, 2, 4])
+    ids[2, 1:], ids[3, 2] = -1, experts
+    ids = ids.cuda()
+    dw = randn(7, 9, 5)
+    dz = layers.route_backward(dw, z, ids, score=score, renormalize=renormalize, scale=1.5)
+    leaf = z.double().requires_grad_(True)
+    live = (ids >= 0) & (ids < experts)
+    s = torch.softmax(leaf, 1) if score == "softmax" else torch.sigmoid(leaf)
+    w = torch.where(live, s.gather(1, ids.clamp(0, experts - 1)), 0.0)
+    if renormalize:
+        w = w / w.sum(1, keepdim=True)
+    want, = torch.autograd.grad(1.5 * w, leaf, dw.double())
+    most = 1.5 * 5 * float(dw.abs().max())
+    assert float((dz.double() - want).abs().max()) <= 16 * 2.0 ** -24 * most
+    assert torch.equal(dz, layers.route_backward(dw, z, ids, score=score, renormalize=renormalize, scale=1.5))
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_infinite_bias(score):
     """A bias of +inf takes its experts first, one of -inf takes them out, in any groups."""
