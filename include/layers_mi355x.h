@@ -109,11 +109,10 @@ int layers_route_backward(const float *dweights, const void *logits, int64_t ld,
  * A target outside [0, classes) is ignored: its loss is 0 (lse is still given).
  * 0 <= rows < 2^31, 1 <= classes, width, ld <= 2^20, and fewer than about 2^23 tiles of
  * 64 x 64 to 256 x 256 logits. float32 uses the float32 matrix instructions, the 16-bit types
- * theirs; both accumulate in float32. Workspace: 8 bytes for 64 to 256 logits of a row (small
- * products of a long width: their logits' partial sums, at most 1024 tiles), and
- * where more than 32 16-bit rows do not lie on 4-byte boundaries (width odd, or, with
- * `unaligned` non-zero, an odd ld or a pointer off 4 bytes) room for their copies on padded
- * rows, w's too.
+ * theirs; both accumulate in float32. Workspace: 8 bytes for 16 to 256 logits of a row (small
+ * products of a long width: their logits' partial sums, at most 1024 tiles), and where more
+ * than 32 16-bit rows do not lie on 4-byte boundaries (width odd, or, with `unaligned` non-zero,
+ * an odd ld or a pointer off 4 bytes) room for their copies on padded rows, w's too.
  */
 size_t layers_cross_entropy_workspace_bytes(int64_t rows, int64_t classes, int64_t width,
                                             int dtype, int unaligned);
@@ -130,8 +129,9 @@ int layers_cross_entropy(const void *x, int64_t ldx, const void *w, const int64_
  * NULL, not both. z is computed again, in pieces of the classes whose dz takes about 512 MiB
  * of the workspace; the products read dz rounded to dtype, which is what the 16-bit matrix
  * instructions take, divided by the largest |dloss + dlse| or |dloss| of a row (for float16
- * times 2^14, which keeps it in range). dx is summed over the pieces in float32. An ignored row without dlse has dz 0 and dx 0; its x is read
- * by dw's product all the same and has to be finite.
+ * times 2^14, which keeps it in range). dx is summed over the pieces in float32. An ignored row
+ * without dlse has dz 0 and dx 0; its x is read by dw's product all the same and has to be
+ * finite.
  */
 size_t layers_cross_entropy_backward_workspace_bytes(int64_t rows, int64_t classes, int64_t width,
                                                      int dtype, int unaligned);

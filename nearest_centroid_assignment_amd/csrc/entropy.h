@@ -51,6 +51,8 @@ __device__ __forceinline__ bool entropy_place(const EntropyProblem &pr, int bloc
     return true;
 }
 
+// 8192 x 65536 x 2048 bf16, tiles of 256 x 256: 1.73 ms, 1270 TFLOP/s, matrix units busy 58 % of
+// the cycles (a plain product of the library at 8192^3: 1418).
 template <class S>
 __global__ __launch_bounds__(S::NW * 64, 2) void entropy_kernel(EntropyProblem pr) {
     __shared__ __align__(1024) char memory[S::NS * S::kStage];
@@ -232,6 +234,8 @@ __global__ __launch_bounds__(512) void entropy_thin_kernel(EntropyProblem pr) {
     if (threadIdx.x % kEach == 0 && row < rows) pr.part[(int64_t)blockIdx.x * rows + row] = make_float2(m, s);
 }
 
+// At that size, in two pieces: 1.03 ms each, 1070 TFLOP/s; the epilogue and its 512 MiB take what
+// dx's product, 0.80 ms, does not.
 template <class S>
 __global__ __launch_bounds__(S::NW * 64, 2) void entropy_dz_kernel(EntropyProblem pr) {
     typedef typename S::type T;
@@ -277,7 +281,7 @@ __global__ __launch_bounds__(S::NW * 64, 2) void entropy_dz_kernel(EntropyProble
         write(ActTag<0>{});
 }
 
-// dx's tile, its depth (the piece's classes) whole or in parts.
+// dx's tile, its depth (the piece's classes) whole or in parts. (0.80 ms a piece, 1370 TFLOP/s.)
 template <class S>
 __device__ __forceinline__ void entropy_dx_block(const EntropyGrad &e, int block, lds_char *smem) {
     typedef typename S::type T;
@@ -356,7 +360,8 @@ __device__ __forceinline__ void entropy_dx_block(const EntropyGrad &e, int block
         finish(ActTag<0>{});
 }
 
-// dw's tile of the piece, its depth (the rows) whole or in parts.
+// dw's tile of the piece, its depth (the rows) whole or in parts. (0.95 ms a piece, 1160 TFLOP/s:
+// both operands come out of LDS transposed.)
 template <class S>
 __device__ __forceinline__ void entropy_dw_block(const EntropyGrad &e, int block, lds_char *smem) {
     typedef typename S::type T;

@@ -108,6 +108,7 @@ __device__ __forceinline__ void store_chunk(T *p, const T (&v)[V]) {
 
 // Every `step`-th row a few lanes, a wave or a block, the next one on its way meanwhile. ONCE:
 // rows that no cache holds pass the caches by (see once_of).
+// 65536 x 2048 bf16: 104 us, 5.2 TB/s.
 template <typename T, typename W, int NT, int C, bool ONCE, bool EVEN>
 __global__ __launch_bounds__(kThreads<NT>) void norm_kernel(NormProblem pr, int64_t step) {
     constexpr int V = vec<T>();
@@ -220,7 +221,8 @@ __global__ __launch_bounds__(256) void norm_long_kernel(NormProblem pr) {
 }
 
 // dx, and the columns' sums over the rows that the lanes, the wave or the block take: every
-// `step`-th. A block leaves one part of the sums.
+// `step`-th. A block leaves one part of the sums. 65536 x 2048 bf16: 137 us, 5.9 TB/s, and 5 for
+// the join.
 template <typename T, typename W, int NT, int C, bool ONCE, bool EVEN>
 __global__ __launch_bounds__(kThreads<NT>) void norm_backward_kernel(NormProblem pr, int64_t step) {
     constexpr int V = vec<T>();

@@ -469,7 +469,8 @@ __device__ __forceinline__ void route_token(const RouteProblem &pr, const Layout
     }
     Keys<K, L, V> key;
 #pragma unroll
-    for (int j = 0; j < V; ++j) key.k[j] = key.of(K == kScored ? c[j] * unit : c[j], l.first + j, own * (V <= 16 ? 16 : 32) + j);
+    for (int j = 0; j < V; ++j)
+        key.k[j] = key.of(K == kScored ? c[j] * unit : c[j], l.first + j, own * (V <= 16 ? 16 : 32) + j);
     typename Key<K, L, V>::type best = Keys<K, L, V>::kEmpty;
     // One more than is returned, where choices may have to be told apart. Of a lane's keys
     // only as many can come up as are asked for, and the one after them.
