@@ -81,8 +81,12 @@ typedef enum { LAYERS_SOFTMAX = 0, LAYERS_SIGMOID = 1 } layers_score;
  *   the chosen experts' s).
  * An expert whose c is -inf or NaN (a logit that a mask has set to -inf, a bias of -inf) is
  * never chosen; where fewer than `top` are left, the ids after them are -1 (experts_plan drops
- * such pairs) and their weights 0. Without bias and with group_best 1 the choice goes by the
- * logits themselves, whose order s keeps. Otherwise it is that of the formulas in float64.
+ * such pairs) and their weights 0. Without bias and with group_best 1 or one group the choice goes
+ * by the logits themselves, whose order s keeps. Otherwise it is that of the formulas in float64.
+ * A softmax row with a NaN or +inf has no s. With bias, or group_best 2 of several groups, it
+ * has no c either: ids -1, weights 0. By the logits its other experts (and +inf, the first) are
+ * chosen all the same; their weights are the shares among them with `renormalize` (NaN with a
+ * chosen +inf), else NaN. A sigmoid's NaN takes out its own expert alone.
  *   bias      (experts) float32, dense, or NULL.
  * 0 <= tokens < 2^26 - 16, 1 <= top <= 64, top <= experts, groups a divisor of experts,
  * groups <= 64, experts / groups <= 32 * (64 / groups rounded down): up to 2048 experts.

@@ -290,8 +290,9 @@ __device__ __forceinline__ int choose_exactly(const float (&z)[V], const RoutePr
     m = lanes_max<L>(m);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const bool live = z[j] > -INFINITY;
-        c[j] = !live ? 0.0 : pr.sigmoid ? 1.0 / (1.0 + exp(-(double)z[j])) : exp((double)z[j] - m);
+        // (A NaN, or a softmax's +inf, makes the sum a NaN: nothing to choose by, as in route_token.)
+        const bool out = z[j] == -INFINITY;
+        c[j] = out ? 0.0 : pr.sigmoid ? 1.0 / (1.0 + exp(-(double)z[j])) : exp((double)z[j] - m);
         sum += c[j];
     }
     sum = lanes_sum<L>(sum);

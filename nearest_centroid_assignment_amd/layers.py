@@ -285,7 +285,8 @@ def route(logits, top, score="softmax", bias=None, groups=1, top_groups=None, gr
     choice alone. With ``groups`` equal runs of experts, only those of the
     ``top_groups`` groups with the largest sums of their ``group_best`` (1 or 2) largest
     score + bias. Weights are the scores, divided by their sum over the chosen with
-    ``renormalize``, times ``scale``. Places for which no expert is left: id -1, weight 0."""
+    ``renormalize``, times ``scale``. Places for which no expert is left: id -1, weight 0 (all
+    places of a softmax row with a NaN or +inf, where the choice needs more than the logits)."""
     if top_groups is None:
         top_groups = groups
     if stream is None:

@@ -1,0 +1,69 @@
+"""Edges of the operators around the experts on the GPU: rows whose answer must not depend on
+their neighbours, the orders of the lanes that the other sizes leave out, the largest sizes."""
+import math
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from nearest_centroid_assignment_amd import layers  # noqa: E402
+from tests import gpu_util as gu  # noqa: E402
+from tests.test_gpu_experts import TYPES, randn  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+# ------------------------------------------------------------------- route
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("n,top,kw", [
+    (40, 4, dict(bias=True)), (40, 4, dict(groups=8, top_groups=3, group_best=2)),
+    (256, 8, dict(bias=True, groups=8, top_groups=4, group_best=2)), (600, 5, dict(bias=True))])
+def test_route_nan_beside_ties(dtype, score, n, top, kw):
+    """Rows with a NaN (or, of softmax scores, an infinite) logit among rows of equal logits, whose
+    choices need float64: every row is answered as it is alone. By the formulas each s of such
+    a softmax row is NaN and nothing is chosen; a sigmoid's NaN takes out its own expert."""
+    gu.announce(f"route beside ties {dtype} {score} {top} of {n} {kw}")
+    kw = dict(kw, score=score)
+    if kw.pop("bias", False):
+        kw["bias"] = torch.full((n,), 0.5, device="cuda")
+    tokens = 37  # waves of four tokens with none, one or more of them
+    z = torch.ones(tokens, n, device="cuda").to(dtype)
+    z[2::3] = randn(1, len(range(2, tokens, 3)), n, dtype=dtype)
+    odd = torch.zeros(tokens, dtype=torch.bool)
+    odd[[1, 6, 11, 12, 20, 21, 22, 31, 36]] = True
+    z[odd.cuda(), 3] = math.nan
+    if score == "softmax":
+        z[[6, 36], 3] = math.inf
+    ids, weights = layers.route(z, top, **kw)
+    for t in range(tokens):
+        alone = layers.route(z[t:t + 1].contiguous(), top, **kw)
+        assert torch.equal(alone[0][0], ids[t]) and torch.equal(alone[1][0], weights[t]), t
+    if score == "softmax":
+        assert (ids[odd.cuda()] == -1).all() and (weights[odd.cuda()] == 0).all()
+    else:
+        assert (ids[odd.cuda()] >= 0).all() and (ids[odd.cuda()] != 3).all()
+    assert (ids[~odd.cuda()] >= 0).all() and weights.isfinite().all()
+    assert ids[0].tolist() == list(range(top))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_route_nan_by_the_logits(dtype):
+    """Where nothing is added the logits choose, and a softmax row with a NaN gives its others:
+    shares among the chosen, or NaN where they need the row's own s."""
+    z = torch.tensor([[1.0, math.nan, 2.0, 0.0], [1.0, math.inf, 2.0, 0.0]], device="cuda").to(dtype)
+    for kw in (dict(), dict(group_best=2)):
+        ids, w = layers.route(z, 2, **kw)
+        assert ids.tolist() == [[2, 0], [1, 2]]
+        e = math.exp(-1)
+        assert torch.allclose(w[0].cpu(), torch.tensor([1 / (1 + e), e / (1 + e)])) and w[1].isnan().all()
+        ids, w = layers.route(z, 2, renormalize=False, **kw)
+        assert ids.tolist() == [[2, 0], [1, 2]] and w.isnan().all()
