@@ -17,14 +17,14 @@ hipError_t launch_entropy_both_t(const EntropyGrad &e, hipStream_t s);
 
 namespace {
 
-// R rows a block, 256 / R threads to a row, each joining every (256 / R)-th of the column
-// tiles' sums (the largest first, then the sums relative to it).
+// R rows a block from row `start` on, 256 / R threads to a row, each joining every (256 / R)-th of
+// the column tiles' sums (the largest first, then the sums relative to it).
 template <int R>
-__global__ __launch_bounds__(256) void entropy_join_kernel(EntropyProblem pr, int tiles) {
+__global__ __launch_bounds__(256) void entropy_join_kernel(EntropyProblem pr, int tiles, int64_t start) {
     constexpr int kSlices = 256 / R;
     __shared__ float most[kSlices][R + 1], sums[kSlices][R + 1];
     const int r = threadIdx.x % R, slice = threadIdx.x / R;
-    const int64_t row = (int64_t)blockIdx.x * R + r;
+    const int64_t row = start + (int64_t)blockIdx.x * R + r;
     const bool there = row < pr.rows;
     const float2 *part = pr.part + (there ? row : pr.rows - 1);
     // (Nothing times an overflowing factor would be a NaN.)
@@ -173,8 +173,16 @@ hipError_t entropy_t(const EntropyProblem &pr, hipStream_t s) {
     const Cut cut = {pr.tile, pr.thin, pr.thin != 0, 0.0};
     // A block to a row of many tiles: 2 rows of 1079 tiles 10.9 us with 16 threads to a row, 4.7.
     const int tiles = (int)cdiv(pr.count, entropy_columns(cut));
-    if (pr.rows <= 512 && tiles > 64) return launch(entropy_join_kernel<1>, pr.rows, 256, 0, s, pr, tiles);
-    return launch(entropy_join_kernel<16>, cdiv(pr.rows, 16), 256, 0, s, pr, tiles);
+    if (pr.rows <= 512 && tiles > 64)
+        return launch(entropy_join_kernel<1>, pr.rows, 256, 0, s, pr, tiles, (int64_t)0);
+    // (One dispatch holds less than 2^32 work-items, 16 of them a row.)
+    constexpr int64_t kMost = 1 << 27;
+    hipError_t done = hipSuccess;
+    for (int64_t start = 0; start < pr.rows && done == hipSuccess; start += kMost) {
+        const int64_t rows = pr.rows - start < kMost ? pr.rows - start : kMost;
+        done = launch(entropy_join_kernel<16>, cdiv(rows, 16), 256, 0, s, pr, tiles, start);
+    }
+    return done;
 }
 template <typename T>
 hipError_t dz_t(const EntropyProblem &pr, hipStream_t s) {

@@ -8,7 +8,8 @@ torch = pytest.importorskip("torch")
 
 from nearest_centroid_assignment_amd import layers  # noqa: E402
 from tests import gpu_util as gu  # noqa: E402
-from tests.test_gpu_experts import TYPES, randn  # noqa: E402
+from tests.test_gpu_experts import TYPES, close, randn  # noqa: E402
+from tests.test_gpu_layers import entropy_ref  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,29 @@ def test_route_nan_by_the_logits(dtype):
         assert torch.allclose(w[0].cpu(), torch.tensor([1 / (1 + e), e / (1 + e)])) and w[1].isnan().all()
         ids, w = layers.route(z, 2, renormalize=False, **kw)
         assert ids.tolist() == [[2, 0], [1, 2]] and w.isnan().all()
+
+
+# ----------------------------------------------------------- cross entropy
+
+
+def test_cross_entropy_of_very_many_rows():
+    """More rows than one dispatch of the kernel that joins their sums holds (2^28): a sample
+    of them, both sides of every border among it, against the formulas in float64."""
+    rows, classes, width, dtype = 2 ** 28 + 21, 40, 2, torch.bfloat16
+    gu.announce(f"cross_entropy {rows} x {classes} x {width}")
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(rows, width, generator=gen, device="cuda", dtype=dtype)
+    w = randn(2, classes, width, dtype=dtype)
+    targets = torch.randint(-1, classes, (rows,), generator=gen, device="cuda")
+    loss, lse = layers.cross_entropy(x, w, targets)
+    dloss = torch.rand(rows, generator=gen, device="cuda")
+    gu.announce("its gradient")
+    dx, _ = layers.cross_entropy_backward(dloss, x, w, targets, lse, need_dw=False)
+    assert loss.isfinite().all() and lse.isfinite().all() and dx.isfinite().all()
+    at = torch.randint(rows, (2000,), generator=gen, device="cuda")
+    at[:64] = torch.arange(64)
+    at[64:128] = torch.arange(2 ** 27 - 32, 2 ** 27 + 32)
+    at[128:181] = torch.arange(2 ** 28 - 32, rows)
+    want = entropy_ref(x[at], w, targets[at], dloss[at], None, dtype)
+    for name, got in (("loss", loss), ("lse", lse), ("dx", dx)):
+        close(got[at], *(t.cpu() for t in want[name]), name)
