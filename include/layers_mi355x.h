@@ -130,10 +130,11 @@ int layers_cross_entropy(const void *x, int64_t ldx, const void *w, const int64_
  *   dz = (dloss + dlse) e^(z - lse) - dloss [j = target], without dloss in ignored rows,
  *   dx = dz w, dw = dz^T x.
  * dlse makes any function of lse a part of the loss (for c lse^2: 2 c lse). dx or dw may be
- * NULL, not both. z is computed again, in pieces of the classes whose dz takes about 512 MiB
- * of the workspace; the products read dz rounded to dtype, which is what the 16-bit matrix
- * instructions take, divided by the largest |dloss + dlse| or |dloss| of a row (for float16
- * times 2^14, which keeps it in range). dx is summed over the pieces in float32. An ignored row
+ * NULL, not both. z is computed again, in pieces of the classes whose dz takes 512 MiB of the
+ * workspace at most, or, past 2^20 16-bit rows (2^19 of float32), 256 classes of all rows; the
+ * products read dz rounded to dtype, which is what the 16-bit matrix instructions take, divided
+ * by the largest |dloss + dlse| or |dloss| of a row (for float16 times 2^14, which keeps it in
+ * range). dx is summed over the pieces in float32. An ignored row
  * without dlse has dz 0 and dx 0; its x is read by dw's product all the same and has to be
  * finite.
  */

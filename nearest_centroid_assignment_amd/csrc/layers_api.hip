@@ -72,7 +72,7 @@ bool route_shape_ok(int64_t tokens, int64_t experts, int64_t top) {
 
 // ---------------------------------------------------------------- entropy
 
-constexpr size_t kPiece = (size_t)1 << 29;  // bytes of dz at a time
+constexpr size_t kPiece = (size_t)1 << 29;  // bytes of dz at a time, but for piece_of's least
 
 bool entropy_shape_ok(int dtype, int64_t rows, int64_t classes, int64_t width) {
     if (rows < 0 || rows > kMaxRows || classes < 1 || classes > kMaxWidth || width < 1 || width > kMaxWidth)
@@ -88,7 +88,8 @@ bool entropy_shape_ok(int dtype, int64_t rows, int64_t classes, int64_t width) {
     }
     return true;
 }
-// The classes of a piece: equal pieces, of whole tiles.
+// The classes of a piece: equal pieces, of whole tiles, 256 at least (dx's float32 sums are read
+// and written once a piece).
 int64_t piece_of(int64_t rows, int64_t classes, int dtype) {
     const int64_t row = (int64_t)(kPiece / size_of(dtype)) / (rows < 1 ? 1 : rows);
     const int64_t most = row < 512 ? 256 : row / 256 * 256;
