@@ -6,6 +6,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/GradMode.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
@@ -101,17 +102,26 @@ PyObject *tuple_of(const at::Tensor &a, const at::Tensor &b, const at::Tensor &c
     if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
-// Warns where a graph is being recorded and one of these asks to be in it: the operator
-// is not. False if the warning has become an error.
+// Warns where a graph is being recorded and one of these asks to be in it, or where one carries
+// a forward-mode tangent: the operator is not, and its result has none. False if the warning
+// has become an error.
 bool say_unrecorded(const char *name, at::ArrayRef<const at::Tensor *> inputs) {
-    if (!c10::GradMode::is_enabled()) return true;
-    for (const at::Tensor *t : inputs)
-        if (t && t->requires_grad())
+    const bool graph = c10::GradMode::is_enabled();
+    const bool tangents = c10::AutogradState::get_tls_state().get_fw_grad_mode();
+    if (!graph && !tangents) return true;
+    for (const at::Tensor *t : inputs) {
+        if (graph && t && t->requires_grad())
             return PyErr_WarnFormat(PyExc_UserWarning, 2,
                                     "%s.%s is not recorded for autograd: an input requires grad, but "
                                     "gradients are explicit calls (%s.%s_backward). Call it under "
                                     "torch.no_grad(), or with detached tensors",
                                     module_name, name, module_name, name) == 0;
+        if (tangents && t && t->_fw_grad(0).defined())
+            return PyErr_WarnFormat(PyExc_UserWarning, 2,
+                                    "%s.%s is not recorded for autograd: an input has a forward-mode "
+                                    "tangent, which the result does not. Call it with the primal",
+                                    module_name, name) == 0;
+    }
     return true;
 }
 

@@ -16,7 +16,7 @@ have any row stride, with the elements of a row next to each other; the header
 has the largest sizes. As in ``binding``, a call enqueues on ``stream`` (the current
 one by default) and returns. Gradients are explicit calls, given what the forward call returned:
 autograd records none of this, and a forward call with an input that requires grad
-warns of it (not under ``torch.no_grad()``).
+(not under ``torch.no_grad()``) or that has a forward-mode tangent warns of it.
 """
 from __future__ import annotations
 

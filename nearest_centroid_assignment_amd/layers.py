@@ -14,7 +14,8 @@ conventions are those of ``experts``: tensors supply pointers, strides and the s
 step of the computation runs in the library's HIP kernels, and there is no CPU fallback;
 matrices may have any row stride, with the elements of a row next to each other; a call
 enqueues on ``stream`` (the current one by default) and returns; gradients are explicit
-calls, and a forward call with an input that requires grad warns of it.
+calls, and a forward call with an input that requires grad or has a forward-mode tangent warns
+of it.
 """
 from __future__ import annotations
 

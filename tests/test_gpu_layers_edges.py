@@ -94,3 +94,24 @@ def test_cross_entropy_of_very_many_rows():
     want = entropy_ref(x[at], w, targets[at], dloss[at], None, dtype)
     for name, got in (("loss", loss), ("lse", lse), ("dx", dx)):
         close(got[at], *(t.cpu() for t in want[name]), name)
+
+
+# --------------------------------------------------------------- tangents
+
+
+def test_warns_of_tangents():
+    """Both ways to a kernel say that the result has no tangent, and give the primal's result."""
+    from torch.autograd import forward_ad
+
+    w, ids = randn(1, 20, 8), torch.arange(3, device="cuda")
+    want = layers.embed(ids, w)
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(w, randn(2, 20, 8))
+        for kw in (dict(), dict(stream=torch.cuda.current_stream())):
+            for call in (lambda: layers.embed(ids, dual, **kw), lambda: layers.layer_norm(dual, **kw),
+                         lambda: layers.route(dual, 2, **kw), lambda: layers.cross_entropy(w, dual, ids[:1].expand(20).contiguous(), **kw)):
+                with pytest.warns(UserWarning, match="tangent"):
+                    out = call()
+                assert forward_ad.unpack_dual(out if torch.is_tensor(out) else out[1]).tangent is None
+        with pytest.warns(UserWarning, match="tangent"):
+            assert torch.equal(layers.embed(ids, dual), want)
