@@ -47,7 +47,7 @@ class Model:
         self.step = 0
 
     def update(self, grads, offsets, lr, rate=1e-3, clip=1.0):
-        norm = torch.stack(torch._foreach_norm(grads)).norm()
+        norm = torch.stack(torch._foreach_norm(grads, dtype=torch.float32)).norm()
         scale = (clip / (norm + 1e-6)).clamp(max=1.0).reshape(1).float()
         self.step += 1
         experts.adamw_step(self.masters, grads, lr=lr, betas=(0.9, 0.99), weight_decay=0.01,
