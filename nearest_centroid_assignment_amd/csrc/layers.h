@@ -75,7 +75,6 @@ hipError_t launch_route_backward(int dtype, const RouteProblem &pr, hipStream_t 
 struct EntropyProblem {
     const void *x, *w;        // rows x width, classes x width, on 4-byte boundaries
     int64_t ldx, ldw, rows, classes, width;
-    int64_t x_cols, w_cols;   // readable columns (a pad is zero)
     const int64_t *targets;
     int tile, thin;           // entropy_plan's tile, and with its `thin` its splits
     // The sums of each row over one column tile, and the target's logit.
@@ -109,7 +108,8 @@ constexpr int64_t kOwnScale = 1024;  // rows
 // dx (first and last piece, sums between them) and dw of a piece.
 struct EntropyGrad {
     const void *dz, *x, *w;   // w, dw: the piece's first row
-    int64_t lddz, ldx, ldw, x_cols, w_cols;
+    int64_t lddz, ldx, ldw;
+    int64_t x_cols, w_cols;   // readable columns (a pad is zero)
     int64_t rows, count, width;
     const float *scale;
     void *dx;                 // NULL: not computed
