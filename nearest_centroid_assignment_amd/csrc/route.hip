@@ -229,7 +229,8 @@ __device__ __forceinline__ bool group_kept(F first, F second, int groups, int ke
         b = larger(b, d);
     }
     const F none = -(F)INFINITY;
-    const F rank = best == 2 && b > none ? a + b : a;
+    // (Half of the sum, which no finite biases overflow. Infinite ranks are those of the formulas.)
+    const F rank = best == 2 ? (F)0.5 * a + (b > none ? (F)0.5 * b : (F)0) : a;
     int before = 0;
     if constexpr (L == 16 && sizeof(F) == 4) {
         // (A group's lanes hold the same key.)
@@ -248,7 +249,7 @@ __device__ __forceinline__ bool group_kept(F first, F second, int groups, int ke
     }
     const bool keep = group < groups && before < kept * lanes;
     const F worst = lanes_max<L>(keep ? -rank : none), other = lanes_max<L>(keep || group >= groups ? none : rank);
-    least = -worst - other;
+    least = (best == 2 ? (F)2 : (F)1) * (-worst - other);
     return keep;
 }
 

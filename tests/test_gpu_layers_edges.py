@@ -95,6 +95,28 @@ def test_route_of_groups_that_leave_lanes(dtype, score, groups, size, kept, best
         close(weights, w, 2.0 ** -18 * w, "weights")
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [4, 40])  # groups of 16 lanes to a token, and of a wave
+def test_route_group_ranks_of_large_biases(dtype, score, size):
+    """Sums of two choices that float32 does not hold, of biases that are the type's lowest or
+    largest value: the groups are those of the formulas in float64, where they are finite."""
+    low, high = torch.finfo(torch.float32).min, torch.finfo(torch.float32).max
+    tokens, groups = 9, 4 if size == 4 else 20
+    logits = randn(1, tokens, groups * size, dtype=dtype)
+    for first, kept in (((-math.inf, low, 0.0, -math.inf), 2), ((2e38, 3e38, -math.inf, 2.5e38), 1),
+                        ((low, low, low, low), 3), ((low, 0.9 * low, low, -math.inf), 1),
+                        ((0.8 * high, high, high, 0.0), 2)):
+        bias = torch.full((groups, size), -math.inf)
+        bias[:4] = torch.tensor(first)[:, None] * (1 - 1e-3 * torch.arange(size))  # no two alike
+        bias = bias.reshape(-1).cuda()
+        kw = dict(score=score, bias=bias, groups=groups, top_groups=kept, group_best=2)
+        ids, weights = layers.route(logits, min(6, kept * size), **kw)
+        want, w, _ = route_ref(logits, min(6, kept * size), score, bias, groups, kept, 2, True, 1.0)
+        assert torch.equal(ids.cpu(), want), first
+        close(weights, w, 2.0 ** -18 * w, "weights")
+
+
 # ----------------------------------------------------------- cross entropy
 
 
