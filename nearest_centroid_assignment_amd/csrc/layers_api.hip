@@ -25,7 +25,7 @@ struct Sections {
 // ------------------------------------------------------------------ embed
 
 bool embed_shape_ok(int64_t tokens, int64_t classes, int64_t width) {
-    return tokens >= 0 && tokens * 64 <= kMaxGridThreads - 256 && tokens <= kMaxRows &&
+    return tokens >= 0 && tokens <= kMaxRows && tokens * 64 <= kMaxGridThreads - 256 &&
            classes >= 1 && classes <= kMaxWidth && width >= 1 && width <= kMaxWidth;
 }
 struct EmbedLayout {
@@ -66,7 +66,7 @@ bool weights_ok(int dtype, int weights_dtype) {
 // ------------------------------------------------------------------ route
 
 bool route_shape_ok(int64_t tokens, int64_t experts, int64_t top) {
-    return tokens >= 0 && tokens * 64 <= kMaxGridThreads - 1024 && top >= 1 && top <= kMaxTop &&
+    return tokens >= 0 && tokens <= kMaxRows && tokens * 64 <= kMaxGridThreads - 1024 && top >= 1 && top <= kMaxTop &&
            experts >= top && experts <= 2048;
 }
 

@@ -1,4 +1,7 @@
-"""What the layers' size queries answer at and past the sizes where a limit begins (no GPU)."""
+"""What the layers' size queries and checks answer at and past the sizes where a limit begins (no GPU: every
+call here is refused)."""
+import os
+
 import pytest
 
 F32, BF16 = 0, 1
@@ -36,3 +39,12 @@ def test_most_rows(lib):
     for rows in (2 ** 28, 2 ** 28 + 16, 2 ** 29 - 1024):
         assert fwd(rows, 64, 2, BF16, 0) >= 12 * rows and bwd(rows, 64, 2, BF16, 0) >= 128 * rows
     assert fwd(2 ** 29 + 1024, 64, 2, BF16, 0) == 0 and fwd(2 ** 31 - 1, 64, 2, BF16, 0) == 0
+
+
+@pytest.mark.skipif(os.path.exists("/dev/kfd"), reason="fake-pointer validation tests run only without a GPU")
+def test_route_refuses_counts_that_overflow(lib):
+    gib, shape = 1 << 30, -2
+    for tokens in (2 ** 26, 2 ** 31, 2 ** 57, 2 ** 58, 2 ** 62, 2 ** 63 - 1):
+        assert lib.layers_route(gib, 8, F32, tokens, 8, 2, 0, None, 1, 1, 1, 1, 1.0, 64 * gib, 128 * gib, None) == shape
+        assert lib.layers_route_backward(gib, 32 * gib, 8, 64 * gib, F32, tokens, 8, 2, 0, 1, 1.0, 128 * gib, 8, None) == shape
+        assert lib.layers_embed(gib, tokens, 32 * gib, F32, 8, 8, 1.0, 64 * gib, 8, None) == shape
