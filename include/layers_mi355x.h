@@ -110,7 +110,8 @@ int layers_route_backward(const float *dweights, const void *logits, int64_t ld,
  * Softmax cross entropy of z = x w^T, z not kept: for every row r of x (rows, width)
  *   lse[r] = log sum_j e^z[r, j], loss[r] = lse[r] - z[r, targets[r]].
  *   w        (classes, width), dense; targets (rows) int64; loss, lse (rows) float32.
- * A target outside [0, classes) is ignored: its loss is 0 (lse is still given).
+ * A target outside [0, classes) is ignored: its loss is 0 (lse is still given). Logits have to
+ * stay below 2^127 in magnitude, or they leave float32 in units of log 2.
  * 0 <= rows < 2^31, 1 <= classes, width, ld <= 2^20, and fewer than about 2^23 tiles of
  * 64 x 64 to 256 x 256 logits. float32 uses the float32 matrix instructions, the 16-bit types
  * theirs; both accumulate in float32. Workspace: 8 bytes for 16 to 256 logits of a row (small

@@ -45,9 +45,10 @@ __device__ __forceinline__ Factors factors_of(const EntropyProblem &pr, int64_t 
 // loses nothing where p is small (rounded as it is, 1 / rows makes every such place off by the
 // same part, and with them all of dx and dw: a mean of 300 rows of 513 classes bf16, norm of
 // dx's error against 64 bits over its norm 0.0024 -> 0.0018, where rounding dx alone leaves
-// 0.0017). float16 holds 2^-24 to 65504: there it is multiplied by 2^14 (most_dz) as well, or
-// most of a large softmax would be zeros. dx and dw are multiplied by the inverse. scale: the
-// factor, and its inverse.
+// 0.0017; factors that differ from row to row keep more of dz's own rounding: with a dlse of each
+// row's own 0.0026 for 83 rows of 12416 classes, 0.0020 for 2394 of 5046). float16 holds 2^-24 to
+// 65504: there it is multiplied by 2^14 (most_dz) as well, or most of a large softmax would be
+// zeros. dx and dw are multiplied by the inverse. scale: the factor, and its inverse.
 //
 // The largest factor of the rows that this thread looks at, every `step`-th; infinity where one
 // is not finite.

@@ -102,7 +102,8 @@ hipError_t launch_entropy_dz(int dtype, const EntropyProblem &pr, hipStream_t s)
 // dz kernel to look at them.
 hipError_t launch_entropy_scale(const EntropyProblem &pr, hipStream_t s);
 // (dx and dw of 64 x 8192 x 512 bf16 21.5 us, with a launch for the scale 23.0; 2048 x 2048 x 512
-// 37.5 and 39; 8192 x 8192 x 512 253 and 240.)
+// 37.5 and 39; 8192 x 8192 x 512 253 and 240. The launch is one block: 4 to 7 us for 8192 rows, 15
+// for 65536, 440 for 2^20, 10700 for 2^24.)
 constexpr int64_t kOwnScale = 1024;  // rows
 
 // dx (first and last piece, sums between them) and dw of a piece.

@@ -9,7 +9,7 @@
 // variance is the mean square of what is left after the mean is taken off (two passes
 // over registers: no cancellation), and the columns' sums of the gradient stay in
 // registers over all rows that they take; the blocks' sums are added in order
-// by a second kernel. Rows that no registers hold are read again from the caches.
+// by a second kernel. Rows longer than four accesses of 512 threads are read again from the caches.
 #include "layers.h"
 #include "rows.h"
 
