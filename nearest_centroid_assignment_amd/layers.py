@@ -173,7 +173,7 @@ def _embed_backward(dy, ids, classes, scale, workspace, stream):
     L = lib()
     nbytes = L.layers_embed_backward_workspace_bytes(tokens, classes, width, code)
     workspace, ps, ns = _scratch(workspace, nbytes, dy, side)
-    dw = _new(dy, side, (classes, width)) if classes > 0 else None
+    dw = _new(dy, side, (classes, width)) if nbytes else None  # (a table that is supported)
     _check(L.layers_embed_backward(pg, ldg, pi, tokens, code, classes, width, scale,
                                    None if dw is None else dw.data_ptr() or None, ps, ns, queue),
            "layers_embed_backward")
@@ -307,7 +307,7 @@ def _route(logits, top, score, bias, groups, top_groups, group_best, renormalize
     pb = None if bias is None else _dense(bias, torch.float32, (experts,), dev, "bias")
     kind = _score_code(score)
     queue, side = _queue(stream, dev)
-    shape = (tokens, max(int(top), 0))
+    shape = (tokens, top if 1 <= top <= experts else 0)  # (no other is taken)
     ids, weights = _new(logits, side, shape, torch.int64), _new(logits, side, shape, torch.float32)
     _check(lib().layers_route(pl, ld, code, tokens, experts, top, kind, pb, groups, top_groups, group_best,
                               bool(renormalize), scale, ids.data_ptr() or None,

@@ -162,3 +162,19 @@ def test_warns_of_tangents():
                 assert forward_ad.unpack_dual(out if torch.is_tensor(out) else out[1]).tangent is None
         with pytest.warns(UserWarning, match="tangent"):
             assert torch.equal(layers.embed(ids, dual), want)
+
+
+# --------------------------------------------------------------- refusals
+
+
+def test_refusals_allocate_nothing():
+    """A count that no call takes is refused before memory for its outputs is asked for."""
+    z, ids, dy = randn(1, 8, 16), torch.zeros(8, dtype=torch.int64, device="cuda"), randn(2, 8, 16)
+    before = torch.cuda.memory_reserved()
+    torch.cuda.reset_peak_memory_stats()
+    at = torch.cuda.memory_allocated()
+    for call in (lambda: layers.route(z, 10 ** 8), lambda: layers.route(z, 17), lambda: layers.route(z, -1),
+                 lambda: layers.embed_backward(dy, ids, 10 ** 8), lambda: layers.embed_backward(dy, ids, -1)):
+        with pytest.raises(layers.KMeansError):
+            call()
+    assert torch.cuda.max_memory_allocated() <= at + 4096 and torch.cuda.memory_reserved() == before
