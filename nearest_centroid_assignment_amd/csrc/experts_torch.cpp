@@ -212,11 +212,11 @@ PyObject *linear(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (a[3] != Py_None && !rows_of(tensor(a[3]), type, rows, w.outs, dev, rr)) NOT_HERE;
     const size_t bytes =
         linear_bytes(rows, w.outs, w.ins, w.experts, code, 0, misplaced(rx, w));
-    if (bytes == 0) NOT_HERE;
+    bool save;
+    if (bytes == 0 || !truth(a[6], save)) NOT_HERE;
     if (!say_unrecorded("linear", {x, tensor(a[1]), tensor(a[2]), tensor(a[3])})) return nullptr;
     Scratch ws(bytes, dev);
     at::Tensor out = new_tensor({rows, w.outs}, type, dev), pre;
-    const int save = PyObject_IsTrue(a[6]);
     if (save) pre = new_tensor({rows, w.outs}, type, dev);
     const int status = linear_call(
         rx.p, rx.ld, w.w, bias, rr.p, rr.ld, w.offsets, code, act, rows, w.outs, w.ins,
@@ -246,8 +246,8 @@ PyObject *linear_backward(PyObject *, PyObject *const *a, Py_ssize_t count) {
         NOT_HERE;
     if (act != EXPERTS_ACT_NONE && !rows_of(tensor(a[3]), type, rows, w.outs, dev, rp)) NOT_HERE;
     if (a[6] != Py_None && !rows_of(tensor(a[6]), type, rows, w.ins, dev, ri)) NOT_HERE;
-    const bool need_dx = PyObject_IsTrue(a[8]), need_dw = PyObject_IsTrue(a[9]),
-               need_db = PyObject_IsTrue(a[10]);
+    bool need_dx, need_dw, need_db;
+    if (!truth(a[8], need_dx) || !truth(a[9], need_dw) || !truth(a[10], need_db)) NOT_HERE;
     if (!need_dx && !need_dw && !need_db) NOT_HERE;
     const size_t bytes =
         linear_bytes(rows, w.outs, w.ins, w.experts, code, 1, misplaced(rx, w));

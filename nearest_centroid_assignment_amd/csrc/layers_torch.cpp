@@ -99,8 +99,9 @@ PyObject *layer_norm(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (code_of(kind) < 0 || (a[1] != Py_None && !(pw = dense(weight, kind, {width}, dev))) ||
         (a[2] != Py_None && !(pb = dense(bias, kind, {width}, dev))))
         NOT_HERE;
+    bool save;
+    if (!truth(a[4], save)) NOT_HERE;
     if (!say_unrecorded("layer_norm", {x, weight, bias})) return nullptr;
-    const int save = PyObject_IsTrue(a[4]);
     at::Tensor out = new_tensor({rows, width}, x->scalar_type(), dev), mean, rstd;
     if (save) {
         mean = new_tensor({rows}, at::kFloat, dev);
@@ -132,8 +133,8 @@ PyObject *layer_norm_backward(PyObject *, PyObject *const *a, Py_ssize_t count) 
     if (code_of(kind) < 0 || (a[2] != Py_None && !(pw = dense(weight, kind, {width}, dev)))) NOT_HERE;
     const float *pm = (const float *)dense(tensor(a[3]), at::kFloat, {rows}, dev);
     const float *ps = (const float *)dense(tensor(a[4]), at::kFloat, {rows}, dev);
-    const bool need_dx = PyObject_IsTrue(a[5]), need_dw = PyObject_IsTrue(a[6]),
-               need_db = PyObject_IsTrue(a[7]);
+    bool need_dx, need_dw, need_db;
+    if (!truth(a[5], need_dx) || !truth(a[6], need_dw) || !truth(a[7], need_db)) NOT_HERE;
     if (!pm || !ps || (!need_dx && !need_dw && !need_db)) NOT_HERE;
     const size_t bytes = need_dw || need_db ? norm_bytes(rows, width, code) : 1;
     if (bytes == 0) NOT_HERE;
@@ -167,11 +168,12 @@ PyObject *route(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (dev < 0 || code < 0 || !rows_of(z, z->scalar_type(), tokens, experts, dev, rz)) NOT_HERE;
     const float *pb = nullptr;
     if (a[3] != Py_None && !(pb = (const float *)dense(tensor(a[3]), at::kFloat, {experts}, dev))) NOT_HERE;
-    if (top > experts) NOT_HERE;
+    bool renormalize;
+    if (top > experts || !truth(a[7], renormalize)) NOT_HERE;
     if (!say_unrecorded("route", {z})) return nullptr;
     at::Tensor ids = new_tensor({tokens, top}, at::kLong, dev), w = new_tensor({tokens, top}, at::kFloat, dev);
     const int status = route_call(rz.p, rz.ld, code, tokens, experts, top, (int)score, pb, groups, kept, best,
-                                  PyObject_IsTrue(a[7]), scale, (int64_t *)ids.data_ptr(),
+                                  renormalize, scale, (int64_t *)ids.data_ptr(),
                                   (float *)w.data_ptr(), queue(dev));
     if (status != KM_OK) return failed(status, "layers_route");
     return tuple_of(ids, w);
@@ -192,10 +194,11 @@ PyObject *route_backward(PyObject *, PyObject *const *a, Py_ssize_t count) {
     if (dev < 0 || code < 0 || !rows_of(z, z->scalar_type(), tokens, experts, dev, rz)) NOT_HERE;
     const int64_t *pi = (const int64_t *)dense(ids, at::kLong, {tokens, top}, dev);
     const float *pg = (const float *)dense(tensor(a[0]), at::kFloat, {tokens, top}, dev);
-    if (!pi || !pg) NOT_HERE;
+    bool renormalize;
+    if (!pi || !pg || !truth(a[4], renormalize)) NOT_HERE;
     at::Tensor out = new_tensor({tokens, experts}, z->scalar_type(), dev);
     const int status = route_backward_call(pg, rz.p, rz.ld, pi, code, tokens, experts, top, (int)score,
-                                           PyObject_IsTrue(a[4]), scale, out.data_ptr(), experts, queue(dev));
+                                           renormalize, scale, out.data_ptr(), experts, queue(dev));
     if (status != KM_OK) return failed(status, "layers_route_backward");
     return wrap(out);
     END_HANDLE_TH_ERRORS
@@ -255,7 +258,8 @@ PyObject *cross_entropy_backward(PyObject *, PyObject *const *a, Py_ssize_t coun
     const float *ps = (const float *)dense(tensor(a[4]), at::kFloat, {e.rows}, e.dev), *pd = nullptr;
     if (!pg || !ps) NOT_HERE;
     if (a[5] != Py_None && !(pd = (const float *)dense(tensor(a[5]), at::kFloat, {e.rows}, e.dev))) NOT_HERE;
-    const bool need_dx = PyObject_IsTrue(a[6]), need_dw = PyObject_IsTrue(a[7]);
+    bool need_dx, need_dw;
+    if (!truth(a[6], need_dx) || !truth(a[7], need_dw)) NOT_HERE;
     const size_t bytes = entropy_backward_bytes(e.rows, e.classes, e.width, e.code, e.misplaced());
     if (bytes == 0 || (!need_dx && !need_dw)) NOT_HERE;
     Scratch ws(bytes, e.dev);

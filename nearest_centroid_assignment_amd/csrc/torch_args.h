@@ -62,6 +62,14 @@ void *dense(const at::Tensor *t, at::ScalarType type, at::IntArrayRef shape, int
     return t->data_ptr();
 }
 
+// The truth of o; false where it has none (then Python says why).
+bool truth(PyObject *o, bool &v) {
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) PyErr_Clear();
+    v = t > 0;
+    return t >= 0;
+}
+
 at::Tensor new_tensor(at::IntArrayRef shape, at::ScalarType type, int dev) {
     return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, dev));
 }

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from nearest_centroid_assignment_amd import layers  # noqa: E402
+from nearest_centroid_assignment_amd import experts, layers  # noqa: E402
 from tests import gpu_util as gu  # noqa: E402
 from tests.test_gpu_experts import TYPES, close, randn  # noqa: E402
 from tests.test_gpu_layers import entropy_ref, route_ref  # noqa: E402
@@ -178,3 +178,20 @@ def test_refusals_allocate_nothing():
         with pytest.raises(layers.KMeansError):
             call()
     assert torch.cuda.max_memory_allocated() <= at + 4096 and torch.cuda.memory_reserved() == before
+
+
+def test_flags_that_are_no_truth_values():
+    """What Python itself raises for them, by the native way as by the other."""
+    x, ids = randn(1, 8, 16), torch.zeros(8, dtype=torch.int64, device="cuda")
+    f, flag = torch.ones(8, device="cuda"), torch.ones(2)
+    for call in (lambda: layers.layer_norm(x, save_stats=flag),
+                 lambda: layers.layer_norm_backward(x, x, None, f, f, need_dx=flag),
+                 lambda: layers.route(x, 2, renormalize=flag),
+                 lambda: layers.route_backward(f[:, None], x, ids[:, None], renormalize=flag),
+                 lambda: layers.cross_entropy_backward(f, x, x, ids, f, need_dw=flag)):
+        with pytest.raises(RuntimeError, match="Boolean value"):
+            call()
+    with pytest.raises(RuntimeError, match="Boolean value"):
+        experts.linear(x, x, save_pre=flag)
+    with pytest.raises(RuntimeError, match="Boolean value"):
+        experts.linear_backward(x[:, :8].contiguous(), x, randn(3, 8, 16), need_dx=flag)
